@@ -50,12 +50,13 @@ HBM_PEAK_GBPS = 8000.0
 # The sources that decide what the measured kernels move: every kernel, the
 # device walk, the host plan and workspace layout (chunk and block split,
 # store kinds, claims) and the public headers.  A committed profile summary
-# is used only while these hash to the value recorded in it.
+# is used only while these hash to the value recorded in it.  The layer
+# kernels (gclip_layer*) are compiled apart and none of this includes them.
 KERNEL_SOURCES = sorted([os.path.join("global_l2_norm_amd", "csrc", f)
                          for f in os.listdir(os.path.join(ROOT, "global_l2_norm_amd", "csrc"))
-                         if f.endswith((".hip", ".hpp", ".cpp"))] +
+                         if f.endswith((".hip", ".hpp", ".cpp")) and not f.startswith("gclip_layer")] +
                         [os.path.join("include", f) for f in os.listdir(os.path.join(ROOT, "include"))
-                         if f.endswith(".h")])
+                         if f.endswith(".h") and not f.startswith("gclip_layer")])
 PROFILES = os.path.join(ROOT, "profiles")
 # byte sizes of the workloads' lists: 120M fp16, 120M fp32, twice that, and 1.3B bf16
 REF_SIZES = [184_496_640, 368_993_280, 737_986_560, 2_622_365_696]

@@ -26,6 +26,10 @@ __all__ = ["GclipError", "GclipResult", "GradList", "clip_grad_norm_", "gclip_li
            "gclip_tensor_norms", "gclip_clip_per_tensor_", "gclip_set_gather_wait", "TENSOR_RESULT_DTYPE",
            "GCLIP_DEVICE_WAIT_TIMEOUT", "gclip_contrib_create",
            "gclip_contrib_destroy", "gclip_accumulate_norm", "gclip_accumulate_clip_", "Contribution",
+           "DropoutMask", "dropout", "dropout_forward", "dropout_backward", "layer_norm", "layer_norm_forward",
+           "layer_norm_backward", "residual_norm", "residual_norm_forward", "residual_norm_backward",
+           "gclip_layernorm_forward", "gclip_layernorm_backward", "gclip_residual_forward", "gclip_residual_backward",
+           "gclip_dropout_apply", "gclip_layer_workspace",
            "GCLIP_F32", "GCLIP_F16", "GCLIP_BF16", "GCLIP_PATH_AUTO", "GCLIP_PATH_FUSED", "GCLIP_PATH_SPLIT"]
 
 DTYPE_CODES = {"f32": GCLIP_F32, "f16": GCLIP_F16, "bf16": GCLIP_BF16}
@@ -500,3 +504,10 @@ def clip_grad_norm_(tensors, max_norm, avg_factor=1.0, error_if_nonfinite=False,
     if st != _lib.GCLIP_OK:
         raise GclipError(st, "clip_grad_norm_")
     return r["norm"]
+
+
+# the layers whose gradients the list clips (include/gclip_layer.h)
+from .layers import (DropoutMask, dropout, dropout_backward, dropout_forward, gclip_dropout_apply,  # noqa: E402
+                     gclip_layer_workspace, gclip_layernorm_backward, gclip_layernorm_forward,
+                     gclip_residual_backward, gclip_residual_forward, layer_norm, layer_norm_backward,
+                     layer_norm_forward, residual_norm, residual_norm_backward, residual_norm_forward)

@@ -1,4 +1,4 @@
-"""ctypes declarations of libgclip's C ABI (include/gclip.h).
+"""ctypes declarations of libgclip's C ABI (include/gclip.h, gclip_layer.h).
 
 Marshalling only: every step of the clipping path runs in the HIP kernels of
 libgclip.so.  Importing this module fails loudly when the library has not
@@ -65,6 +65,31 @@ class GclipAmpParams(ctypes.Structure):
                 ("growth_interval", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class GclipDropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("step", ctypes.c_uint32),
+                ("site", ctypes.c_uint32), ("d_step", ctypes.c_void_p)]
+
+
+class GclipLayerForward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_double), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldresidual", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("ldh", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p)]
+
+
+class GclipLayerBackward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("dresidual", ctypes.c_void_p),
+                ("lddresidual", ctypes.c_int64), ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64)]
+
+
 assert ctypes.sizeof(GclipResult) == 64
 assert ctypes.sizeof(GclipAmpState) == 16
 
@@ -102,6 +127,12 @@ def _declare(lib):
         "gclip_clip_noalloc_": ([ctypes.POINTER(vp), ctypes.POINTER(i64), i32, i32, dbl, dbl, i32, vp, vp], i32),
         "gclip_ref_read": ([vp, i64, vp, vp], i32),
         "gclip_ref_copy": ([vp, vp, i64, vp], i32),
+        "gclip_layernorm_forward": ([ctypes.POINTER(GclipLayerForward), vp], i32),
+        "gclip_layernorm_backward": ([ctypes.POINTER(GclipLayerBackward), vp], i32),
+        "gclip_residual_forward": ([ctypes.POINTER(GclipLayerForward), ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_residual_backward": ([ctypes.POINTER(GclipLayerBackward), ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_dropout_apply": ([vp, i64, vp, i64, i64, i64, i32, ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_layer_workspace": ([i64, i64], i64),
         "gclip_status_string": ([i32], ctypes.c_char_p),
         "gclip_last_hip_error": ([], i32),
         "gclip_version": ([], i32),
@@ -131,7 +162,7 @@ def load():
 
 lib = load()
 
-# The C ABI's declared entry points (include/gclip.h, include/gclip_ref.h), for the export check.
+# The C ABI's declared entry points (include/gclip.h, gclip_ref.h and gclip_layer.h), for the export check.
 EXPORTS = ("gclip_list_create", "gclip_list_destroy", "gclip_list_info", "gclip_list_set_path",
            "gclip_list_set_wait", "gclip_norm",
            "gclip_scale", "gclip_clip_", "gclip_result_read", "gclip_plan_query", "gclip_plan_trace", "gclip_status_string",
@@ -139,4 +170,5 @@ EXPORTS = ("gclip_list_create", "gclip_list_destroy", "gclip_list_info", "gclip_
            "gclip_norm_amp", "gclip_clip_amp_", "gclip_adamw_step_amp", "gclip_tensor_norms",
            "gclip_clip_per_tensor_", "gclip_contrib_create", "gclip_contrib_destroy", "gclip_accumulate_norm",
            "gclip_accumulate_clip_", "gclip_set_gather_wait", "gclip_clip_noalloc_", "gclip_ref_read",
-           "gclip_ref_copy")
+           "gclip_ref_copy", "gclip_layernorm_forward", "gclip_layernorm_backward", "gclip_residual_forward",
+           "gclip_residual_backward", "gclip_dropout_apply", "gclip_layer_workspace")

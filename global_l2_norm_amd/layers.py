@@ -1,0 +1,462 @@
+"""The memory-bound layers of a pre-norm training step (include/gclip_layer.h):
+layer norm, dropout from a counter-based generator, and the residual step
+that runs both in one pass, forward and backward.
+
+As in the rest of the package the functions named like the C ABI take its
+structures with raw device addresses, and the others torch tensors, which
+serve as device memory and streams: every step runs in the HIP kernels.
+
+- ``layer_norm_forward`` / ``_backward``, ``dropout_forward`` / ``_backward``
+  and ``residual_norm_forward`` / ``_backward`` are the passes themselves, for
+  a program that writes its own backward pass: the weights' gradients go into
+  buffers of the caller's, added to what the microbatches before left there
+  when ``accumulate`` is set, from where a ``GradList`` clips them.
+- ``layer_norm``, ``dropout`` and ``residual_norm`` are the same under
+  autograd.
+
+A matrix is a tensor whose last dimension is adjacent in memory and whose
+other dimensions lie at one distance (a contiguous tensor, a slice of the
+columns of a wider one, one row expanded).
+"""
+import ctypes
+
+from . import _check, _lib
+from ._lib import GCLIP_BF16, GCLIP_F16, GCLIP_F32, GclipDropout, GclipLayerBackward, GclipLayerForward
+
+_byref = ctypes.byref
+
+
+# ---------------------------------------------------------------- C ABI names
+def gclip_layernorm_forward(args, stream):
+    _check(_lib.lib.gclip_layernorm_forward(_byref(args), stream), "gclip_layernorm_forward")
+
+
+def gclip_layernorm_backward(args, stream):
+    _check(_lib.lib.gclip_layernorm_backward(_byref(args), stream), "gclip_layernorm_backward")
+
+
+def gclip_residual_forward(args, drop, stream):
+    _check(_lib.lib.gclip_residual_forward(_byref(args), _byref(drop) if drop is not None else None, stream),
+           "gclip_residual_forward")
+
+
+def gclip_residual_backward(args, drop, stream):
+    _check(_lib.lib.gclip_residual_backward(_byref(args), _byref(drop) if drop is not None else None, stream),
+           "gclip_residual_backward")
+
+
+def gclip_dropout_apply(x, ldx, y, ldy, rows, size, dtype, drop, stream):
+    _check(_lib.lib.gclip_dropout_apply(x, ldx, y, ldy, rows, size, dtype, _byref(drop), stream),
+           "gclip_dropout_apply")
+
+
+def gclip_layer_workspace(rows, size):
+    return _lib.lib.gclip_layer_workspace(rows, size)
+
+
+# ---------------------------------------------------------------- tensors as operands
+_codes = {}
+
+
+def _code(t, name):
+    if not _codes:
+        import torch
+        _codes.update({torch.float32: GCLIP_F32, torch.float16: GCLIP_F16, torch.bfloat16: GCLIP_BF16})
+    c = _codes.get(t.dtype)
+    if c is None:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    return c
+
+
+def _device(t, name):
+    """The tensor's device, which has to be the current one: kernels are
+    enqueued there."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    d = t.device
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {d}, the current device is {torch.cuda.current_device()}")
+    return d
+
+
+def _ld(t, name):
+    """Distance of a matrix's rows in elements."""
+    if t.is_contiguous():
+        return t.shape[-1]
+    shape, stride = t.shape, t.stride()
+    if t.numel() == 0:
+        return shape[-1]
+    lead = [(n, s) for n, s in zip(shape[:-1], stride[:-1]) if n != 1]
+    if (shape[-1] != 1 and stride[-1] != 1) or any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
+        raise ValueError(f"{name}: the last dimension must be adjacent in memory and the others at one distance")
+    return lead[-1][1] if lead else shape[-1]
+
+
+def _like(t, x, name):
+    """ld of a matrix of x's shape, dtype and device."""
+    if t.dtype != x.dtype:
+        raise TypeError(f"{name} must have dtype {x.dtype}, not {t.dtype}")
+    if t.shape != x.shape or t.device != x.device:
+        raise ValueError(f"{name} must have shape {tuple(x.shape)} on {x.device}")
+    return _ld(t, name)
+
+
+def _vector(t, n, dtypes, x, name):
+    """Address of a contiguous vector of n elements; None (no such operand) is 0."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+    if t.numel() != n or not t.is_contiguous() or t.device != x.device:
+        raise ValueError(f"{name} must hold {n} contiguous elements on {x.device}")
+    return t.data_ptr()
+
+
+def _extent(x, name):
+    """(rows, size) of a matrix."""
+    if x.dim() == 0:
+        raise ValueError(f"{name} must have at least one dimension")
+    size = x.shape[-1]
+    if size:
+        return x.numel() // size, size
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, 0
+
+
+def _f32():
+    import torch
+    return torch.float32
+
+
+class _On:
+    """The stream of a call: its raw handle, and new tensors and operands'
+    lifetimes on a stream that is not the current one."""
+
+    def __init__(self, stream, operands):
+        import torch
+        current = torch.cuda.current_stream()
+        self.raw = current.cuda_stream if stream is None else stream.cuda_stream
+        self.guard = None
+        if stream is not None and stream != current:
+            for t in operands:
+                if t is not None:
+                    t.record_stream(stream)
+            self.guard = torch.cuda.stream(stream)
+            self.guard.__enter__()
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def _weights_of(weight, bias, x, size):
+    wt = weight if weight is not None else bias
+    if wt is None:
+        return None, None, GCLIP_F32
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have one dtype")
+    allowed = (_f32(), x.dtype)
+    return _vector(weight, size, allowed, x, "weight"), _vector(bias, size, allowed, x, "bias"), _code(wt, "weight")
+
+
+# ---------------------------------------------------------------- dropout
+class DropoutMask:
+    """Which elements a dropout keeps, as a function of its arguments alone:
+    nothing is stored, and the backward pass takes the same object.
+
+    p        probability of dropping, to 16 bits (0 <= p <= 1)
+    seed     64 bits
+    step     32 bits: another mask every step ...
+    site     32 bits: ... and for every place of a step that drops
+    counter  optional device tensor whose first int32 is added to step: a
+             captured graph takes it anew at each replay (``counter.add_(1)``
+             between the replays, and not between a pass and its backward)
+    """
+
+    __slots__ = ("p", "seed", "step", "site", "counter", "args")
+
+    def __init__(self, p, seed, step=0, site=0, counter=None):
+        p = float(p)
+        if not 0.0 <= p <= 1.0:
+            raise ValueError(f"p must be in [0, 1], not {p}")
+        if not (0 <= seed < 1 << 64 and 0 <= step < 1 << 32 and 0 <= site < 1 << 32):
+            raise ValueError("seed takes 64 bits, step and site take 32")
+        address = None
+        if counter is not None:
+            import torch
+            if counter.dtype != torch.int32 or not counter.is_cuda or counter.numel() < 1:
+                raise ValueError("counter must be an int32 device tensor")
+            address = counter.data_ptr()
+        self.p, self.seed, self.step, self.site, self.counter = p, seed, step, site, counter
+        self.args = GclipDropout(p, seed, step, site, address)
+
+    def at(self, step=None, site=None):
+        """The mask of another step or site."""
+        return DropoutMask(self.p, self.seed, self.step if step is None else step,
+                           self.site if site is None else site, self.counter)
+
+    @property
+    def drops(self):
+        """Whether p is large enough to drop anything."""
+        return self.p >= 2.0 ** -17
+
+
+def dropout_forward(x, mask, out=None, stream=None):
+    """x where the mask keeps it, times 1 / (1 - p); else 0.  out may be x."""
+    import torch
+    _device(x, "x")
+    rows, size = _extent(x, "x")
+    with _On(stream, (x, out, mask.counter)) as raw:
+        if out is None:
+            out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        gclip_dropout_apply(x.data_ptr(), _ld(x, "x"), out.data_ptr(), _like(out, x, "out"), rows, size, _code(x, "x"),
+                            mask.args, raw)
+    return out
+
+
+def dropout_backward(dy, mask, out=None, stream=None):
+    """The gradient of ``dropout_forward``: the same map of dy."""
+    return dropout_forward(dy, mask, out, stream)
+
+
+# ---------------------------------------------------------------- layer norm and the residual step
+def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out=None, stats=True, stream=None):
+    """(y, mean, rstd) of the norm over the last dimension.  mean and rstd are
+    what the backward pass takes, and None without ``stats``."""
+    return _forward(x, None, weight, bias, eps, None, None, out, stats, stream)[1:]
+
+
+def residual_norm_forward(x, residual, weight=None, bias=None, eps=1e-5, mask=None, *, out_h=None, out=None,
+                          stats=True, stream=None):
+    """(h, y, mean, rstd) of h = residual + dropout(x), y = norm(h).  out_h
+    may be residual or x (in place)."""
+    return _forward(x, residual, weight, bias, eps, mask, out_h, out, stats, stream)
+
+
+def _forward(x, residual, weight, bias, eps, mask, h, y, stats, stream):
+    import torch
+    _device(x, "x")
+    rows, size = _extent(x, "x")
+    wp, bp, wdt = _weights_of(weight, bias, x, size)
+    ldr = _like(residual, x, "residual") if residual is not None else 0
+    with _On(stream, (x, residual, weight, bias, h, y, mask.counter if mask is not None else None)) as raw:
+        if y is None:
+            y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if residual is not None and h is None:
+            h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        mean = rstd = mp = rp = None
+        if stats:
+            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
+            mp, rp = mean.data_ptr(), rstd.data_ptr()
+        if residual is None:
+            gclip_layernorm_forward(GclipLayerForward(
+                rows, size, _code(x, "x"), wdt, eps, x.data_ptr(), _ld(x, "x"), None, 0, wp, bp, None, 0,
+                y.data_ptr(), _like(y, x, "out"), mp, rp), raw)
+        else:
+            gclip_residual_forward(GclipLayerForward(
+                rows, size, _code(x, "x"), wdt, eps, x.data_ptr(), _ld(x, "x"), residual.data_ptr(), ldr, wp, bp,
+                h.data_ptr(), _like(h, x, "out_h"), y.data_ptr(), _like(y, x, "out"), mp, rp),
+                mask.args if mask is not None and mask.drops else None, raw)
+    return h, y, mean, rstd
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, *, dweight=None, dbias=None, accumulate=False,
+                        weight_grad=None, bias_grad=None, out=None, stream=None):
+    """(dx, dweight, dbias) of the norm of x, from the mean and rstd that its
+    forward pass returned.
+
+    dweight, dbias  where the weights' gradients go (binary32 or x's dtype);
+                    by default new tensors of weight's dtype
+    accumulate      add to them instead (the microbatches' +=)
+    weight_grad, bias_grad  whether they are wanted; by default when weight is
+                    given, or a buffer for them
+    """
+    dx, _, dw, db = _backward(dy, None, x, mean, rstd, weight, None, False, dweight, dbias, accumulate, weight_grad,
+                              bias_grad, out, None, stream)
+    return dx, dw, db
+
+
+def residual_norm_backward(dy, dh, h, mean, rstd, weight=None, mask=None, *, dweight=None, dbias=None,
+                           accumulate=False, weight_grad=None, bias_grad=None, out=None, out_residual=None,
+                           stream=None):
+    """(dx, dresidual, dweight, dbias) of the residual step, from the h, mean
+    and rstd that its forward pass returned and the same mask.  dh is the
+    gradient of h from its other uses, or None.  Without dropout dx is
+    dresidual, the same tensor.  Otherwise as ``layer_norm_backward``."""
+    return _backward(dy, dh, h, mean, rstd, weight, mask if mask is not None and mask.drops else None, True, dweight,
+                     dbias, accumulate, weight_grad, bias_grad, out, out_residual, stream)
+
+
+def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, accumulate, weight_grad, bias_grad, dx,
+              dres, stream):
+    import torch
+    _device(x, "x")
+    rows, size = _extent(x, "x")
+    wp, _, wdt = _weights_of(weight, None, x, size)
+    want_w = dweight is not None or (weight is not None if weight_grad is None else weight_grad)
+    want_b = dbias is not None or (weight is not None if bias_grad is None else bias_grad)
+    if accumulate and ((want_w and dweight is None) or (want_b and dbias is None)):
+        raise ValueError("accumulate needs the buffers to add to: dweight and dbias")
+    f32 = torch.float32
+    allowed = (f32, x.dtype)
+    mp, rp = _vector(mean, rows, (f32,), x, "mean"), _vector(rstd, rows, (f32,), x, "rstd")
+    lddy, lddh = _like(dy, x, "dy"), _like(dh, x, "dh") if dh is not None else 0
+    if residual and mask is None:
+        if dx is not None and dres is not None and dx is not dres:
+            raise ValueError("without dropout dx is dresidual: give one buffer")
+        dres = dres if dres is not None else dx
+    operands = (dy, dh, x, mean, rstd, weight, dweight, dbias, dx, dres, mask.counter if mask is not None else None)
+    with _On(stream, operands) as raw:
+        gt = weight.dtype if weight is not None else f32
+        wants = [t for t in (dweight, dbias) if t is not None]
+        if wants:
+            gt = wants[0].dtype
+            if wants[-1].dtype != gt:
+                raise TypeError("dweight and dbias must have one dtype")
+        if want_w and dweight is None:
+            dweight = torch.empty(size, dtype=gt, device=x.device)
+        if want_b and dbias is None:
+            dbias = torch.empty(size, dtype=gt, device=x.device)
+        wsp, nbytes = None, 0
+        gdt = GCLIP_F32
+        if want_w or want_b:
+            nbytes = gclip_layer_workspace(rows, size)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+            wsp = workspace.data_ptr()
+            gdt = _code(dweight if dweight is not None else dbias, "dweight")
+        if residual:
+            if dres is None:
+                dres = torch.empty_like(x, memory_format=torch.contiguous_format)
+            if mask is not None and dx is None:
+                dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        elif dx is None:
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        second = not residual or mask is not None  # dx apart from dresidual
+        args = GclipLayerBackward(
+            rows, size, _code(x, "x"), wdt, gdt, 1 if accumulate else 0, dy.data_ptr(), lddy,
+            dh.data_ptr() if dh is not None else None, lddh, x.data_ptr(), _ld(x, "x"), mp, rp, wp,
+            dres.data_ptr() if residual else None, _like(dres, x, "out_residual") if residual else 0,
+            dx.data_ptr() if second else None, _like(dx, x, "out") if second else 0,
+            _vector(dweight, size, allowed, x, "dweight"), _vector(dbias, size, allowed, x, "dbias"), wsp, nbytes)
+        if residual:
+            gclip_residual_backward(args, mask.args if mask is not None else None, raw)
+        else:
+            gclip_layernorm_backward(args, raw)
+    return (dx if second else dres), dres, dweight, dbias
+
+
+# ---------------------------------------------------------------- under autograd
+_functions = {}
+
+
+def _matrix_of(t):
+    """A gradient from autograd in a form that the kernels take: an expanded
+    or permuted one is copied."""
+    try:
+        _ld(t, "gradient")
+        return t
+    except ValueError:
+        return t.contiguous()
+
+
+def _autograd():
+    """The autograd functions (torch is imported where it is used only)."""
+    if _functions:
+        return _functions
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Dropout(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, mask):
+            ctx.mask = mask
+            return dropout_forward(x, mask)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy):
+            return dropout_backward(_matrix_of(dy), ctx.mask), None
+
+    class LayerNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, weight, bias, eps):
+            y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
+            ctx.save_for_backward(x, mean, rstd, weight)
+            ctx.bias_dtype = bias.dtype if bias is not None else None
+            return y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy):
+            x, mean, rstd, weight = ctx.saved_tensors
+            dw, db = _grad_buffers(ctx, x, weight, 1)
+            dx, dw, db = layer_norm_backward(_matrix_of(dy), x, mean, rstd, weight, dweight=dw, dbias=db,
+                                             weight_grad=False, bias_grad=False)
+            return dx, dw, db, None
+
+    class ResidualNorm(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, residual, weight, bias, eps, mask):
+            h, y, mean, rstd = residual_norm_forward(x, residual, weight, bias, eps, mask)
+            ctx.save_for_backward(h, mean, rstd, weight)
+            ctx.bias_dtype = bias.dtype if bias is not None else None
+            ctx.mask = mask
+            ctx.set_materialize_grads(False)
+            return h, y
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dh, dy):
+            h, mean, rstd, weight = ctx.saved_tensors
+            mask = ctx.mask
+            dh = _matrix_of(dh) if dh is not None else None
+            if dy is None:  # y is not used: the residual sum alone
+                if dh is None:
+                    return (None,) * 6
+                return dropout_backward(dh, mask) if mask is not None else dh, dh, None, None, None, None
+            dw, db = _grad_buffers(ctx, h, weight, 2)
+            dx, dres, dw, db = residual_norm_backward(_matrix_of(dy), dh, h, mean, rstd, weight, mask, dweight=dw,
+                                                      dbias=db, weight_grad=False, bias_grad=False)
+            return dx, dres, dw, db, None, None
+
+    _functions.update(dropout=Dropout, layer_norm=LayerNorm, residual_norm=ResidualNorm)
+    return _functions
+
+
+def _grad_buffers(ctx, x, weight, at):
+    """New buffers for those weights' gradients that are asked for."""
+    import torch
+    new = lambda dtype: torch.empty(x.shape[-1], dtype=dtype, device=x.device)  # noqa: E731
+    return (new(weight.dtype) if ctx.needs_input_grad[at] else None,
+            new(ctx.bias_dtype) if ctx.needs_input_grad[at + 1] else None)
+
+
+def _tracked(*tensors):
+    import torch
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+def dropout(x, mask):
+    """Dropout of x by the mask (a ``DropoutMask``)."""
+    return _autograd()["dropout"].apply(x, mask) if _tracked(x) else dropout_forward(x, mask)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5):
+    """The norm of x over its last dimension."""
+    if not _tracked(x, weight, bias):
+        return layer_norm_forward(x, weight, bias, eps, stats=False)[0]
+    return _autograd()["layer_norm"].apply(x, weight, bias, eps)
+
+
+def residual_norm(x, residual, weight=None, bias=None, eps=1e-5, mask=None):
+    """(h, y): h = residual + dropout(x), y = the norm of h.  Without a mask
+    nothing is dropped (evaluation)."""
+    if not _tracked(x, residual, weight, bias):
+        return residual_norm_forward(x, residual, weight, bias, eps, mask, stats=False)[:2]
+    return _autograd()["residual_norm"].apply(x, residual, weight, bias, eps, mask)
