@@ -20,7 +20,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgclip.so")
 STAMPS_LIB = os.path.join(HERE, "_stamps", "libgclip.so")
 SOURCES = ["gclip_api.cpp", "gclip_plan.cpp", "gclip_trace.cpp", "gclip_kernels.hip", "gclip_tensor.hip",
-           "gclip_adamw.hip", "gclip_noalloc.hip", "gclip_ref.hip", "gclip_layer_api.cpp", "gclip_layer_any.hip"]
+           "gclip_adamw.hip", "gclip_noalloc.hip", "gclip_ref.hip", "gclip_layer_api.cpp", "gclip_layer_any.hip",
+           "gclip_layer_forward_f32.hip", "gclip_layer_forward_f16.hip", "gclip_layer_forward_bf16.hip",
+           "gclip_layer_backward_f32.hip", "gclip_layer_backward_f16.hip", "gclip_layer_backward_bf16.hip"]
 ARCH = os.environ.get("GCLIP_OFFLOAD_ARCH", "gfx950")
 
 

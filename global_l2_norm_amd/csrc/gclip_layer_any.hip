@@ -166,27 +166,6 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_cols_grad_any(BwdArgs a) {
   }
 }
 
-// The sum of the parts, part by part, into dweight and dbias.
-template <int DT>
-__global__ __launch_bounds__(kAnyThreads) void k_norm_weight_grad(BwdArgs a) {
-  const uint64_t i = (uint64_t)blockIdx.x * kAnyThreads + threadIdx.x;
-  if (i >= 2ull * a.size) return;
-  const uint64_t out = i < a.size ? a.dweight : a.dbias;
-  if (!out) return;
-  float t = 0.0f;
-  for (uint32_t p = 0; p < a.parts; ++p) t += a.partials[(uint64_t)p * 2 * a.size + i];
-  const uint64_t c = i < a.size ? i : i - a.size;
-  if (DT == GCLIP_F32 || a.gdt == GCLIP_F32) {
-    const uint64_t p = out + c * 4u;
-    if (a.accumulate) t += elem_float<GCLIP_F32>(load_elem<GCLIP_F32>(p));
-    store_elem<GCLIP_F32>(p, elem_bits<GCLIP_F32>(t));
-  } else {
-    const uint64_t p = out + c * 2u;
-    if (a.accumulate) t += elem_float<DT>(load_elem<DT>(p));
-    store_elem<DT>(p, elem_bits<DT>(t));
-  }
-}
-
 template <int DT>
 __global__ __launch_bounds__(kAnyThreads) void k_dropout_any(Rows x, Rows y, uint32_t rows, uint32_t size, DropArgs d) {
   const uint32_t groups = (size + kGroup - 1) / kGroup;
@@ -217,8 +196,8 @@ hipError_t backward_any(const BwdArgs& a, const DropArgs* drop, hipStream_t st) 
   const uint32_t groups = (a.size + kGroup - 1) / kGroup;
   if (a.dweight || a.dbias) {
     hipLaunchKernelGGL((k_norm_cols_grad_any<DT>), dim3((groups + 63) / 64, a.parts), block, 0, st, a);
-    const uint64_t n = 2ull * a.size;
-    hipLaunchKernelGGL((k_norm_weight_grad<DT>), dim3((uint32_t)((n + kAnyThreads - 1) / kAnyThreads)), block, 0, st, a);
+    const hipError_t e = join_weight_grads<DT>(a, st);
+    if (e != hipSuccess) return e;
   }
   if (a.rows > 0) {
     const dim3 grid(std::min<uint32_t>(a.rows, 1u << 20));
@@ -238,27 +217,40 @@ hipError_t dropout_any(const Rows& x, const Rows& y, uint32_t rows, uint32_t siz
 
 }  // namespace
 
-// As many parts as leave each at least 16 rows, at most 256, and at most
-// 64 MiB of them for long rows.
+// A part for each workgroup of the kernel with rows in registers.  Else as
+// many as leave each at least 16 rows, at most 256, and at most 64 MiB of
+// them for long rows.
 uint32_t layer_parts(int64_t rows, int64_t size) {
+  if (rows > 0 && in_registers((uint32_t)size)) {
+    const uint32_t at_once = kBwdThreads / kBwdShapes[row_shape_of(kBwdShapes, (uint32_t)size)].lanes;
+    return std::min<uint32_t>(((uint32_t)rows + at_once - 1) / at_once, kBwdParts);
+  }
   const int64_t by_rows = std::max<int64_t>(1, (rows + 15) / 16);
   const int64_t by_bytes = std::max<int64_t>(1, (64ll << 20) / (8 * size));
   return (uint32_t)std::min<int64_t>({by_rows, by_bytes, 256});
 }
 
 hipError_t launch_layer_forward(const FwdArgs& a, int32_t dtype, bool residual, const DropArgs* drop, hipStream_t st) {
+  const bool regs = in_registers(a.size);
   switch (dtype) {
-    case GCLIP_F32: return forward_any<GCLIP_F32>(a, residual, drop, st);
-    case GCLIP_F16: return forward_any<GCLIP_F16>(a, residual, drop, st);
-    default: return forward_any<GCLIP_BF16>(a, residual, drop, st);
+    case GCLIP_F32:
+      return regs ? forward_rows<GCLIP_F32>(a, residual, drop, st) : forward_any<GCLIP_F32>(a, residual, drop, st);
+    case GCLIP_F16:
+      return regs ? forward_rows<GCLIP_F16>(a, residual, drop, st) : forward_any<GCLIP_F16>(a, residual, drop, st);
+    default:
+      return regs ? forward_rows<GCLIP_BF16>(a, residual, drop, st) : forward_any<GCLIP_BF16>(a, residual, drop, st);
   }
 }
 
-hipError_t launch_layer_backward(const BwdArgs& a, int32_t dtype, const DropArgs* drop, hipStream_t st) {
+hipError_t launch_layer_backward(const BwdArgs& a, int32_t dtype, bool residual, const DropArgs* drop, hipStream_t st) {
+  const bool regs = a.rows > 0 && in_registers(a.size);
   switch (dtype) {
-    case GCLIP_F32: return backward_any<GCLIP_F32>(a, drop, st);
-    case GCLIP_F16: return backward_any<GCLIP_F16>(a, drop, st);
-    default: return backward_any<GCLIP_BF16>(a, drop, st);
+    case GCLIP_F32:
+      return regs ? backward_rows<GCLIP_F32>(a, residual, drop, st) : backward_any<GCLIP_F32>(a, drop, st);
+    case GCLIP_F16:
+      return regs ? backward_rows<GCLIP_F16>(a, residual, drop, st) : backward_any<GCLIP_F16>(a, drop, st);
+    default:
+      return regs ? backward_rows<GCLIP_BF16>(a, residual, drop, st) : backward_any<GCLIP_BF16>(a, drop, st);
   }
 }
 

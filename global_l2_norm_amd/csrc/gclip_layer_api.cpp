@@ -108,7 +108,8 @@ gclip_status forward(const gclip_layer_forward* a, bool residual, const gclip_dr
   if (!apart({x, r, h, y, w, b, m, s})) return GCLIP_EINVAL;
   if (a->rows == 0) return GCLIP_OK;
   const gclip::FwdArgs k{{x.at, x.ld}, {r.at, r.ld}, {h.at, h.ld}, {y.at, y.ld}, address(a->weight), address(a->bias),
-                         a->mean, a->rstd, (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, (float)a->eps};
+                         a->mean, a->rstd, (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, (float)a->eps,
+                         (float)(1.0 / std::sqrt((double)(float)a->eps))};
   return status_of(gclip::launch_layer_forward(k, a->dtype, residual, drops ? &d : nullptr,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -147,7 +148,7 @@ gclip_status backward(const gclip_layer_backward* a, bool residual, const gclip_
                          address(a->weight), address(a->dweight), address(a->dbias), static_cast<float*>(a->workspace),
                          (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, a->grad_dtype, a->accumulate ? 1 : 0,
                          gclip::layer_parts(a->rows, a->size)};
-  return status_of(gclip::launch_layer_backward(k, a->dtype, two ? &d : nullptr, static_cast<hipStream_t>(stream)));
+  return status_of(gclip::launch_layer_backward(k, a->dtype, residual, two ? &d : nullptr, static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

@@ -1,0 +1,227 @@
+// gclip_layer_backward.hpp -- the gradients of the norm and of the residual
+// step for rows that fit into registers, and the join of the weights'
+// gradients; instantiated for one storage format in each of
+// gclip_layer_backward_*.hip.
+#pragma once
+
+#include "gclip_layer_device.hpp"
+
+namespace gclip {
+
+// One pass: a row's dy and x are read once, into the registers of LANES
+// lanes, where the row's two sums and then dx are taken from them; the
+// columns' sums stay in registers over all rows of the workgroup, whose rows
+// meet in shared memory at the end.  While a row is worked on, the loads of
+// the workgroup's next one are under way.
+template <int DT, int LANES, int NV, bool RES, bool DROP>
+__global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
+  constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
+  constexpr uint32_t kCols = LANES * NV * kGroup;
+  constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
+  __shared__ float red[2][2][kBwdThreads / 64];
+  __shared__ float sums[kMeet > 1 ? kMeet * kCols : 1];
+  const uint32_t lane = threadIdx.x % LANES;
+  uint32_t slot = threadIdx.x / LANES;
+  if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
+  const uint32_t step = DROP ? drop_step(d) : 0u;
+
+  Raw8<DT> ny[NV], nx[NV], nh[NV];
+  float nmean, nrstd;
+  uint32_t base = blockIdx.x * kRows;
+  const auto fetch = [&](uint32_t first) {
+    // rows past the end are read as the last one; they count for nothing
+    const uint32_t r = min(first + slot, a.rows - 1);
+    const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld, dh = a.dh.at + r * a.dh.ld;
+    nmean = a.mean[r];
+    nrstd = a.rstd[r];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const uint32_t c = column_of(lane, LANES, k);
+      ny[k] = load_clamped<DT, true>(dy, c, a.size);
+      nx[k] = load_clamped<DT, true>(x, c, a.size);
+      if constexpr (RES) nh[k] = a.dh.at ? load_clamped<DT, true>(dh, c, a.size) : zero8<DT>();
+    }
+  };
+  fetch(base);
+  float w[NV][8], dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+  }
+  const float count = (float)a.size;
+  uint32_t turn = 0;
+
+  while (base < a.rows) {
+    const uint32_t r = base + slot;
+    const float mean = nmean, rstd = nrstd;
+    float g[NV][8], n[NV][8];
+    Raw8<DT> hh[NV];
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const uint32_t c = column_of(lane, LANES, k);
+      settle<DT>(ny[k], r < a.rows ? c : a.size, a.size);
+      settle<DT>(nx[k], c, a.size);
+      unpack<DT>(ny[k], g[k]);
+      unpack<DT>(nx[k], n[k]);
+      if constexpr (RES) {
+        settle<DT>(nh[k], c, a.size);
+        hh[k] = nh[k];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        n[k][j] = (n[k][j] - mean) * rstd;
+        dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
+        db[k][j] += g[k][j];
+        g[k][j] *= w[k][j];
+        s1 += g[k][j];
+        s2 = __builtin_fmaf(g[k][j], n[k][j], s2);
+      }
+    }
+    const uint32_t next = base + gridDim.x * kRows;
+    if (next < a.rows) fetch(next);
+    float c1, c2;
+    if constexpr (LANES > 64) {
+      // both sums behind one barrier; the next row's use the other words
+      const uint32_t wave = threadIdx.x >> 6, own = wave / (LANES / 64) * (LANES / 64);
+      s1 = lanes_sum<64>(s1);
+      s2 = lanes_sum<64>(s2);
+      if ((threadIdx.x & 63) == 0) {
+        red[turn][0][wave] = s1;
+        red[turn][1][wave] = s2;
+      }
+      __syncthreads();
+      c1 = red[turn][0][own];
+      c2 = red[turn][1][own];
+#pragma unroll
+      for (uint32_t i = 1; i < LANES / 64; ++i) {
+        c1 += red[turn][0][own + i];
+        c2 += red[turn][1][own + i];
+      }
+      turn ^= 1u;
+    } else {
+      c1 = lanes_sum<LANES>(s1);
+      c2 = lanes_sum<LANES>(s2);
+    }
+    c1 /= count;  // exact for constant gradients
+    c2 /= count;
+    if (r < a.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const uint32_t c = column_of(lane, LANES, k);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = rstd * (g[k][j] - c1 - n[k][j] * c2);
+        if constexpr (RES) {
+          float q[8];
+          unpack<DT>(hh[k], q);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] += q[j];
+        }
+        store_columns<DT>(a.dres.at + r * a.dres.ld, c, a.size, pack<DT>(v));
+        if constexpr (DROP) {
+          drop_group(d, step, r, c / kGroup, v);
+          store_columns<DT>(a.dx.at + r * a.dx.ld, c, a.size, pack<DT>(v));
+        }
+      }
+    }
+    base = next;
+  }
+
+  // this workgroup's part of the columns' sums: dweight, then dbias
+  if (!a.dweight && !a.dbias) return;
+#pragma unroll
+  for (uint32_t which = 0; which < 2; ++which) {
+    float(&v)[NV][8] = which ? db : dw;
+    if constexpr (kMeet > 1) {
+      const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = across_rows<LANES>(v[k][j]);
+          if (LANES >= 64 || threadIdx.x % 64 < LANES) sums[row * kCols + column_of(lane, LANES, k) + j] = t;
+        }
+      }
+      __syncthreads();
+      for (uint32_t c = threadIdx.x; c < a.size; c += kBwdThreads) {
+        float t = sums[c];
+#pragma unroll
+        for (uint32_t i = 1; i < kMeet; ++i) t += sums[i * kCols + c];
+        if (a.parts == 1) store_weight_grad<DT>(a, which, c, t);
+        else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t c = column_of(lane, LANES, k) + j;
+          if (c < a.size) {
+            if (a.parts == 1) store_weight_grad<DT>(a, which, c, v[k][j]);
+            else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = v[k][j];
+          }
+        }
+      }
+    }
+  }
+}
+
+// The sum of the parts: a workgroup takes 64 columns, its waves share the
+// parts, in a fixed order.
+constexpr uint32_t kJoinThreads = 1024;
+template <int DT>
+__global__ __launch_bounds__(kJoinThreads) void k_join_weight_grads(BwdArgs a) {
+  constexpr uint32_t kWavesOf = kJoinThreads / 64;
+  __shared__ float red[kWavesOf][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t i = (uint64_t)blockIdx.x * 64 + lane, width = 2ull * a.size;
+  float t = 0.0f;
+  if (i < width) {
+#pragma unroll 8
+    for (uint32_t p = wave; p < a.parts; p += kWavesOf) t += a.partials[p * width + i];
+  }
+  red[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && i < width) {
+#pragma unroll
+    for (uint32_t k = 1; k < kWavesOf; ++k) t += red[k][lane];
+    store_weight_grad<DT>(a, i >= a.size, (uint32_t)(i < a.size ? i : i - a.size), t);
+  }
+}
+
+template <int DT>
+hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((k_join_weight_grads<DT>), dim3((uint32_t)((2ull * a.size + 63) / 64)), dim3(kJoinThreads), 0, st,
+                     a);
+  return hipGetLastError();
+}
+
+template <int DT, int LANES, int NV>
+hipError_t backward_shape(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  const dim3 grid(a.parts), block(kBwdThreads);
+  if (!residual) hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, false, false>), grid, block, 0, st, a, DropArgs{});
+  else if (!drop) hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, false>), grid, block, 0, st, a, DropArgs{});
+  else hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, true>), grid, block, 0, st, a, *drop);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.parts == 1 || (!a.dweight && !a.dbias)) return e;
+  return join_weight_grads<DT>(a, st);
+}
+
+template <int DT, int I = 0>
+hipError_t backward_of(int shape, const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kBwdShapes) / sizeof(kBwdShapes[0]))) {
+    if (shape != I) return backward_of<DT, I + 1>(shape, a, residual, drop, st);
+  }
+  return backward_shape<DT, kBwdShapes[I].lanes, kBwdShapes[I].groups>(a, residual, drop, st);
+}
+
+template <int DT>
+hipError_t backward_rows(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  return backward_of<DT>(row_shape_of(kBwdShapes, a.size), a, residual, drop, st);
+}
+
+}  // namespace gclip

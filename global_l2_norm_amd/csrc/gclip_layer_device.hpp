@@ -119,50 +119,53 @@ __device__ __forceinline__ void store8(uint64_t a, const Raw8<DT>& r) {
   }
 }
 
+// The elements of r moved down by n (1 to 7) places, zeros after them.
+template <int DT>
+__device__ __forceinline__ Raw8<DT> shifted_down(const Raw8<DT>& s, uint32_t n) {
+  Raw8<DT> r;
+  if constexpr (DT == GCLIP_F32) {
+    uint32_t v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = s.q[k >> 2][k & 3];
+#pragma unroll
+    for (uint32_t b = 4; b > 0; b >>= 1) {
+      if (n & b) {
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) v[k] = k + b < 8 ? v[k + b < 8 ? k + b : 0] : 0u;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
+  } else {
+    uint64_t lo = (uint64_t)s.q[0][0] | ((uint64_t)s.q[0][1] << 32);
+    uint64_t hi = (uint64_t)s.q[0][2] | ((uint64_t)s.q[0][3] << 32);
+    const uint32_t sh = 16u * n;  // 16 to 112 bits
+    if (sh >= 64) {
+      lo = hi >> (sh - 64);
+      hi = 0;
+    } else {
+      lo = (lo >> sh) | (hi << (64 - sh));
+      hi >>= sh;
+    }
+    r.q[0] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+  }
+  return r;
+}
+
 // The n (1 to 7) elements at a, zeros after them.  Elements in front of a
 // belong to the same row when front is set: then one vector ending at the
-// row's end is read and shifted, which keeps the tail's load in step with the
-// others; a row of fewer than eight elements is read one by one.
+// row's end is read and shifted; a row of fewer than eight elements is read
+// one by one.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load_tail(uint64_t a, uint32_t n, bool front) {
+  if (front) return shifted_down<DT>(load8<DT, false>(a - (uint64_t)(kGroup - n) * kElem<DT>), kGroup - n);
   Raw8<DT> r = zero8<DT>();
-  if (front) {
-    const Raw8<DT> s = load8<DT, false>(a - (uint64_t)(kGroup - n) * kElem<DT>);
-    if constexpr (DT == GCLIP_F32) {
-      uint32_t v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = s.q[k >> 2][k & 3];
-      const uint32_t sh = kGroup - n;
-#pragma unroll
-      for (uint32_t b = 4; b > 0; b >>= 1) {
-        if (sh & b) {
-#pragma unroll
-          for (uint32_t k = 0; k < 8; ++k) v[k] = k + b < 8 ? v[k + b < 8 ? k + b : 0] : 0u;
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
-    } else {
-      uint64_t lo = (uint64_t)s.q[0][0] | ((uint64_t)s.q[0][1] << 32);
-      uint64_t hi = (uint64_t)s.q[0][2] | ((uint64_t)s.q[0][3] << 32);
-      const uint32_t sh = 16u * (kGroup - n);  // 16 to 112 bits
-      if (sh >= 64) {
-        lo = hi >> (sh - 64);
-        hi = 0;
-      } else {
-        lo = (lo >> sh) | (hi << (64 - sh));
-        hi >>= sh;
-      }
-      r.q[0] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
-    }
-  } else {
-#pragma unroll
-    for (uint32_t k = 0; k < 7; ++k) {
-      if (k < n) {
-        const uint32_t e = load_elem<DT>(a + (uint64_t)k * kElem<DT>);
-        if constexpr (DT == GCLIP_F32) r.q[k >> 2][k & 3] = e;
-        else r.q[0][k >> 1] |= e << (16 * (k & 1));
-      }
+  for (uint32_t k = 0; k < 7; ++k) {
+    if (k < n) {
+      const uint32_t e = load_elem<DT>(a + (uint64_t)k * kElem<DT>);
+      if constexpr (DT == GCLIP_F32) r.q[k >> 2][k & 3] = e;
+      else r.q[0][k >> 1] |= e << (16 * (k & 1));
     }
   }
   return r;
@@ -259,6 +262,127 @@ __device__ __forceinline__ void drop_group(const DropArgs& d, uint32_t step, uin
   for (int k = 0; k < 8; ++k) {
     const uint32_t u = k & 1 ? b.w[k >> 1] >> 16 : b.w[k >> 1] & 0xffffu;
     v[k] = u >= d.threshold ? v[k] * d.scale : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------- rows in registers
+// A row of 8 to LANES * NV * 8 columns is held by LANES lanes, NV groups
+// each: lane l takes the groups l, l + LANES, ...  Loads are unconditional --
+// a lane whose group passes the row's end reads the row's last eight elements
+// instead -- and settled afterwards: shifted where the group is the row's
+// ragged end, zero past it.  So a row's loads are all under way before
+// anything is waited for, and none leaves the row.
+__device__ __forceinline__ uint32_t column_of(uint32_t lane, uint32_t lanes, int k) {
+  return (lane + (uint32_t)k * lanes) * kGroup;
+}
+
+template <int DT, bool NT>
+__device__ __forceinline__ Raw8<DT> load_clamped(uint64_t row, uint32_t c, uint32_t size) {
+  const uint32_t o = c + kGroup <= size ? c : size - kGroup;
+  return load8<DT, NT>(row + o * kElem<DT>);
+}
+
+template <int DT>
+__device__ __forceinline__ void settle(Raw8<DT>& r, uint32_t c, uint32_t size) {
+  if (c + kGroup > size) r = c < size ? shifted_down<DT>(r, c + kGroup - size) : zero8<DT>();
+}
+
+template <int DT>
+__device__ __forceinline__ void store_columns(uint64_t row, uint32_t c, uint32_t size, const Raw8<DT>& r) {
+  if (c + kGroup <= size) store8<DT, false>(row + c * kElem<DT>, r);
+  else if (c < size) store_tail<DT>(row + c * kElem<DT>, r, size - c);
+}
+
+// Eight elements of weight or bias, as settle() leaves a row's.
+template <int DT>
+__device__ __forceinline__ void weight_columns(uint64_t w, int wdt, uint32_t c, uint32_t size, float def,
+                                               float (&v)[8]) {
+  if (w == 0) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = def;
+  } else if (DT == GCLIP_F32 || wdt == GCLIP_F32) {
+    Raw8<GCLIP_F32> r = load_clamped<GCLIP_F32, false>(w, c, size);
+    settle<GCLIP_F32>(r, c, size);
+    unpack<GCLIP_F32>(r, v);
+  } else {
+    Raw8<DT> r = load_clamped<DT, false>(w, c, size);
+    settle<DT>(r, c, size);
+    unpack<DT>(r, v);
+  }
+}
+
+// Sum over each aligned run of N lanes of a wave, the same bits in all of
+// them (a + b == b + a at every level), by register permutations alone:
+// quads, mirrored halves and rows of sixteen, then swaps between the rows.
+template <int CTRL>
+__device__ __forceinline__ float permuted(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (N >= 2) v += permuted<0xB1>(v);   // quad_perm 1,0,3,2
+  if constexpr (N >= 4) v += permuted<0x4E>(v);   // quad_perm 2,3,0,1
+  if constexpr (N >= 8) v += permuted<0x141>(v);  // row_half_mirror
+  if constexpr (N >= 16) v += permuted<0x140>(v); // row_mirror
+  if constexpr (N >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (N >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
+}
+
+// Sum over the LANES lanes of a row, the same bits in all of them.  Rows of
+// more than a wave meet in `red`, a word for each wave of the workgroup; one
+// barrier, so two sums in a row need two `red`s, and the third may use the
+// first again.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = lanes_sum<(LANES < 64 ? LANES : 64)>(v);
+  if constexpr (LANES > 64) {
+    constexpr int kWavesOfRow = LANES / 64;
+    const uint32_t wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = v;
+    __syncthreads();
+    const float* own = red + wave / kWavesOfRow * kWavesOfRow;
+    v = own[0];
+#pragma unroll
+    for (int i = 1; i < kWavesOfRow; ++i) v += own[i];
+  }
+  return v;
+}
+
+// Sum over the lanes of a wave that hold the same column of its 64 / LANES rows.
+template <int LANES>
+__device__ __forceinline__ float across_rows(float v) {
+  if constexpr (LANES <= 8) v += permuted<0x128>(v);  // row_ror 8
+  if constexpr (LANES <= 16) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  if constexpr (LANES <= 32) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  }
+  return v;
+}
+
+// A column's gradient into dweight (which 0) or dbias (1), unless unwanted.
+template <int DT>
+__device__ __forceinline__ void store_weight_grad(const BwdArgs& a, uint32_t which, uint32_t c, float t) {
+  const uint64_t out = which ? a.dbias : a.dweight;
+  if (!out) return;
+  if (DT == GCLIP_F32 || a.gdt == GCLIP_F32) {
+    const uint64_t p = out + c * 4ull;
+    if (a.accumulate) t += elem_float<GCLIP_F32>(load_elem<GCLIP_F32>(p));
+    store_elem<GCLIP_F32>(p, elem_bits<GCLIP_F32>(t));
+  } else {
+    const uint64_t p = out + c * 2ull;
+    if (a.accumulate) t += elem_float<DT>(load_elem<DT>(p));
+    store_elem<DT>(p, elem_bits<DT>(t));
   }
 }
 

@@ -1,0 +1,168 @@
+// gclip_layer_forward.hpp -- the norm and the residual step for rows that
+// fit into registers; instantiated for one storage format in each of
+// gclip_layer_forward_*.hip.
+#pragma once
+
+#include "gclip_layer_device.hpp"
+
+namespace gclip {
+
+template <int LANES>
+constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
+
+#ifndef GCLIP_FWD_WGS
+#define GCLIP_FWD_WGS 8
+#endif
+
+// One pass: a row's elements are read once, into the registers of LANES
+// lanes, where its mean, its squared deviations from it and y are taken from
+// them in turn.  While a row is worked on, the loads of the workgroup's next
+// one are under way; weight and bias stay in registers.
+template <int DT, int LANES, int NV, bool RES, bool DROP>
+__global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
+  constexpr int kThreads = kFwdThreads<LANES>;
+  constexpr uint32_t kRows = kThreads / LANES;  // of a workgroup at a time
+  __shared__ float red[2][kThreads / 64];
+  const uint32_t lane = threadIdx.x % LANES;
+  uint32_t slot = threadIdx.x / LANES;
+  if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
+  const uint32_t step = DROP ? drop_step(d) : 0u;
+
+  Raw8<DT> nx[NV], nr[NV];
+  uint32_t base = blockIdx.x * kRows;
+  const auto fetch = [&](uint32_t first) {
+    // rows past the end are read as the last one, and not written
+    const uint32_t r = min(first + slot, a.rows - 1);
+    const uint64_t x = a.x.at + r * a.x.ld, q = a.residual.at + r * a.residual.ld;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      nx[k] = load_clamped<DT, true>(x, column_of(lane, LANES, k), a.size);
+      if constexpr (RES) nr[k] = load_clamped<DT, true>(q, column_of(lane, LANES, k), a.size);
+    }
+  };
+  fetch(base);
+  float w[NV][8], b[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+    weight_columns<DT>(a.bias, a.wdt, column_of(lane, LANES, k), a.size, 0.0f, b[k]);
+  }
+  const float count = (float)a.size;
+
+  while (base < a.rows) {
+    const uint32_t r = base + slot;
+    float v[NV][8];
+    Raw8<DT> o[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const uint32_t c = column_of(lane, LANES, k);
+      settle<DT>(nx[k], c, a.size);
+      unpack<DT>(nx[k], v[k]);
+      if constexpr (RES) {
+        float q[8];
+        settle<DT>(nr[k], c, a.size);
+        unpack<DT>(nr[k], q);
+        if constexpr (DROP) drop_group(d, step, r, c / kGroup, v[k]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] += q[j];
+        o[k] = pack<DT>(v[k]);
+        unpack<DT>(o[k], v[k]);
+      }
+    }
+    const uint32_t next = base + gridDim.x * kRows;
+    if (next < a.rows) fetch(next);
+    if constexpr (RES) {
+      if (r < a.rows) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          store_columns<DT>(a.h.at + r * a.h.ld, column_of(lane, LANES, k), a.size, o[k]);
+      }
+    }
+
+    // the mean, then the squares of what is left of it; rows whose sums leave
+    // binary32 go through this again, scaled by a power of two (so does a row
+    // with a NaN or an infinity, to no effect)
+    float scale = 1.0f, mean, var;
+    for (;;) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[k][j], scale, s);
+      mean = row_sum<LANES>(s, red[0]) / count;  // exact for a constant row
+      s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const uint32_t c = column_of(lane, LANES, k);
+        if (c + kGroup <= a.size) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = __builtin_fmaf(v[k][j], scale, -mean);
+            s = __builtin_fmaf(t, t, s);
+          }
+        } else {
+          uint32_t left = c < a.size ? a.size - c : 0u;
+          // recomputed for each row: the eight conditions would else be kept
+          // in scalar registers over the loop, more than there are
+          asm volatile("" : "+v"(left));
+#pragma unroll
+          for (uint32_t j = 0; j < 8; ++j) {
+            const float t = j < left ? __builtin_fmaf(v[k][j], scale, -mean) : 0.0f;
+            s = __builtin_fmaf(t, t, s);
+          }
+        }
+      }
+      var = row_sum<LANES>(s, red[1]) / count;
+      const bool over = !(var <= 0x1.fffffep+127f) && scale == 1.0f;
+      if (!(LANES > 64 ? over : __any(over))) break;
+      if (over) scale = 0x1p-96f;
+    }
+    float rstd = scale / sqrtf(var + a.eps * scale * scale);
+    if (scale != 1.0f) {
+      mean *= 0x1p+96f;
+      rstd = rstd > a.rstd_max ? a.rstd_max : rstd;  // a constant row
+    }
+
+    if (r < a.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[k][j] = __builtin_fmaf((v[k][j] - mean) * rstd, w[k][j], b[k][j]);
+        store_columns<DT>(a.y.at + r * a.y.ld, column_of(lane, LANES, k), a.size, pack<DT>(v[k]));
+      }
+      if (a.mean && lane == 0) {
+        a.mean[r] = mean;
+        a.rstd[r] = rstd;
+      }
+    }
+    base = next;
+  }
+}
+
+template <int DT, int LANES, int NV>
+hipError_t forward_shape(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  constexpr int kThreads = kFwdThreads<LANES>;
+  constexpr uint32_t kRows = kThreads / LANES;
+  const uint32_t most = 256u * GCLIP_FWD_WGS * 256 / kThreads;
+  const uint32_t need = (a.rows + kRows - 1) / kRows;
+  const dim3 grid(need < most ? need : most), block(kThreads);
+  if (!residual) hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, false, false>), grid, block, 0, st, a, DropArgs{});
+  else if (!drop) hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, false>), grid, block, 0, st, a, DropArgs{});
+  else hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, true>), grid, block, 0, st, a, *drop);
+  return hipGetLastError();
+}
+
+template <int DT, int I = 0>
+hipError_t forward_of(int shape, const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kFwdShapes) / sizeof(kFwdShapes[0]))) {
+    if (shape != I) return forward_of<DT, I + 1>(shape, a, residual, drop, st);
+  }
+  return forward_shape<DT, kFwdShapes[I].lanes, kFwdShapes[I].groups>(a, residual, drop, st);
+}
+
+template <int DT>
+hipError_t forward_rows(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  return forward_of<DT>(row_shape_of(kFwdShapes, a.size), a, residual, drop, st);
+}
+
+}  // namespace gclip

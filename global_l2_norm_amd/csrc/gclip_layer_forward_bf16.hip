@@ -1,0 +1,6 @@
+// gclip_layer_forward_bf16.hip -- the forward kernels of gclip_layer_forward.hpp for one storage format.
+#include "gclip_layer_forward.hpp"
+
+namespace gclip {
+template hipError_t forward_rows<GCLIP_BF16>(const FwdArgs&, bool, const DropArgs*, hipStream_t);
+}  // namespace gclip
