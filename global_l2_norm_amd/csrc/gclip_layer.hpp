@@ -30,6 +30,7 @@ struct FwdArgs {
   uint32_t rows, size;
   int32_t wdt;
   float eps, rstd_max;  // rstd_max: 1 / sqrt(eps)
+  int32_t streamed;     // see kStreamBytes
 };
 
 struct BwdArgs {
@@ -40,6 +41,7 @@ struct BwdArgs {
   uint32_t rows, size;
   int32_t wdt, gdt, accumulate;
   uint32_t parts;
+  int32_t streamed;  // see kStreamBytes
 };
 
 // The norms' kernels hold a row of kRegistersMin to kRegistersMax columns in
@@ -50,14 +52,17 @@ constexpr uint32_t kRegistersMin = 8, kRegistersMax = 16384;
 struct RowShape {
   uint32_t lanes, groups;
 };
-#ifndef GCLIP_FWD_SHAPES
-#define GCLIP_FWD_SHAPES {8, 1}, {16, 1}, {32, 1}, {64, 1}, {32, 3}, {64, 2}, {64, 3}, {64, 4}, {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}
+constexpr RowShape kFwdShapes[] = {{8, 1},  {16, 1}, {32, 1},  {64, 1},  {32, 3},  {64, 2}, {64, 3},
+                                   {64, 4}, {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
+constexpr RowShape kBwdShapes[] = {{8, 1},   {16, 1},  {32, 1},  {64, 1},  {64, 2},
+                                   {128, 2}, {256, 2}, {512, 2}, {512, 3}, {512, 4}};
+// Few rows: more lanes each.
+#ifndef GCLIP_FEW_ROWS
+#define GCLIP_FEW_ROWS 512
 #endif
-#ifndef GCLIP_BWD_SHAPES
-#define GCLIP_BWD_SHAPES {8, 1}, {16, 1}, {32, 1}, {64, 1}, {32, 3}, {64, 2}, {64, 3}, {128, 2}, {256, 2}, {256, 3}, {512, 2}, {512, 3}, {512, 4}
-#endif
-constexpr RowShape kFwdShapes[] = {GCLIP_FWD_SHAPES};
-constexpr RowShape kBwdShapes[] = {GCLIP_BWD_SHAPES};
+constexpr uint32_t kFewRows = GCLIP_FEW_ROWS;
+constexpr RowShape kFewShapes[] = {{8, 1},   {16, 1},  {32, 1},   {64, 1},  {128, 1},
+                                   {256, 1}, {512, 1}, {1024, 1}, {1024, 2}};
 template <int N>
 constexpr int row_shape_of(const RowShape (&shapes)[N], uint32_t size) {
   int i = 0;
@@ -69,10 +74,16 @@ inline bool in_registers(uint32_t size) { return size >= kRegistersMin && size <
 // Threads of a workgroup of the backward kernel, and the most workgroups,
 // each of which leaves one partial sum of the weights' gradients.
 constexpr uint32_t kBwdThreads = 512;
-#ifndef GCLIP_BWD_WGS
-#define GCLIP_BWD_WGS 1
+constexpr uint32_t kBwdParts = 256;
+
+// What a call moves decides how.  Up to kStreamBytes the matrices may lie in
+// the 256 MB cache before memory, where the kernel before has left them:
+// ordinary loads find them there, and nontemporal stores leave them there.
+// Above, nontemporal loads and ordinary stores are faster.
+#ifndef GCLIP_STREAM_MB
+#define GCLIP_STREAM_MB 144
 #endif
-constexpr uint32_t kBwdParts = 256 * GCLIP_BWD_WGS;
+constexpr uint64_t kStreamBytes = (uint64_t)GCLIP_STREAM_MB << 20;
 
 // Partial sums of the weights' gradients for a matrix of this shape.
 uint32_t layer_parts(int64_t rows, int64_t size);

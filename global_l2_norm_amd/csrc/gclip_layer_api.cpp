@@ -85,6 +85,11 @@ bool dropout_args(const gclip_dropout* d, DropArgs* out, bool* any) {
   return true;
 }
 
+// Whether a call that reads and writes `matrices` of this shape streams them.
+int32_t streamed(int64_t rows, int64_t size, uint64_t es, uint64_t matrices) {
+  return (__uint128_t)(uint64_t)rows * (uint64_t)size * es * matrices > gclip::kStreamBytes ? 1 : 0;
+}
+
 gclip_status status_of(hipError_t e) { return e == hipSuccess ? GCLIP_OK : gclip::hip_fail(e); }
 
 gclip_status forward(const gclip_layer_forward* a, bool residual, const gclip_dropout* drop, void* stream) {
@@ -109,7 +114,7 @@ gclip_status forward(const gclip_layer_forward* a, bool residual, const gclip_dr
   if (a->rows == 0) return GCLIP_OK;
   const gclip::FwdArgs k{{x.at, x.ld}, {r.at, r.ld}, {h.at, h.ld}, {y.at, y.ld}, address(a->weight), address(a->bias),
                          a->mean, a->rstd, (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, (float)a->eps,
-                         (float)(1.0 / std::sqrt((double)(float)a->eps))};
+                         (float)(1.0 / std::sqrt((double)(float)a->eps)), streamed(a->rows, a->size, es, residual ? 4 : 2)};
   return status_of(gclip::launch_layer_forward(k, a->dtype, residual, drops ? &d : nullptr,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -147,7 +152,8 @@ gclip_status backward(const gclip_layer_backward* a, bool residual, const gclip_
   const gclip::BwdArgs k{{dy.at, dy.ld}, {dh.at, dh.ld}, {x.at, x.ld}, {out.at, out.ld}, {dx.at, dx.ld}, a->mean, a->rstd,
                          address(a->weight), address(a->dweight), address(a->dbias), static_cast<float*>(a->workspace),
                          (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, a->grad_dtype, a->accumulate ? 1 : 0,
-                         gclip::layer_parts(a->rows, a->size)};
+                         gclip::layer_parts(a->rows, a->size),
+                         streamed(a->rows, a->size, es, 3 + (a->dh ? 1 : 0) + (two ? 1 : 0))};
   return status_of(gclip::launch_layer_backward(k, a->dtype, residual, two ? &d : nullptr, static_cast<hipStream_t>(stream)));
 }
 

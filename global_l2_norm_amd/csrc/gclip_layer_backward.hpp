@@ -13,7 +13,7 @@ namespace gclip {
 // columns' sums stay in registers over all rows of the workgroup, whose rows
 // meet in shared memory at the end.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
-template <int DT, int LANES, int NV, bool RES, bool DROP>
+template <int DT, int LANES, int NV, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
   constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
   constexpr uint32_t kCols = LANES * NV * kGroup;
@@ -37,16 +37,19 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const uint32_t c = column_of(lane, LANES, k);
-      ny[k] = load_clamped<DT, true>(dy, c, a.size);
-      nx[k] = load_clamped<DT, true>(x, c, a.size);
-      if constexpr (RES) nh[k] = a.dh.at ? load_clamped<DT, true>(dh, c, a.size) : zero8<DT>();
+      ny[k] = load_clamped<DT, STREAMED>(dy, c, a.size);
+      nx[k] = load_clamped<DT, STREAMED>(x, c, a.size);
+      if constexpr (RES) nh[k] = a.dh.at ? load_clamped<DT, STREAMED>(dh, c, a.size) : zero8<DT>();
     }
   };
   fetch(base);
-  float w[NV][8], dw[NV][8], db[NV][8];
+  // four groups' weights would not fit beside the sums: they are read again
+  // for each row, from the caches
+  constexpr bool kKeep = NV < 4;
+  float w[kKeep ? NV : 1][8], dw[NV][8], db[NV][8];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+    if constexpr (kKeep) weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
   }
@@ -64,6 +67,13 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
       const uint32_t c = column_of(lane, LANES, k);
       settle<DT>(ny[k], r < a.rows ? c : a.size, a.size);
       settle<DT>(nx[k], c, a.size);
+      float wk[8];
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wk[j] = w[k][j];
+      } else {
+        weight_columns<DT>(a.weight, a.wdt, c, a.size, 1.0f, wk);
+      }
       unpack<DT>(ny[k], g[k]);
       unpack<DT>(nx[k], n[k]);
       if constexpr (RES) {
@@ -75,7 +85,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
         n[k][j] = (n[k][j] - mean) * rstd;
         dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
         db[k][j] += g[k][j];
-        g[k][j] *= w[k][j];
+        g[k][j] *= wk[j];
         s1 += g[k][j];
         s2 = __builtin_fmaf(g[k][j], n[k][j], s2);
       }
@@ -120,10 +130,10 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
 #pragma unroll
           for (int j = 0; j < 8; ++j) v[j] += q[j];
         }
-        store_columns<DT>(a.dres.at + r * a.dres.ld, c, a.size, pack<DT>(v));
+        store_columns<DT, kNtStore<DT, STREAMED>>(a.dres.at + r * a.dres.ld, c, a.size, pack<DT>(v));
         if constexpr (DROP) {
           drop_group(d, step, r, c / kGroup, v);
-          store_columns<DT>(a.dx.at + r * a.dx.ld, c, a.size, pack<DT>(v));
+          store_columns<DT, kNtStore<DT, STREAMED>>(a.dx.at + r * a.dx.ld, c, a.size, pack<DT>(v));
         }
       }
     }
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_weight_grads(BwdArgs a) {
   const uint64_t i = (uint64_t)blockIdx.x * 64 + lane, width = 2ull * a.size;
   float t = 0.0f;
   if (i < width) {
-#pragma unroll 8
+#pragma unroll 16
     for (uint32_t p = wave; p < a.parts; p += kWavesOf) t += a.partials[p * width + i];
   }
   red[wave][lane] = t;
@@ -200,12 +210,15 @@ hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int DT, int LANES, int NV>
+template <int DT, int LANES, int NV, bool STREAMED>
 hipError_t backward_shape(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   const dim3 grid(a.parts), block(kBwdThreads);
-  if (!residual) hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, false, false>), grid, block, 0, st, a, DropArgs{});
-  else if (!drop) hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, false>), grid, block, 0, st, a, DropArgs{});
-  else hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, true>), grid, block, 0, st, a, *drop);
+  if (!residual)
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+  else if (!drop)
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+  else
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, true, STREAMED>), grid, block, 0, st, a, *drop);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.parts == 1 || (!a.dweight && !a.dbias)) return e;
   return join_weight_grads<DT>(a, st);
@@ -216,7 +229,9 @@ hipError_t backward_of(int shape, const BwdArgs& a, bool residual, const DropArg
   if constexpr (I + 1 < (int)(sizeof(kBwdShapes) / sizeof(kBwdShapes[0]))) {
     if (shape != I) return backward_of<DT, I + 1>(shape, a, residual, drop, st);
   }
-  return backward_shape<DT, kBwdShapes[I].lanes, kBwdShapes[I].groups>(a, residual, drop, st);
+  constexpr RowShape s = kBwdShapes[I];
+  return a.streamed ? backward_shape<DT, s.lanes, s.groups, true>(a, residual, drop, st)
+                    : backward_shape<DT, s.lanes, s.groups, false>(a, residual, drop, st);
 }
 
 template <int DT>

@@ -287,11 +287,18 @@ __device__ __forceinline__ void settle(Raw8<DT>& r, uint32_t c, uint32_t size) {
   if (c + kGroup > size) r = c < size ? shifted_down<DT>(r, c + kGroup - size) : zero8<DT>();
 }
 
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void store_columns(uint64_t row, uint32_t c, uint32_t size, const Raw8<DT>& r) {
-  if (c + kGroup <= size) store8<DT, false>(row + c * kElem<DT>, r);
+  if (c + kGroup <= size) store8<DT, NT>(row + c * kElem<DT>, r);
   else if (c < size) store_tail<DT>(row + c * kElem<DT>, r, size - c);
 }
+
+// A streamed call's loads are nontemporal and its stores ordinary; another's
+// the other way round (but for binary32 rows, which are stored in two
+// instructions that interleave, whose halves of a line have to meet in a
+// cache).  See kStreamBytes.
+template <int DT, bool STREAMED>
+constexpr bool kNtStore = !STREAMED && DT != GCLIP_F32;
 
 // Eight elements of weight or bias, as settle() leaves a row's.
 template <int DT>

@@ -7,21 +7,26 @@
 
 namespace gclip {
 
+// The most threads of a workgroup: four waves, of which rows of up to a wave
+// share one; workgroups of a wave each where the rows are few.
 template <int LANES>
 constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
 
 #ifndef GCLIP_FWD_WGS
-#define GCLIP_FWD_WGS 8
+#define GCLIP_FWD_WGS 4
+#endif
+#ifndef GCLIP_FWD_WGS1
+#define GCLIP_FWD_WGS1 8
 #endif
 
 // One pass: a row's elements are read once, into the registers of LANES
 // lanes, where its mean, its squared deviations from it and y are taken from
 // them in turn.  While a row is worked on, the loads of the workgroup's next
 // one are under way; weight and bias stay in registers.
-template <int DT, int LANES, int NV, bool RES, bool DROP>
+template <int DT, int LANES, int NV, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
   constexpr int kThreads = kFwdThreads<LANES>;
-  constexpr uint32_t kRows = kThreads / LANES;  // of a workgroup at a time
+  const uint32_t at_once = LANES > 64 ? kThreads / LANES : blockDim.x / LANES;  // rows of a workgroup
   __shared__ float red[2][kThreads / 64];
   const uint32_t lane = threadIdx.x % LANES;
   uint32_t slot = threadIdx.x / LANES;
@@ -29,15 +34,15 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
   const uint32_t step = DROP ? drop_step(d) : 0u;
 
   Raw8<DT> nx[NV], nr[NV];
-  uint32_t base = blockIdx.x * kRows;
+  uint32_t base = blockIdx.x * at_once;
   const auto fetch = [&](uint32_t first) {
     // rows past the end are read as the last one, and not written
     const uint32_t r = min(first + slot, a.rows - 1);
     const uint64_t x = a.x.at + r * a.x.ld, q = a.residual.at + r * a.residual.ld;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      nx[k] = load_clamped<DT, true>(x, column_of(lane, LANES, k), a.size);
-      if constexpr (RES) nr[k] = load_clamped<DT, true>(q, column_of(lane, LANES, k), a.size);
+      nx[k] = load_clamped<DT, STREAMED>(x, column_of(lane, LANES, k), a.size);
+      if constexpr (RES) nr[k] = load_clamped<DT, STREAMED>(q, column_of(lane, LANES, k), a.size);
     }
   };
   fetch(base);
@@ -69,13 +74,13 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
         unpack<DT>(o[k], v[k]);
       }
     }
-    const uint32_t next = base + gridDim.x * kRows;
+    const uint32_t next = base + gridDim.x * at_once;
     if (next < a.rows) fetch(next);
     if constexpr (RES) {
       if (r < a.rows) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-          store_columns<DT>(a.h.at + r * a.h.ld, column_of(lane, LANES, k), a.size, o[k]);
+          store_columns<DT, kNtStore<DT, STREAMED>>(a.h.at + r * a.h.ld, column_of(lane, LANES, k), a.size, o[k]);
       }
     }
 
@@ -128,7 +133,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[k][j] = __builtin_fmaf((v[k][j] - mean) * rstd, w[k][j], b[k][j]);
-        store_columns<DT>(a.y.at + r * a.y.ld, column_of(lane, LANES, k), a.size, pack<DT>(v[k]));
+        store_columns<DT, kNtStore<DT, STREAMED>>(a.y.at + r * a.y.ld, column_of(lane, LANES, k), a.size, pack<DT>(v[k]));
       }
       if (a.mean && lane == 0) {
         a.mean[r] = mean;
@@ -139,16 +144,20 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
   }
 }
 
-template <int DT, int LANES, int NV>
+template <int DT, int LANES, int NV, bool STREAMED>
 hipError_t forward_shape(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  constexpr int kThreads = kFwdThreads<LANES>;
-  constexpr uint32_t kRows = kThreads / LANES;
-  const uint32_t most = 256u * GCLIP_FWD_WGS * 256 / kThreads;
-  const uint32_t need = (a.rows + kRows - 1) / kRows;
-  const dim3 grid(need < most ? need : most), block(kThreads);
-  if (!residual) hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, false, false>), grid, block, 0, st, a, DropArgs{});
-  else if (!drop) hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, false>), grid, block, 0, st, a, DropArgs{});
-  else hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, true>), grid, block, 0, st, a, *drop);
+  // workgroups of a wave until there are four for each compute unit
+  const uint32_t threads = LANES <= 64 && a.rows < 1024 * (64 / LANES) ? 64 : kFwdThreads<LANES>;
+  const uint32_t at_once = threads / LANES;
+  const uint32_t most = 256u * (NV == 1 ? GCLIP_FWD_WGS1 : GCLIP_FWD_WGS) * 256 / threads;
+  const uint32_t need = (a.rows + at_once - 1) / at_once;
+  const dim3 grid(need < most ? need : most), block(threads);
+  if (!residual)
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+  else if (!drop)
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+  else
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, true, STREAMED>), grid, block, 0, st, a, *drop);
   return hipGetLastError();
 }
 
@@ -157,11 +166,23 @@ hipError_t forward_of(int shape, const FwdArgs& a, bool residual, const DropArgs
   if constexpr (I + 1 < (int)(sizeof(kFwdShapes) / sizeof(kFwdShapes[0]))) {
     if (shape != I) return forward_of<DT, I + 1>(shape, a, residual, drop, st);
   }
-  return forward_shape<DT, kFwdShapes[I].lanes, kFwdShapes[I].groups>(a, residual, drop, st);
+  constexpr RowShape s = kFwdShapes[I];
+  return a.streamed ? forward_shape<DT, s.lanes, s.groups, true>(a, residual, drop, st)
+                    : forward_shape<DT, s.lanes, s.groups, false>(a, residual, drop, st);
+}
+
+template <int DT, int I = 0>
+hipError_t forward_few(int shape, const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kFewShapes) / sizeof(kFewShapes[0]))) {
+    if (shape != I) return forward_few<DT, I + 1>(shape, a, residual, drop, st);
+  }
+  return forward_shape<DT, kFewShapes[I].lanes, kFewShapes[I].groups, false>(a, residual, drop, st);
 }
 
 template <int DT>
 hipError_t forward_rows(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  static_assert(GCLIP_STREAM_MB < 100 || (uint64_t)kFewRows * kRegistersMax * 4 * 4 <= kStreamBytes, "few rows are not streamed");
+  if (a.rows <= kFewRows) return forward_few<DT>(row_shape_of(kFewShapes, a.size), a, residual, drop, st);
   return forward_of<DT>(row_shape_of(kFwdShapes, a.size), a, residual, drop, st);
 }
 

@@ -20,6 +20,11 @@ columns of a wider one, one row expanded).
 """
 import ctypes
 
+try:
+    import torch
+except ImportError:  # the functions named like the C ABI do without it
+    torch = None
+
 from . import _check, _lib
 from ._lib import GCLIP_BF16, GCLIP_F16, GCLIP_F32, GclipDropout, GclipLayerBackward, GclipLayerForward
 
@@ -55,37 +60,44 @@ def gclip_layer_workspace(rows, size):
 
 
 # ---------------------------------------------------------------- tensors as operands
-_codes = {}
+if torch is not None:
+    _CODES = {torch.float32: GCLIP_F32, torch.float16: GCLIP_F16, torch.bfloat16: GCLIP_BF16}
+    _F32 = torch.float32
+    # a small call takes a few microseconds: torch.cuda.current_stream() alone
+    # would be a third of it
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _code(t, name):
-    if not _codes:
-        import torch
-        _codes.update({torch.float32: GCLIP_F32, torch.float16: GCLIP_F16, torch.bfloat16: GCLIP_BF16})
-    c = _codes.get(t.dtype)
-    if c is None:
-        raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    return c
-
-
-def _device(t, name):
-    """The tensor's device, which has to be the current one: kernels are
-    enqueued there."""
-    import torch
-    if not t.is_cuda:
+def _matrix(x, name):
+    """(device index, rows, size, ld, dtype code) of the matrix that a call
+    goes by; its device has to be the current one: kernels are enqueued
+    there."""
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name}: unsupported dtype {x.dtype}")
+    device = x.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be a device tensor")
-    d = t.device
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {d}, the current device is {torch.cuda.current_device()}")
-    return d
+    if device != _current_device():
+        raise ValueError(f"{name} is on device {device}, the current one is {_current_device()}")
+    shape = x.shape
+    if not shape:
+        raise ValueError(f"{name} must have at least one dimension")
+    size = shape[-1]
+    if size:
+        return device, x.numel() // size, size, size if x.is_contiguous() else _ld(x, name), code
+    rows = 1
+    for n in shape[:-1]:
+        rows *= n
+    return device, rows, 0, 0, code
 
 
 def _ld(t, name):
     """Distance of a matrix's rows in elements."""
-    if t.is_contiguous():
-        return t.shape[-1]
     shape, stride = t.shape, t.stride()
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return shape[-1]
     lead = [(n, s) for n, s in zip(shape[:-1], stride[:-1]) if n != 1]
     if (shape[-1] != 1 and stride[-1] != 1) or any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
@@ -97,72 +109,37 @@ def _like(t, x, name):
     """ld of a matrix of x's shape, dtype and device."""
     if t.dtype != x.dtype:
         raise TypeError(f"{name} must have dtype {x.dtype}, not {t.dtype}")
-    if t.shape != x.shape or t.device != x.device:
+    if t.shape != x.shape or t.get_device() != x.get_device():
         raise ValueError(f"{name} must have shape {tuple(x.shape)} on {x.device}")
-    return _ld(t, name)
+    return t.shape[-1] if t.is_contiguous() else _ld(t, name)
 
 
-def _vector(t, n, dtypes, x, name):
-    """Address of a contiguous vector of n elements; None (no such operand) is 0."""
-    if t is None:
-        return None
-    if t.dtype not in dtypes:
+def _vector(t, n, x, name):
+    """Address of a contiguous binary32 vector, or one of x's dtype."""
+    if t.dtype != _F32 and t.dtype != x.dtype:
         raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-    if t.numel() != n or not t.is_contiguous() or t.device != x.device:
+    if t.numel() != n or not t.is_contiguous() or t.get_device() != x.get_device():
         raise ValueError(f"{name} must hold {n} contiguous elements on {x.device}")
     return t.data_ptr()
 
 
-def _extent(x, name):
-    """(rows, size) of a matrix."""
-    if x.dim() == 0:
-        raise ValueError(f"{name} must have at least one dimension")
-    size = x.shape[-1]
-    if size:
-        return x.numel() // size, size
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
-    return rows, 0
+def _statistic(t, n, x, name):
+    if t.dtype != _F32:
+        raise TypeError(f"{name} must be float32, not {t.dtype}")
+    return _vector(t, n, x, name)
 
 
-def _f32():
-    import torch
-    return torch.float32
-
-
-class _On:
-    """The stream of a call: its raw handle, and new tensors and operands'
-    lifetimes on a stream that is not the current one."""
-
-    def __init__(self, stream, operands):
-        import torch
-        current = torch.cuda.current_stream()
-        self.raw = current.cuda_stream if stream is None else stream.cuda_stream
-        self.guard = None
-        if stream is not None and stream != current:
-            for t in operands:
-                if t is not None:
-                    t.record_stream(stream)
-            self.guard = torch.cuda.stream(stream)
-            self.guard.__enter__()
-
-    def __enter__(self):
-        return self.raw
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
-
-
-def _weights_of(weight, bias, x, size):
-    wt = weight if weight is not None else bias
-    if wt is None:
-        return None, None, GCLIP_F32
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have one dtype")
-    allowed = (_f32(), x.dtype)
-    return _vector(weight, size, allowed, x, "weight"), _vector(bias, size, allowed, x, "bias"), _code(wt, "weight")
+def _there(stream, f, *args):
+    """f(*args) on another stream than the current one: its new tensors are
+    that stream's, and its operands' memory is not given out before it has
+    run."""
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+        elif isinstance(t, DropoutMask) and t.counter is not None:
+            t.counter.record_stream(stream)
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 # ---------------------------------------------------------------- dropout
@@ -189,7 +166,6 @@ class DropoutMask:
             raise ValueError("seed takes 64 bits, step and site take 32")
         address = None
         if counter is not None:
-            import torch
             if counter.dtype != torch.int32 or not counter.is_cuda or counter.numel() < 1:
                 raise ValueError("counter must be an int32 device tensor")
             address = counter.data_ptr()
@@ -209,14 +185,15 @@ class DropoutMask:
 
 def dropout_forward(x, mask, out=None, stream=None):
     """x where the mask keeps it, times 1 / (1 - p); else 0.  out may be x."""
-    import torch
-    _device(x, "x")
-    rows, size = _extent(x, "x")
-    with _On(stream, (x, out, mask.counter)) as raw:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        gclip_dropout_apply(x.data_ptr(), _ld(x, "x"), out.data_ptr(), _like(out, x, "out"), rows, size, _code(x, "x"),
-                            mask.args, raw)
+    if stream is not None:
+        return _there(stream, dropout_forward, x, mask, out)
+    device, rows, size, ld, code = _matrix(x, "x")
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldo = size
+    else:
+        ldo = _like(out, x, "out")
+    gclip_dropout_apply(x.data_ptr(), ld, out.data_ptr(), ldo, rows, size, code, mask.args, _raw_stream(device))
     return out
 
 
@@ -229,40 +206,50 @@ def dropout_backward(dy, mask, out=None, stream=None):
 def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out=None, stats=True, stream=None):
     """(y, mean, rstd) of the norm over the last dimension.  mean and rstd are
     what the backward pass takes, and None without ``stats``."""
-    return _forward(x, None, weight, bias, eps, None, None, out, stats, stream)[1:]
+    args = x, None, weight, bias, eps, None, None, out, stats
+    return (_forward(*args) if stream is None else _there(stream, _forward, *args))[1:]
 
 
 def residual_norm_forward(x, residual, weight=None, bias=None, eps=1e-5, mask=None, *, out_h=None, out=None,
                           stats=True, stream=None):
     """(h, y, mean, rstd) of h = residual + dropout(x), y = norm(h).  out_h
     may be residual or x (in place)."""
-    return _forward(x, residual, weight, bias, eps, mask, out_h, out, stats, stream)
+    args = x, residual, weight, bias, eps, mask, out_h, out, stats
+    return _forward(*args) if stream is None else _there(stream, _forward, *args)
 
 
-def _forward(x, residual, weight, bias, eps, mask, h, y, stats, stream):
-    import torch
-    _device(x, "x")
-    rows, size = _extent(x, "x")
-    wp, bp, wdt = _weights_of(weight, bias, x, size)
-    ldr = _like(residual, x, "residual") if residual is not None else 0
-    with _On(stream, (x, residual, weight, bias, h, y, mask.counter if mask is not None else None)) as raw:
-        if y is None:
-            y = torch.empty_like(x, memory_format=torch.contiguous_format)
-        if residual is not None and h is None:
-            h = torch.empty_like(x, memory_format=torch.contiguous_format)
-        mean = rstd = mp = rp = None
-        if stats:
-            mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device).unbind(0)
-            mp, rp = mean.data_ptr(), rstd.data_ptr()
-        if residual is None:
-            gclip_layernorm_forward(GclipLayerForward(
-                rows, size, _code(x, "x"), wdt, eps, x.data_ptr(), _ld(x, "x"), None, 0, wp, bp, None, 0,
-                y.data_ptr(), _like(y, x, "out"), mp, rp), raw)
-        else:
-            gclip_residual_forward(GclipLayerForward(
-                rows, size, _code(x, "x"), wdt, eps, x.data_ptr(), _ld(x, "x"), residual.data_ptr(), ldr, wp, bp,
-                h.data_ptr(), _like(h, x, "out_h"), y.data_ptr(), _like(y, x, "out"), mp, rp),
-                mask.args if mask is not None and mask.drops else None, raw)
+def _forward(x, residual, weight, bias, eps, mask, h, y, stats):
+    device, rows, size, ld, code = _matrix(x, "x")
+    wp = bp = None
+    wdt = GCLIP_F32
+    if bias is not None:
+        bp, wdt = _vector(bias, size, x, "bias"), _CODES[bias.dtype]
+    if weight is not None:
+        wp, wdt = _vector(weight, size, x, "weight"), _CODES[weight.dtype]
+        if bias is not None and bias.dtype != weight.dtype:
+            raise TypeError("weight and bias must have one dtype")
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldy = size
+    else:
+        ldy = _like(y, x, "out")
+    mean = rstd = mp = rp = None
+    if stats:
+        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=_F32, device=x.device).unbind(0)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
+    if residual is None:
+        gclip_layernorm_forward(GclipLayerForward(rows, size, code, wdt, eps, x.data_ptr(), ld, None, 0, wp, bp, None,
+                                                  0, y.data_ptr(), ldy, mp, rp), _raw_stream(device))
+        return None, y, mean, rstd
+    ldr = _like(residual, x, "residual")
+    if h is None:
+        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldh = size
+    else:
+        ldh = _like(h, x, "out_h")
+    gclip_residual_forward(GclipLayerForward(rows, size, code, wdt, eps, x.data_ptr(), ld, residual.data_ptr(), ldr,
+                                             wp, bp, h.data_ptr(), ldh, y.data_ptr(), ldy, mp, rp),
+                           mask.args if mask is not None and mask.drops else None, _raw_stream(device))
     return h, y, mean, rstd
 
 
@@ -277,8 +264,8 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, dweight=None, dbias=N
     weight_grad, bias_grad  whether they are wanted; by default when weight is
                     given, or a buffer for them
     """
-    dx, _, dw, db = _backward(dy, None, x, mean, rstd, weight, None, False, dweight, dbias, accumulate, weight_grad,
-                              bias_grad, out, None, stream)
+    args = dy, None, x, mean, rstd, weight, None, False, dweight, dbias, accumulate, weight_grad, bias_grad, out, None
+    dx, _, dw, db = _backward(*args) if stream is None else _there(stream, _backward, *args)
     return dx, dw, db
 
 
@@ -289,72 +276,77 @@ def residual_norm_backward(dy, dh, h, mean, rstd, weight=None, mask=None, *, dwe
     and rstd that its forward pass returned and the same mask.  dh is the
     gradient of h from its other uses, or None.  Without dropout dx is
     dresidual, the same tensor.  Otherwise as ``layer_norm_backward``."""
-    return _backward(dy, dh, h, mean, rstd, weight, mask if mask is not None and mask.drops else None, True, dweight,
-                     dbias, accumulate, weight_grad, bias_grad, out, out_residual, stream)
+    args = (dy, dh, h, mean, rstd, weight, mask if mask is not None and mask.drops else None, True, dweight, dbias,
+            accumulate, weight_grad, bias_grad, out, out_residual)
+    return _backward(*args) if stream is None else _there(stream, _backward, *args)
 
 
 def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, accumulate, weight_grad, bias_grad, dx,
-              dres, stream):
-    import torch
-    _device(x, "x")
-    rows, size = _extent(x, "x")
-    wp, _, wdt = _weights_of(weight, None, x, size)
+              dres):
+    device, rows, size, ld, code = _matrix(x, "x")
+    wp, wdt, gt = None, GCLIP_F32, _F32
+    if weight is not None:
+        wp, gt = _vector(weight, size, x, "weight"), weight.dtype
+        wdt = _CODES[gt]
     want_w = dweight is not None or (weight is not None if weight_grad is None else weight_grad)
     want_b = dbias is not None or (weight is not None if bias_grad is None else bias_grad)
     if accumulate and ((want_w and dweight is None) or (want_b and dbias is None)):
         raise ValueError("accumulate needs the buffers to add to: dweight and dbias")
-    f32 = torch.float32
-    allowed = (f32, x.dtype)
-    mp, rp = _vector(mean, rows, (f32,), x, "mean"), _vector(rstd, rows, (f32,), x, "rstd")
-    lddy, lddh = _like(dy, x, "dy"), _like(dh, x, "dh") if dh is not None else 0
-    if residual and mask is None:
+    mp, rp = _statistic(mean, rows, x, "mean"), _statistic(rstd, rows, x, "rstd")
+    lddy, hp, lddh = _like(dy, x, "dy"), None, 0
+    if dh is not None:
+        hp, lddh = dh.data_ptr(), _like(dh, x, "dh")
+    wgp = bgp = wsp = None
+    nbytes = 0
+    if want_w or want_b:
+        if dweight is not None:
+            gt = dweight.dtype
+            if dbias is not None and dbias.dtype != gt:
+                raise TypeError("dweight and dbias must have one dtype")
+        elif dbias is not None:
+            gt = dbias.dtype
+        if want_w:
+            if dweight is None:
+                dweight = torch.empty(size, dtype=gt, device=x.device)
+            wgp = _vector(dweight, size, x, "dweight")
+        if want_b:
+            if dbias is None:
+                dbias = torch.empty(size, dtype=gt, device=x.device)
+            bgp = _vector(dbias, size, x, "dbias")
+        nbytes = gclip_layer_workspace(rows, size)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+        wsp = workspace.data_ptr()
+    second = not residual or mask is not None  # dx apart from dresidual
+    if not second:
         if dx is not None and dres is not None and dx is not dres:
             raise ValueError("without dropout dx is dresidual: give one buffer")
         dres = dres if dres is not None else dx
-    operands = (dy, dh, x, mean, rstd, weight, dweight, dbias, dx, dres, mask.counter if mask is not None else None)
-    with _On(stream, operands) as raw:
-        gt = weight.dtype if weight is not None else f32
-        wants = [t for t in (dweight, dbias) if t is not None]
-        if wants:
-            gt = wants[0].dtype
-            if wants[-1].dtype != gt:
-                raise TypeError("dweight and dbias must have one dtype")
-        if want_w and dweight is None:
-            dweight = torch.empty(size, dtype=gt, device=x.device)
-        if want_b and dbias is None:
-            dbias = torch.empty(size, dtype=gt, device=x.device)
-        wsp, nbytes = None, 0
-        gdt = GCLIP_F32
-        if want_w or want_b:
-            nbytes = gclip_layer_workspace(rows, size)
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-            wsp = workspace.data_ptr()
-            gdt = _code(dweight if dweight is not None else dbias, "dweight")
-        if residual:
-            if dres is None:
-                dres = torch.empty_like(x, memory_format=torch.contiguous_format)
-            if mask is not None and dx is None:
-                dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-        elif dx is None:
+    xp = sp = None
+    lddx = ldds = 0
+    if second:
+        if dx is None:
             dx = torch.empty_like(x, memory_format=torch.contiguous_format)
-        second = not residual or mask is not None  # dx apart from dresidual
-        args = GclipLayerBackward(
-            rows, size, _code(x, "x"), wdt, gdt, 1 if accumulate else 0, dy.data_ptr(), lddy,
-            dh.data_ptr() if dh is not None else None, lddh, x.data_ptr(), _ld(x, "x"), mp, rp, wp,
-            dres.data_ptr() if residual else None, _like(dres, x, "out_residual") if residual else 0,
-            dx.data_ptr() if second else None, _like(dx, x, "out") if second else 0,
-            _vector(dweight, size, allowed, x, "dweight"), _vector(dbias, size, allowed, x, "dbias"), wsp, nbytes)
-        if residual:
-            gclip_residual_backward(args, mask.args if mask is not None else None, raw)
+            lddx = size
         else:
-            gclip_layernorm_backward(args, raw)
-    return (dx if second else dres), dres, dweight, dbias
+            lddx = _like(dx, x, "out")
+        xp = dx.data_ptr()
+    if residual:
+        if dres is None:
+            dres = torch.empty_like(x, memory_format=torch.contiguous_format)
+            ldds = size
+        else:
+            ldds = _like(dres, x, "out_residual")
+        sp = dres.data_ptr()
+    args = GclipLayerBackward(rows, size, code, wdt, _CODES[gt], 1 if accumulate else 0, dy.data_ptr(), lddy, hp, lddh,
+                              x.data_ptr(), ld, mp, rp, wp, sp, ldds, xp, lddx, wgp, bgp, wsp, nbytes)
+    if residual:
+        gclip_residual_backward(args, mask.args if mask is not None else None, _raw_stream(device))
+    else:
+        gclip_layernorm_backward(args, _raw_stream(device))
+    return dx if second else dres, dres, dweight, dbias
 
 
 # ---------------------------------------------------------------- under autograd
-_functions = {}
-
-
 def _matrix_of(t):
     """A gradient from autograd in a form that the kernels take: an expanded
     or permuted one is copied."""
@@ -365,14 +357,10 @@ def _matrix_of(t):
         return t.contiguous()
 
 
-def _autograd():
-    """The autograd functions (torch is imported where it is used only)."""
-    if _functions:
-        return _functions
-    import torch
+if torch is not None:
     from torch.autograd.function import once_differentiable
 
-    class Dropout(torch.autograd.Function):
+    class _Dropout(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, mask):
             ctx.mask = mask
@@ -383,7 +371,7 @@ def _autograd():
         def backward(ctx, dy):
             return dropout_backward(_matrix_of(dy), ctx.mask), None
 
-    class LayerNorm(torch.autograd.Function):
+    class _LayerNorm(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, weight, bias, eps):
             y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
@@ -400,7 +388,7 @@ def _autograd():
                                              weight_grad=False, bias_grad=False)
             return dx, dw, db, None
 
-    class ResidualNorm(torch.autograd.Function):
+    class _ResidualNorm(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, residual, weight, bias, eps, mask):
             h, y, mean, rstd = residual_norm_forward(x, residual, weight, bias, eps, mask)
@@ -425,33 +413,28 @@ def _autograd():
                                                       dbias=db, weight_grad=False, bias_grad=False)
             return dx, dres, dw, db, None, None
 
-    _functions.update(dropout=Dropout, layer_norm=LayerNorm, residual_norm=ResidualNorm)
-    return _functions
-
 
 def _grad_buffers(ctx, x, weight, at):
     """New buffers for those weights' gradients that are asked for."""
-    import torch
     new = lambda dtype: torch.empty(x.shape[-1], dtype=dtype, device=x.device)  # noqa: E731
     return (new(weight.dtype) if ctx.needs_input_grad[at] else None,
             new(ctx.bias_dtype) if ctx.needs_input_grad[at + 1] else None)
 
 
 def _tracked(*tensors):
-    import torch
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 
 def dropout(x, mask):
     """Dropout of x by the mask (a ``DropoutMask``)."""
-    return _autograd()["dropout"].apply(x, mask) if _tracked(x) else dropout_forward(x, mask)
+    return _Dropout.apply(x, mask) if _tracked(x) else dropout_forward(x, mask)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5):
     """The norm of x over its last dimension."""
     if not _tracked(x, weight, bias):
         return layer_norm_forward(x, weight, bias, eps, stats=False)[0]
-    return _autograd()["layer_norm"].apply(x, weight, bias, eps)
+    return _LayerNorm.apply(x, weight, bias, eps)
 
 
 def residual_norm(x, residual, weight=None, bias=None, eps=1e-5, mask=None):
@@ -459,4 +442,4 @@ def residual_norm(x, residual, weight=None, bias=None, eps=1e-5, mask=None):
     nothing is dropped (evaluation)."""
     if not _tracked(x, residual, weight, bias):
         return residual_norm_forward(x, residual, weight, bias, eps, mask, stats=False)[:2]
-    return _autograd()["residual_norm"].apply(x, residual, weight, bias, eps, mask)
+    return _ResidualNorm.apply(x, residual, weight, bias, eps, mask)
