@@ -54,8 +54,11 @@ struct RowShape {
 };
 constexpr RowShape kFwdShapes[] = {{8, 1},  {16, 1}, {32, 1},  {64, 1},  {32, 3},  {64, 2}, {64, 3},
                                    {64, 4}, {256, 2}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
+#ifndef GCLIP_BWD8
+#define GCLIP_BWD8 {512, 2}
+#endif
 constexpr RowShape kBwdShapes[] = {{8, 1},   {16, 1},  {32, 1},  {64, 1},  {64, 2},
-                                   {128, 2}, {256, 2}, {512, 2}, {512, 3}, {512, 4}};
+                                   {128, 2}, {256, 2}, GCLIP_BWD8, {1024, 2}};
 // Few rows: more lanes each.
 #ifndef GCLIP_FEW_ROWS
 #define GCLIP_FEW_ROWS 512
@@ -71,9 +74,10 @@ constexpr int row_shape_of(const RowShape (&shapes)[N], uint32_t size) {
 }
 inline bool in_registers(uint32_t size) { return size >= kRegistersMin && size <= kRegistersMax; }
 
-// Threads of a workgroup of the backward kernel, and the most workgroups,
-// each of which leaves one partial sum of the weights' gradients.
-constexpr uint32_t kBwdThreads = 512;
+// Threads of a workgroup of the backward kernel: all that a compute unit's
+// registers hold, so that each unit leaves one partial sum of the weights'
+// gradients, of kBwdParts at most.
+constexpr uint32_t bwd_threads(uint32_t lanes, uint32_t groups) { return groups == 1 || lanes > 512 ? 1024 : 512; }
 constexpr uint32_t kBwdParts = 256;
 
 // What a call moves decides how.  Up to kStreamBytes the matrices may lie in

@@ -14,12 +14,18 @@ namespace gclip {
 // meet in shared memory at the end.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
 template <int DT, int LANES, int NV, bool RES, bool DROP, bool STREAMED>
-__global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
+__global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
+  constexpr uint32_t kBwdThreads = bwd_threads(LANES, NV);
   constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
+  // sixteen waves' registers do not hold two groups' sums beside the row: they
+  // lie in shared memory, each lane's its own, and the weights are read again
+  // for each row, from the caches
+  constexpr bool kLong = LANES > 512 && NV > 1;
+  static_assert(!kLong || kRows == 1, "a long row has its workgroup to itself");
   constexpr uint32_t kCols = LANES * NV * kGroup;
   constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
   __shared__ float red[2][2][kBwdThreads / 64];
-  __shared__ float sums[kMeet > 1 ? kMeet * kCols : 1];
+  __shared__ __align__(16) float sums[kLong ? 2 * kCols : kMeet > 1 ? kMeet * kCols : 1];
   const uint32_t lane = threadIdx.x % LANES;
   uint32_t slot = threadIdx.x / LANES;
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
@@ -43,15 +49,19 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
     }
   };
   fetch(base);
-  // four groups' weights would not fit beside the sums: they are read again
-  // for each row, from the caches
-  constexpr bool kKeep = NV < 4;
-  float w[kKeep ? NV : 1][8], dw[NV][8], db[NV][8];
+  float w[kLong ? 1 : NV][8], dw[kLong ? 1 : NV][8], db[kLong ? 1 : NV][8];
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  f32x4* const own = reinterpret_cast<f32x4*>(sums) + threadIdx.x;  // [dw, db][NV][2], kBwdThreads apart
+  if constexpr (kLong) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if constexpr (kKeep) weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+    for (int k = 0; k < 4 * NV; ++k) own[k * kBwdThreads] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+    for (int k = 0; k < NV; ++k) {
+      weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+    }
   }
   const float count = (float)a.size;
   uint32_t turn = 0;
@@ -67,13 +77,6 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
       const uint32_t c = column_of(lane, LANES, k);
       settle<DT>(ny[k], r < a.rows ? c : a.size, a.size);
       settle<DT>(nx[k], c, a.size);
-      float wk[8];
-      if constexpr (kKeep) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) wk[j] = w[k][j];
-      } else {
-        weight_columns<DT>(a.weight, a.wdt, c, a.size, 1.0f, wk);
-      }
       unpack<DT>(ny[k], g[k]);
       unpack<DT>(nx[k], n[k]);
       if constexpr (RES) {
@@ -81,10 +84,31 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
         hh[k] = nh[k];
       }
 #pragma unroll
+      for (int j = 0; j < 8; ++j) n[k][j] = (n[k][j] - mean) * rstd;
+      float wk[8];
+      if constexpr (kLong) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          f32x4 t = own[(2 * k + i) * kBwdThreads], u = own[(2 * NV + 2 * k + i) * kBwdThreads];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            t[j] = __builtin_fmaf(g[k][4 * i + j], n[k][4 * i + j], t[j]);
+            u[j] += g[k][4 * i + j];
+          }
+          own[(2 * k + i) * kBwdThreads] = t;
+          own[(2 * NV + 2 * k + i) * kBwdThreads] = u;
+        }
+        weight_columns<DT>(a.weight, a.wdt, c, a.size, 1.0f, wk);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
+          db[k][j] += g[k][j];
+          wk[j] = w[k][j];
+        }
+      }
+#pragma unroll
       for (int j = 0; j < 8; ++j) {
-        n[k][j] = (n[k][j] - mean) * rstd;
-        dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
-        db[k][j] += g[k][j];
         g[k][j] *= wk[j];
         s1 += g[k][j];
         s2 = __builtin_fmaf(g[k][j], n[k][j], s2);
@@ -144,8 +168,23 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
   if (!a.dweight && !a.dbias) return;
 #pragma unroll
   for (uint32_t which = 0; which < 2; ++which) {
-    float(&v)[NV][8] = which ? db : dw;
-    if constexpr (kMeet > 1) {
+    if constexpr (kLong) {
+#pragma unroll
+      for (int k = 0; k < 2 * NV; ++k) {
+        const f32x4 t = own[(which * 2 * NV + k) * kBwdThreads];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t c = column_of(lane, LANES, k / 2) + k % 2 * 4 + j;
+          if (c < a.size) {
+            if (a.parts == 1) store_weight_grad<DT>(a, which, c, t[j]);
+            else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t[j];
+          }
+        }
+      }
+      continue;
+    }
+    float(&v)[kLong ? 1 : NV][8] = which ? db : dw;
+    if constexpr (kMeet > 1 && !kLong) {
       const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
       __syncthreads();
 #pragma unroll
@@ -164,7 +203,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_rows_grad(BwdArgs a, DropA
         if (a.parts == 1) store_weight_grad<DT>(a, which, c, t);
         else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t;
       }
-    } else {
+    } else if constexpr (!kLong) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -211,8 +250,10 @@ hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
 }
 
 template <int DT, int LANES, int NV, bool STREAMED>
-hipError_t backward_shape(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  const dim3 grid(a.parts), block(kBwdThreads);
+hipError_t backward_shape(BwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
+  const uint32_t threads = bwd_threads(LANES, NV), at_once = threads / LANES;
+  a.parts = (a.rows - 1) / at_once + 1 < kBwdParts ? (a.rows - 1) / at_once + 1 : kBwdParts;
+  const dim3 grid(a.parts), block(threads);
   if (!residual)
     hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else if (!drop)

@@ -216,6 +216,44 @@ __device__ __forceinline__ void store_group8(uint64_t row, uint32_t g, uint32_t 
   else if (c < size) store_tail<DT>(row + (uint64_t)c * kElem<DT>, r, size - c);
 }
 
+// Unit u, 16 bytes, of a row: a group, or half of one of binary32.
+template <int DT, bool NT>
+__device__ __forceinline__ u32x4 load_unit(uint64_t row, uint32_t u, uint32_t size) {
+  if constexpr (DT == GCLIP_F32) {
+    typedef __attribute__((address_space(1))) u32x4_any4 g_t;
+    const uint32_t c = u * 4;
+    if (c + 4 <= size) {
+      const g_t* p = reinterpret_cast<const g_t*>(row + c * 4ull);
+      return NT ? __builtin_nontemporal_load(p) : *p;
+    }
+    u32x4 q{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (uint32_t k = 0; k < 3; ++k)
+      if (c + k < size) q[k] = load_elem<DT>(row + (c + k) * 4ull);
+    return q;
+  } else {
+    return load_group8<DT, NT>(row, u, size).q[0];
+  }
+}
+template <int DT, bool NT>
+__device__ __forceinline__ void store_unit(uint64_t row, uint32_t u, uint32_t size, const u32x4& q) {
+  if constexpr (DT == GCLIP_F32) {
+    typedef __attribute__((address_space(1))) u32x4_any4 g_t;
+    const uint32_t c = u * 4;
+    if (c + 4 <= size) {
+      g_t* p = reinterpret_cast<g_t*>(row + c * 4ull);
+      if constexpr (NT) __builtin_nontemporal_store(q, p);
+      else *p = q;
+    } else {
+#pragma unroll
+      for (uint32_t k = 0; k < 3; ++k)
+        if (c + k < size) store_elem<DT>(row + (c + k) * 4ull, q[k]);
+    }
+  } else {
+    store_group8<DT, NT>(row, u, size, Raw8<DT>{{q}});
+  }
+}
+
 // ---------------------------------------------------------------- weights
 // Eight elements of weight or bias (binary32 or the matrices' format; `def`
 // where there is none).
@@ -251,6 +289,13 @@ __device__ __forceinline__ Words4 philox(uint32_t c0, uint32_t c1, uint32_t c2, 
 }
 
 __device__ __forceinline__ uint32_t drop_step(const DropArgs& d) { return d.step + (d.d_step ? *d.d_step : 0u); }
+
+// The generator's halves for one half of a group.
+__device__ __forceinline__ uint64_t philox_half(const DropArgs& d, uint32_t step, uint32_t row, uint32_t g, uint32_t h) {
+  const Words4 b = philox(g, row, d.site, step, d.k0, d.k1);
+  const uint64_t lo = (uint64_t)b.w[0] | ((uint64_t)b.w[1] << 32), hi = (uint64_t)b.w[2] | ((uint64_t)b.w[3] << 32);
+  return h ? hi : lo;
+}
 
 // v * scale where kept, else 0 (a select: a dropped NaN is 0).  The product
 // is rounded before whatever is added to it, so the residual step's h does
