@@ -166,65 +166,23 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_cols_grad_any(BwdArgs a) {
   }
 }
 
-// A lane takes kDropUnits units of 16 bytes, a workgroup's width apart, and
-// follows their row and column by addition.  A unit of a 16-bit format is a
-// group; of binary32 half of one, whose two lanes run the generator both:
-// lanes' accesses are adjacent then, and there is twice the time for it.
-#ifndef GCLIP_DROP_UNITS
-#define GCLIP_DROP_UNITS 2
-#endif
-#ifndef GCLIP_DROP_LNT
-#define GCLIP_DROP_LNT false
-#endif
-#ifndef GCLIP_DROP_SNT
-#define GCLIP_DROP_SNT true
-#endif
-constexpr int kDropUnits = GCLIP_DROP_UNITS;
-template <int DT>
-constexpr uint32_t kUnit = DT == GCLIP_F32 ? 4u : 8u;
-
+// A lane takes a unit of 16 bytes.  A unit of a 16-bit format is a group; of
+// binary32 half of one, whose two lanes run the generator both: a wave's
+// accesses are adjacent then, and there is twice the time for it.  Bound by
+// memory, with the generator's products (20 for eight elements, at a quarter
+// of the full rate) close behind in 16 bits: 1.3B's 16384 x 2048 in bfloat16
+// takes 23.5 us (two units a lane: 24.1), 5.7 TB/s.
 template <int DT, bool STREAMED>
 __global__ __launch_bounds__(kAnyThreads) void k_dropout(Rows x, Rows y, uint32_t rows, uint32_t size, DropArgs d) {
   const uint32_t units = (size + kUnit<DT> - 1) / kUnit<DT>;
-  const uint32_t step = drop_step(d);
-  const uint64_t i = (uint64_t)blockIdx.x * (kAnyThreads * kDropUnits) + threadIdx.x;
-  uint32_t r = (uint32_t)(i / units), u = (uint32_t)(i % units);
-  const uint32_t dr = kAnyThreads / units, du = kAnyThreads % units;
-  uint32_t rr[kDropUnits], uu[kDropUnits];
-  u32x4 q[kDropUnits];
-#pragma unroll
-  for (int k = 0; k < kDropUnits; ++k) {
-    rr[k] = r;
-    uu[k] = u;
-    if (r < rows) q[k] = load_unit<DT, GCLIP_DROP_LNT>(x.at + r * x.ld, u, size);
-    r += dr;
-    u += du;
-    if (u >= units) {
-      u -= units;
-      ++r;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kDropUnits; ++k) {
-    if (rr[k] < rows) {
-      if constexpr (DT == GCLIP_F32) {
-        const uint64_t b = philox_half(d, step, rr[k], uu[k] / 2, uu[k] & 1);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t h = (uint32_t)(b >> (16 * j)) & 0xffffu;
-          q[k][j] = h >= d.threshold ? __float_as_uint(__uint_as_float(q[k][j]) * d.scale) : 0u;
-        }
-      } else {
-        float f[8];
-        Raw8<DT> v{{q[k]}};
-        unpack<DT>(v, f);
-        drop_group(d, step, rr[k], uu[k], f);
-        v = pack<DT>(f);
-        q[k] = v.q[0];
-      }
-      store_unit<DT, GCLIP_DROP_SNT>(y.at + rr[k] * y.ld, uu[k], size, q[k]);
-    }
-  }
+  const uint64_t i = (uint64_t)blockIdx.x * kAnyThreads + threadIdx.x;
+  const uint64_t row = i / units;
+  if (row >= rows) return;
+  const uint32_t r = (uint32_t)row, u = (uint32_t)(i % units);
+  float v[kUnit<DT>];
+  unpack_unit<DT>(load_unit<DT, STREAMED>(x.at + r * x.ld, u, size), v);
+  drop_unit<DT>(d, drop_step(d), r, u * kUnit<DT>, v);
+  store_unit<DT, true>(y.at + r * y.ld, u, size, pack_unit<DT>(v));
 }
 
 template <int DT>
@@ -256,9 +214,10 @@ hipError_t backward_any(const BwdArgs& a, const DropArgs* drop, hipStream_t st) 
 
 template <int DT>
 hipError_t dropout(const Rows& x, const Rows& y, uint32_t rows, uint32_t size, const DropArgs& d, hipStream_t st) {
-  const uint64_t total = (uint64_t)rows * ((size + kUnit<DT> - 1) / kUnit<DT>), per = kAnyThreads * kDropUnits;
-  hipLaunchKernelGGL((k_dropout<DT, false>), dim3((uint32_t)((total + per - 1) / per)), dim3(kAnyThreads), 0, st, x, y, rows,
-                     size, d);
+  const uint64_t total = (uint64_t)rows * ((size + kUnit<DT> - 1) / kUnit<DT>);
+  const dim3 grid((uint32_t)((total + kAnyThreads - 1) / kAnyThreads)), block(kAnyThreads);
+  if (total * 32 > kStreamBytes) hipLaunchKernelGGL((k_dropout<DT, true>), grid, block, 0, st, x, y, rows, size, d);
+  else hipLaunchKernelGGL((k_dropout<DT, false>), grid, block, 0, st, x, y, rows, size, d);
   return hipGetLastError();
 }
 
@@ -269,9 +228,8 @@ hipError_t dropout(const Rows& x, const Rows& y, uint32_t rows, uint32_t size, c
 // them for long rows.
 uint32_t layer_parts(int64_t rows, int64_t size) {
   if (rows > 0 && in_registers((uint32_t)size)) {
-    const RowShape s = kBwdShapes[row_shape_of(kBwdShapes, (uint32_t)size)];
-    const uint32_t at_once = bwd_threads(s.lanes, s.groups) / s.lanes;
-    return std::min<uint32_t>(((uint32_t)rows + at_once - 1) / at_once, kBwdParts);
+    const uint32_t n = (uint32_t)rows;
+    return std::max(bwd_parts<GCLIP_F32>(n, (uint32_t)size), bwd_parts<GCLIP_BF16>(n, (uint32_t)size));
   }
   const int64_t by_rows = std::max<int64_t>(1, (rows + 15) / 16);
   const int64_t by_bytes = std::max<int64_t>(1, (64ll << 20) / (8 * size));

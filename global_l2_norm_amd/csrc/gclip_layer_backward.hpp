@@ -13,16 +13,17 @@ namespace gclip {
 // columns' sums stay in registers over all rows of the workgroup, whose rows
 // meet in shared memory at the end.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
-template <int DT, int LANES, int NV, bool RES, bool DROP, bool STREAMED>
-__global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
-  constexpr uint32_t kBwdThreads = bwd_threads(LANES, NV);
+template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
+__global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
+  constexpr uint32_t kBwdThreads = bwd_threads(LANES, NV * kUnit<DT>);
   constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
   // sixteen waves' registers do not hold two groups' sums beside the row: they
   // lie in shared memory, each lane's its own, and the weights are read again
   // for each row, from the caches
-  constexpr bool kLong = LANES > 512 && NV > 1;
+  constexpr bool kLong = LANES > 512 && NV * kUnit<DT> > 8;
+  constexpr bool kLate = kLong;  // nor dh of the next row: a row's own is loaded while its sums meet
   static_assert(!kLong || kRows == 1, "a long row has its workgroup to itself");
-  constexpr uint32_t kCols = LANES * NV * kGroup;
+  constexpr uint32_t kCols = LANES * NV * kUnit<DT>;
   constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
   __shared__ float red[2][2][kBwdThreads / 64];
   __shared__ __align__(16) float sums[kLong ? 2 * kCols : kMeet > 1 ? kMeet * kCols : 1];
@@ -31,7 +32,7 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
   const uint32_t step = DROP ? drop_step(d) : 0u;
 
-  Raw8<DT> ny[NV], nx[NV], nh[NV];
+  u32x4 ny[NV], nx[NV], nh[NV];
   float nmean, nrstd;
   uint32_t base = blockIdx.x * kRows;
   const auto fetch = [&](uint32_t first) {
@@ -42,25 +43,26 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
     nrstd = a.rstd[r];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const uint32_t c = column_of(lane, LANES, k);
-      ny[k] = load_clamped<DT, STREAMED>(dy, c, a.size);
-      nx[k] = load_clamped<DT, STREAMED>(x, c, a.size);
-      if constexpr (RES) nh[k] = a.dh.at ? load_clamped<DT, STREAMED>(dh, c, a.size) : zero8<DT>();
+      ny[k] = load_columns<DT, LANES, SURE, STREAMED>(dy, lane, k, a.size);
+      nx[k] = load_columns<DT, LANES, SURE, STREAMED>(x, lane, k, a.size);
+      if constexpr (RES && !kLate)
+        nh[k] = a.dh.at ? load_columns<DT, LANES, SURE, STREAMED>(dh, lane, k, a.size) : u32x4{0u, 0u, 0u, 0u};
     }
   };
   fetch(base);
-  float w[kLong ? 1 : NV][8], dw[kLong ? 1 : NV][8], db[kLong ? 1 : NV][8];
+  float w[kLong ? 1 : NV][kUnit<DT>], dw[kLong ? 1 : NV][kUnit<DT>], db[kLong ? 1 : NV][kUnit<DT>];
   typedef float f32x4 __attribute__((ext_vector_type(4)));
-  f32x4* const own = reinterpret_cast<f32x4*>(sums) + threadIdx.x;  // [dw, db][NV][2], kBwdThreads apart
+  constexpr uint32_t kQuads = kUnit<DT> / 4;
+  f32x4* const own = reinterpret_cast<f32x4*>(sums) + threadIdx.x;  // [dw, db][NV][kQuads], kBwdThreads apart
   if constexpr (kLong) {
 #pragma unroll
-    for (int k = 0; k < 4 * NV; ++k) own[k * kBwdThreads] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t k = 0; k < 2 * NV * kQuads; ++k) own[k * kBwdThreads] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
+      weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.0f;
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = db[k][j] = 0.0f;
     }
   }
   const float count = (float)a.size;
@@ -69,49 +71,56 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
   while (base < a.rows) {
     const uint32_t r = base + slot;
     const float mean = nmean, rstd = nrstd;
-    float g[NV][8], n[NV][8];
-    Raw8<DT> hh[NV];
+    float g[NV][kUnit<DT>], n[NV][kUnit<DT>];
+    u32x4 hh[NV];
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const uint32_t c = column_of(lane, LANES, k);
-      settle<DT>(ny[k], r < a.rows ? c : a.size, a.size);
-      settle<DT>(nx[k], c, a.size);
-      unpack<DT>(ny[k], g[k]);
-      unpack<DT>(nx[k], n[k]);
-      if constexpr (RES) {
-        settle<DT>(nh[k], c, a.size);
+      settle<DT, LANES, SURE>(ny[k], lane, k, a.size);
+      if (r >= a.rows) ny[k] = u32x4{0u, 0u, 0u, 0u};
+      settle<DT, LANES, SURE>(nx[k], lane, k, a.size);
+      unpack_unit<DT>(ny[k], g[k]);
+      unpack_unit<DT>(nx[k], n[k]);
+      if constexpr (RES && !kLate) {
+        settle<DT, LANES, SURE>(nh[k], lane, k, a.size);
         hh[k] = nh[k];
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) n[k][j] = (n[k][j] - mean) * rstd;
-      float wk[8];
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) n[k][j] = (n[k][j] - mean) * rstd;
+      float wk[kUnit<DT>];
       if constexpr (kLong) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          f32x4 t = own[(2 * k + i) * kBwdThreads], u = own[(2 * NV + 2 * k + i) * kBwdThreads];
+        for (uint32_t i = 0; i < kQuads; ++i) {
+          f32x4 t = own[(k * kQuads + i) * kBwdThreads], u = own[((NV + k) * kQuads + i) * kBwdThreads];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             t[j] = __builtin_fmaf(g[k][4 * i + j], n[k][4 * i + j], t[j]);
             u[j] += g[k][4 * i + j];
           }
-          own[(2 * k + i) * kBwdThreads] = t;
-          own[(2 * NV + 2 * k + i) * kBwdThreads] = u;
+          own[(k * kQuads + i) * kBwdThreads] = t;
+          own[((NV + k) * kQuads + i) * kBwdThreads] = u;
         }
-        weight_columns<DT>(a.weight, a.wdt, c, a.size, 1.0f, wk);
+        weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, wk);
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) {
           dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
           db[k][j] += g[k][j];
           wk[j] = w[k][j];
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) {
         g[k][j] *= wk[j];
         s1 += g[k][j];
         s2 = __builtin_fmaf(g[k][j], n[k][j], s2);
+      }
+    }
+    if constexpr (RES && kLate) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        hh[k] = a.dh.at ? load_columns<DT, LANES, SURE, STREAMED>(a.dh.at + r * a.dh.ld, lane, k, a.size)
+                        : u32x4{0u, 0u, 0u, 0u};
       }
     }
     const uint32_t next = base + gridDim.x * kRows;
@@ -144,20 +153,21 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
     if (r < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const uint32_t c = column_of(lane, LANES, k);
-        float v[8];
+        const uint32_t c = column_of<DT>(lane, LANES, k);
+        float v[kUnit<DT>];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = rstd * (g[k][j] - c1 - n[k][j] * c2);
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = rstd * (g[k][j] - c1 - n[k][j] * c2);
         if constexpr (RES) {
-          float q[8];
-          unpack<DT>(hh[k], q);
+          float q[kUnit<DT>];
+          if constexpr (kLate) settle<DT, LANES, SURE>(hh[k], lane, k, a.size);
+          unpack_unit<DT>(hh[k], q);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] += q[j];
+          for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] += q[j];
         }
-        store_columns<DT, kNtStore<DT, STREAMED>>(a.dres.at + r * a.dres.ld, c, a.size, pack<DT>(v));
+        store_columns<DT, LANES, SURE, !STREAMED>(a.dres.at + r * a.dres.ld, lane, k, a.size, pack_unit<DT>(v));
         if constexpr (DROP) {
-          drop_group(d, step, r, c / kGroup, v);
-          store_columns<DT, kNtStore<DT, STREAMED>>(a.dx.at + r * a.dx.ld, c, a.size, pack<DT>(v));
+          drop_unit<DT>(d, step, r, c, v);
+          store_columns<DT, LANES, SURE, !STREAMED>(a.dx.at + r * a.dx.ld, lane, k, a.size, pack_unit<DT>(v));
         }
       }
     }
@@ -170,11 +180,11 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
   for (uint32_t which = 0; which < 2; ++which) {
     if constexpr (kLong) {
 #pragma unroll
-      for (int k = 0; k < 2 * NV; ++k) {
-        const f32x4 t = own[(which * 2 * NV + k) * kBwdThreads];
+      for (uint32_t k = 0; k < NV * kQuads; ++k) {
+        const f32x4 t = own[(which * NV * kQuads + k) * kBwdThreads];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t c = column_of(lane, LANES, k / 2) + k % 2 * 4 + j;
+          const uint32_t c = column_of<DT>(lane, LANES, k / kQuads) + k % kQuads * 4 + j;
           if (c < a.size) {
             if (a.parts == 1) store_weight_grad<DT>(a, which, c, t[j]);
             else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t[j];
@@ -183,16 +193,16 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
       }
       continue;
     }
-    float(&v)[kLong ? 1 : NV][8] = which ? db : dw;
+    float(&v)[kLong ? 1 : NV][kUnit<DT>] = which ? db : dw;
     if constexpr (kMeet > 1 && !kLong) {
       const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) {
           const float t = across_rows<LANES>(v[k][j]);
-          if (LANES >= 64 || threadIdx.x % 64 < LANES) sums[row * kCols + column_of(lane, LANES, k) + j] = t;
+          if (LANES >= 64 || threadIdx.x % 64 < LANES) sums[row * kCols + column_of<DT>(lane, LANES, k) + j] = t;
         }
       }
       __syncthreads();
@@ -207,8 +217,8 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV)) void k_norm_rows_grad(BwdAr
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t c = column_of(lane, LANES, k) + j;
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+          const uint32_t c = column_of<DT>(lane, LANES, k) + j;
           if (c < a.size) {
             if (a.parts == 1) store_weight_grad<DT>(a, which, c, v[k][j]);
             else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = v[k][j];
@@ -249,17 +259,16 @@ hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int DT, int LANES, int NV, bool STREAMED>
+template <int DT, int LANES, int NV, int SURE, bool STREAMED>
 hipError_t backward_shape(BwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
-  const uint32_t threads = bwd_threads(LANES, NV), at_once = threads / LANES;
-  a.parts = (a.rows - 1) / at_once + 1 < kBwdParts ? (a.rows - 1) / at_once + 1 : kBwdParts;
-  const dim3 grid(a.parts), block(threads);
+  a.parts = bwd_parts<DT>(a.rows, a.size);
+  const dim3 grid(a.parts), block(bwd_threads(LANES, NV * kUnit<DT>));
   if (!residual)
-    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, SURE, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else if (!drop)
-    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, SURE, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else
-    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, true, true, STREAMED>), grid, block, 0, st, a, *drop);
+    hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, SURE, true, true, STREAMED>), grid, block, 0, st, a, *drop);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.parts == 1 || (!a.dweight && !a.dbias)) return e;
   return join_weight_grads<DT>(a, st);
@@ -267,17 +276,17 @@ hipError_t backward_shape(BwdArgs a, bool residual, const DropArgs* drop, hipStr
 
 template <int DT, int I = 0>
 hipError_t backward_of(int shape, const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  if constexpr (I + 1 < (int)(sizeof(kBwdShapes) / sizeof(kBwdShapes[0]))) {
+  if constexpr (I + 1 < (int)(sizeof(kBwdShapes<DT>) / sizeof(RowShape))) {
     if (shape != I) return backward_of<DT, I + 1>(shape, a, residual, drop, st);
   }
-  constexpr RowShape s = kBwdShapes[I];
-  return a.streamed ? backward_shape<DT, s.lanes, s.groups, true>(a, residual, drop, st)
-                    : backward_shape<DT, s.lanes, s.groups, false>(a, residual, drop, st);
+  constexpr RowShape s = kBwdShapes<DT>[I];
+  return a.streamed ? backward_shape<DT, s.lanes, s.units, sure_units(kBwdShapes<DT>, I), true>(a, residual, drop, st)
+                    : backward_shape<DT, s.lanes, s.units, sure_units(kBwdShapes<DT>, I), false>(a, residual, drop, st);
 }
 
 template <int DT>
 hipError_t backward_rows(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  return backward_of<DT>(row_shape_of(kBwdShapes, a.size), a, residual, drop, st);
+  return backward_of<DT>(row_shape_of(kBwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }
 
 }  // namespace gclip

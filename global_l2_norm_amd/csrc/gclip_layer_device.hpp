@@ -119,6 +119,20 @@ __device__ __forceinline__ void store8(uint64_t a, const Raw8<DT>& r) {
   }
 }
 
+// 128 bits moved down by sh (16 to 112) places, zeros after them.
+__device__ __forceinline__ u32x4 shifted128(const u32x4& q, uint32_t sh) {
+  uint64_t lo = (uint64_t)q[0] | ((uint64_t)q[1] << 32);
+  uint64_t hi = (uint64_t)q[2] | ((uint64_t)q[3] << 32);
+  if (sh >= 64) {
+    lo = hi >> (sh - 64);
+    hi = 0;
+  } else {
+    lo = (lo >> sh) | (hi << (64 - sh));
+    hi >>= sh;
+  }
+  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // The elements of r moved down by n (1 to 7) places, zeros after them.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> shifted_down(const Raw8<DT>& s, uint32_t n) {
@@ -137,17 +151,7 @@ __device__ __forceinline__ Raw8<DT> shifted_down(const Raw8<DT>& s, uint32_t n) 
 #pragma unroll
     for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
   } else {
-    uint64_t lo = (uint64_t)s.q[0][0] | ((uint64_t)s.q[0][1] << 32);
-    uint64_t hi = (uint64_t)s.q[0][2] | ((uint64_t)s.q[0][3] << 32);
-    const uint32_t sh = 16u * n;  // 16 to 112 bits
-    if (sh >= 64) {
-      lo = hi >> (sh - 64);
-      hi = 0;
-    } else {
-      lo = (lo >> sh) | (hi << (64 - sh));
-      hi >>= sh;
-    }
-    r.q[0] = u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+    r.q[0] = shifted128(s.q[0], 16u * n);
   }
   return r;
 }
@@ -216,12 +220,16 @@ __device__ __forceinline__ void store_group8(uint64_t row, uint32_t g, uint32_t 
   else if (c < size) store_tail<DT>(row + (uint64_t)c * kElem<DT>, r, size - c);
 }
 
-// Unit u, 16 bytes, of a row: a group, or half of one of binary32.
+// Columns of a unit of 16 bytes: a group, or half of one of binary32.
+template <int DT>
+constexpr uint32_t kUnit = DT == GCLIP_F32 ? 4u : 8u;
+
+// Unit u of a row: zeros past its end.
 template <int DT, bool NT>
 __device__ __forceinline__ u32x4 load_unit(uint64_t row, uint32_t u, uint32_t size) {
   if constexpr (DT == GCLIP_F32) {
     typedef __attribute__((address_space(1))) u32x4_any4 g_t;
-    const uint32_t c = u * 4;
+    const uint32_t c = u * kUnit<DT>;
     if (c + 4 <= size) {
       const g_t* p = reinterpret_cast<const g_t*>(row + c * 4ull);
       return NT ? __builtin_nontemporal_load(p) : *p;
@@ -310,56 +318,130 @@ __device__ __forceinline__ void drop_group(const DropArgs& d, uint32_t step, uin
   }
 }
 
+template <int DT>
+__device__ __forceinline__ void drop_unit(const DropArgs& d, uint32_t step, uint32_t row, uint32_t c,
+                                          float (&v)[kUnit<DT>]) {
+#pragma clang fp contract(off)
+  if constexpr (DT == GCLIP_F32) {
+    const uint64_t b = philox_half(d, step, row, c / kGroup, c & 4u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = (uint32_t)(b >> (16 * j)) & 0xffffu;
+      v[j] = u >= d.threshold ? v[j] * d.scale : 0.0f;
+    }
+  } else {
+    drop_group(d, step, row, c / kGroup, v);
+  }
+}
+
 // ---------------------------------------------------------------- rows in registers
-// A row of 8 to LANES * NV * 8 columns is held by LANES lanes, NV groups
-// each: lane l takes the groups l, l + LANES, ...  Loads are unconditional --
-// a lane whose group passes the row's end reads the row's last eight elements
-// instead -- and settled afterwards: shifted where the group is the row's
-// ragged end, zero past it.  So a row's loads are all under way before
-// anything is waited for, and none leaves the row.
+// A row of at least eight columns is held by LANES lanes, NV units of 16
+// bytes each: lane l takes the units l, l + LANES, ..., so a wave's accesses
+// are adjacent.  Loads are unconditional -- a lane whose unit passes the
+// row's end reads the row's last 16 bytes instead -- and settled afterwards:
+// shifted where the unit is the row's ragged end, zero past it.  So a row's
+// loads are all under way before anything is waited for, and none leaves the
+// row.
+template <int DT>
 __device__ __forceinline__ uint32_t column_of(uint32_t lane, uint32_t lanes, int k) {
-  return (lane + (uint32_t)k * lanes) * kGroup;
-}
-
-template <int DT, bool NT>
-__device__ __forceinline__ Raw8<DT> load_clamped(uint64_t row, uint32_t c, uint32_t size) {
-  const uint32_t o = c + kGroup <= size ? c : size - kGroup;
-  return load8<DT, NT>(row + o * kElem<DT>);
+  return (lane + (uint32_t)k * lanes) * kUnit<DT>;
 }
 
 template <int DT>
-__device__ __forceinline__ void settle(Raw8<DT>& r, uint32_t c, uint32_t size) {
-  if (c + kGroup > size) r = c < size ? shifted_down<DT>(r, c + kGroup - size) : zero8<DT>();
+__device__ __forceinline__ void unpack_unit(const u32x4& q, float (&v)[kUnit<DT>]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == GCLIP_F32) {
+      v[k] = __uint_as_float(q[k]);
+    } else {
+      v[2 * k] = elem_float<DT>(q[k] & 0xffffu);
+      v[2 * k + 1] = elem_float<DT>(q[k] >> 16);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 pack_unit(const float (&v)[kUnit<DT>]) {
+  u32x4 q;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == GCLIP_F32) q[k] = __float_as_uint(v[k]);
+    else q[k] = elem_bits<DT>(v[2 * k]) | (elem_bits<DT>(v[2 * k + 1]) << 16);
+  }
+  return q;
 }
 
 template <int DT, bool NT>
-__device__ __forceinline__ void store_columns(uint64_t row, uint32_t c, uint32_t size, const Raw8<DT>& r) {
-  if (c + kGroup <= size) store8<DT, NT>(row + c * kElem<DT>, r);
-  else if (c < size) store_tail<DT>(row + c * kElem<DT>, r, size - c);
+__device__ __forceinline__ u32x4 load16(uint64_t at) {
+  if constexpr (DT == GCLIP_F32) {
+    typedef __attribute__((address_space(1))) u32x4_any4 g_t;
+    const g_t* p = reinterpret_cast<const g_t*>(at);
+    return NT ? __builtin_nontemporal_load(p) : *p;
+  } else {
+    typedef __attribute__((address_space(1))) u32x4_any2 g_t;
+    const g_t* p = reinterpret_cast<const g_t*>(at);
+    return NT ? __builtin_nontemporal_load(p) : *p;
+  }
 }
 
-// A streamed call's loads are nontemporal and its stores ordinary; another's
-// the other way round (but for binary32 rows, which are stored in two
-// instructions that interleave, whose halves of a line have to meet in a
-// cache).  See kStreamBytes.
-template <int DT, bool STREAMED>
-constexpr bool kNtStore = !STREAMED && DT != GCLIP_F32;
+template <int DT, bool NT>
+__device__ __forceinline__ void store16(uint64_t at, const u32x4& q) {
+  if constexpr (DT == GCLIP_F32) {
+    typedef __attribute__((address_space(1))) u32x4_any4 g_t;
+    g_t* p = reinterpret_cast<g_t*>(at);
+    if constexpr (NT) __builtin_nontemporal_store(q, p);
+    else *p = q;
+  } else {
+    typedef __attribute__((address_space(1))) u32x4_any2 g_t;
+    g_t* p = reinterpret_cast<g_t*>(at);
+    if constexpr (NT) __builtin_nontemporal_store(q, p);
+    else *p = q;
+  }
+}
 
-// Eight elements of weight or bias, as settle() leaves a row's.
-template <int DT>
-__device__ __forceinline__ void weight_columns(uint64_t w, int wdt, uint32_t c, uint32_t size, float def,
-                                               float (&v)[8]) {
+// The units k < SURE lie in every row that a shape is used for (the shape
+// before it would hold the others): nothing is clamped or settled there.
+template <int DT, int LANES, int SURE, bool NT>
+__device__ __forceinline__ u32x4 load_columns(uint64_t row, uint32_t lane, int k, uint32_t size) {
+  if (k < SURE) return load16<DT, NT>(row + (uint64_t)(k * LANES * 16) + lane * 16u);
+  const uint32_t c = column_of<DT>(lane, LANES, k);
+  return load16<DT, NT>(row + (c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>);
+}
+
+template <int DT, int LANES, int SURE>
+__device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t size) {
+  if (k < SURE) return;
+  const uint32_t c = column_of<DT>(lane, LANES, k);
+  if (c + kUnit<DT> > size)
+    q = c < size ? shifted128(q, 8u * kElem<DT> * (c + kUnit<DT> - size)) : u32x4{0u, 0u, 0u, 0u};
+}
+
+template <int DT, int LANES, int SURE, bool NT>
+__device__ __forceinline__ void store_columns(uint64_t row, uint32_t lane, int k, uint32_t size, const u32x4& q) {
+  const uint32_t c = column_of<DT>(lane, LANES, k);
+  if (k < SURE) store16<DT, NT>(row + (uint64_t)(k * LANES * 16) + lane * 16u, q);
+  else if (c < size) store_unit<DT, NT>(row, c / kUnit<DT>, size, q);
+}
+
+// The columns of unit k of weight or bias as settle() leaves a row's.
+template <int DT, int LANES, int SURE>
+__device__ __forceinline__ void weight_columns(uint64_t w, int wdt, uint32_t lane, int k, uint32_t size, float def,
+                                               float (&v)[kUnit<DT>]) {
   if (w == 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = def;
-  } else if (DT == GCLIP_F32 || wdt == GCLIP_F32) {
-    Raw8<GCLIP_F32> r = load_clamped<GCLIP_F32, false>(w, c, size);
-    settle<GCLIP_F32>(r, c, size);
-    unpack<GCLIP_F32>(r, v);
+    for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = def;
+  } else if (DT != GCLIP_F32 && wdt == GCLIP_F32) {
+    if constexpr (DT != GCLIP_F32) {
+      const uint32_t c = column_of<DT>(lane, LANES, k);
+      Raw8<GCLIP_F32> r = load8<GCLIP_F32, false>(w + (k < SURE || c + kGroup <= size ? c : size - kGroup) * 4ull);
+      if (k >= SURE && c + kGroup > size)
+        r = c < size ? shifted_down<GCLIP_F32>(r, c + kGroup - size) : zero8<GCLIP_F32>();
+      unpack<GCLIP_F32>(r, v);
+    }
   } else {
-    Raw8<DT> r = load_clamped<DT, false>(w, c, size);
-    settle<DT>(r, c, size);
-    unpack<DT>(r, v);
+    u32x4 q = load_columns<DT, LANES, SURE, false>(w, lane, k, size);
+    settle<DT, LANES, SURE>(q, lane, k, size);
+    unpack_unit<DT>(q, v);
   }
 }
 

@@ -23,7 +23,7 @@ constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
 // lanes, where its mean, its squared deviations from it and y are taken from
 // them in turn.  While a row is worked on, the loads of the workgroup's next
 // one are under way; weight and bias stay in registers.
-template <int DT, int LANES, int NV, bool RES, bool DROP, bool STREAMED>
+template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
   constexpr int kThreads = kFwdThreads<LANES>;
   const uint32_t at_once = LANES > 64 ? kThreads / LANES : blockDim.x / LANES;  // rows of a workgroup
@@ -33,7 +33,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
   const uint32_t step = DROP ? drop_step(d) : 0u;
 
-  Raw8<DT> nx[NV], nr[NV];
+  u32x4 nx[NV], nr[NV];
   uint32_t base = blockIdx.x * at_once;
   const auto fetch = [&](uint32_t first) {
     // rows past the end are read as the last one, and not written
@@ -41,37 +41,37 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
     const uint64_t x = a.x.at + r * a.x.ld, q = a.residual.at + r * a.residual.ld;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      nx[k] = load_clamped<DT, STREAMED>(x, column_of(lane, LANES, k), a.size);
-      if constexpr (RES) nr[k] = load_clamped<DT, STREAMED>(q, column_of(lane, LANES, k), a.size);
+      nx[k] = load_columns<DT, LANES, SURE, STREAMED>(x, lane, k, a.size);
+      if constexpr (RES) nr[k] = load_columns<DT, LANES, SURE, STREAMED>(q, lane, k, a.size);
     }
   };
   fetch(base);
-  float w[NV][8], b[NV][8];
+  float w[NV][kUnit<DT>], b[NV][kUnit<DT>];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    weight_columns<DT>(a.weight, a.wdt, column_of(lane, LANES, k), a.size, 1.0f, w[k]);
-    weight_columns<DT>(a.bias, a.wdt, column_of(lane, LANES, k), a.size, 0.0f, b[k]);
+    weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
+    weight_columns<DT, LANES, SURE>(a.bias, a.wdt, lane, k, a.size, 0.0f, b[k]);
   }
   const float count = (float)a.size;
 
   while (base < a.rows) {
     const uint32_t r = base + slot;
-    float v[NV][8];
-    Raw8<DT> o[NV];
+    float v[NV][kUnit<DT>];
+    u32x4 o[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const uint32_t c = column_of(lane, LANES, k);
-      settle<DT>(nx[k], c, a.size);
-      unpack<DT>(nx[k], v[k]);
+      const uint32_t c = column_of<DT>(lane, LANES, k);
+      settle<DT, LANES, SURE>(nx[k], lane, k, a.size);
+      unpack_unit<DT>(nx[k], v[k]);
       if constexpr (RES) {
-        float q[8];
-        settle<DT>(nr[k], c, a.size);
-        unpack<DT>(nr[k], q);
-        if constexpr (DROP) drop_group(d, step, r, c / kGroup, v[k]);
+        float q[kUnit<DT>];
+        settle<DT, LANES, SURE>(nr[k], lane, k, a.size);
+        unpack_unit<DT>(nr[k], q);
+        if constexpr (DROP) drop_unit<DT>(d, step, r, c, v[k]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] += q[j];
-        o[k] = pack<DT>(v[k]);
-        unpack<DT>(o[k], v[k]);
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[k][j] += q[j];
+        o[k] = pack_unit<DT>(v[k]);
+        unpack_unit<DT>(o[k], v[k]);
       }
     }
     const uint32_t next = base + gridDim.x * at_once;
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
       if (r < a.rows) {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-          store_columns<DT, kNtStore<DT, STREAMED>>(a.h.at + r * a.h.ld, column_of(lane, LANES, k), a.size, o[k]);
+          store_columns<DT, LANES, SURE, !STREAMED>(a.h.at + r * a.h.ld, lane, k, a.size, o[k]);
       }
     }
 
@@ -93,25 +93,25 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s = __builtin_fmaf(v[k][j], scale, s);
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) s = __builtin_fmaf(v[k][j], scale, s);
       mean = row_sum<LANES>(s, red[0]) / count;  // exact for a constant row
       s = 0.0f;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const uint32_t c = column_of(lane, LANES, k);
-        if (c + kGroup <= a.size) {
+        const uint32_t c = column_of<DT>(lane, LANES, k);
+        if (k < SURE || c + kUnit<DT> <= a.size) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (uint32_t j = 0; j < kUnit<DT>; ++j) {
             const float t = __builtin_fmaf(v[k][j], scale, -mean);
             s = __builtin_fmaf(t, t, s);
           }
         } else {
           uint32_t left = c < a.size ? a.size - c : 0u;
-          // recomputed for each row: the eight conditions would else be kept
+          // recomputed for each row: the conditions would else be kept
           // in scalar registers over the loop, more than there are
           asm volatile("" : "+v"(left));
 #pragma unroll
-          for (uint32_t j = 0; j < 8; ++j) {
+          for (uint32_t j = 0; j < kUnit<DT>; ++j) {
             const float t = j < left ? __builtin_fmaf(v[k][j], scale, -mean) : 0.0f;
             s = __builtin_fmaf(t, t, s);
           }
@@ -132,8 +132,8 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[k][j] = __builtin_fmaf((v[k][j] - mean) * rstd, w[k][j], b[k][j]);
-        store_columns<DT, kNtStore<DT, STREAMED>>(a.y.at + r * a.y.ld, column_of(lane, LANES, k), a.size, pack<DT>(v[k]));
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[k][j] = __builtin_fmaf((v[k][j] - mean) * rstd, w[k][j], b[k][j]);
+        store_columns<DT, LANES, SURE, !STREAMED>(a.y.at + r * a.y.ld, lane, k, a.size, pack_unit<DT>(v[k]));
       }
       if (a.mean && lane == 0) {
         a.mean[r] = mean;
@@ -144,46 +144,46 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
   }
 }
 
-template <int DT, int LANES, int NV, bool STREAMED>
+template <int DT, int LANES, int NV, int SURE, bool STREAMED>
 hipError_t forward_shape(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   // workgroups of a wave until there are four for each compute unit
   const uint32_t threads = LANES <= 64 && a.rows < 1024 * (64 / LANES) ? 64 : kFwdThreads<LANES>;
   const uint32_t at_once = threads / LANES;
-  const uint32_t most = 256u * (NV == 1 ? GCLIP_FWD_WGS1 : GCLIP_FWD_WGS) * 256 / threads;
+  const uint32_t most = 256u * (NV * kUnit<DT> <= 8 ? GCLIP_FWD_WGS1 : GCLIP_FWD_WGS) * 256 / threads;
   const uint32_t need = (a.rows + at_once - 1) / at_once;
   const dim3 grid(need < most ? need : most), block(threads);
   if (!residual)
-    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, SURE, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else if (!drop)
-    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, SURE, true, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else
-    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, true, true, STREAMED>), grid, block, 0, st, a, *drop);
+    hipLaunchKernelGGL((k_norm_rows<DT, LANES, NV, SURE, true, true, STREAMED>), grid, block, 0, st, a, *drop);
   return hipGetLastError();
 }
 
 template <int DT, int I = 0>
 hipError_t forward_of(int shape, const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  if constexpr (I + 1 < (int)(sizeof(kFwdShapes) / sizeof(kFwdShapes[0]))) {
+  if constexpr (I + 1 < (int)(sizeof(kFwdShapes<DT>) / sizeof(RowShape))) {
     if (shape != I) return forward_of<DT, I + 1>(shape, a, residual, drop, st);
   }
-  constexpr RowShape s = kFwdShapes[I];
-  return a.streamed ? forward_shape<DT, s.lanes, s.groups, true>(a, residual, drop, st)
-                    : forward_shape<DT, s.lanes, s.groups, false>(a, residual, drop, st);
+  constexpr RowShape s = kFwdShapes<DT>[I];
+  return a.streamed ? forward_shape<DT, s.lanes, s.units, sure_units(kFwdShapes<DT>, I), true>(a, residual, drop, st)
+                    : forward_shape<DT, s.lanes, s.units, sure_units(kFwdShapes<DT>, I), false>(a, residual, drop, st);
 }
 
 template <int DT, int I = 0>
 hipError_t forward_few(int shape, const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  if constexpr (I + 1 < (int)(sizeof(kFewShapes) / sizeof(kFewShapes[0]))) {
+  if constexpr (I + 1 < (int)(sizeof(kFewShapes<DT>) / sizeof(RowShape))) {
     if (shape != I) return forward_few<DT, I + 1>(shape, a, residual, drop, st);
   }
-  return forward_shape<DT, kFewShapes[I].lanes, kFewShapes[I].groups, false>(a, residual, drop, st);
+  return forward_shape<DT, kFewShapes<DT>[I].lanes, kFewShapes<DT>[I].units, sure_units(kFewShapes<DT>, I), false>(a, residual, drop, st);
 }
 
 template <int DT>
 hipError_t forward_rows(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   static_assert(GCLIP_STREAM_MB < 100 || (uint64_t)kFewRows * kRegistersMax * 4 * 4 <= kStreamBytes, "few rows are not streamed");
-  if (a.rows <= kFewRows) return forward_few<DT>(row_shape_of(kFewShapes, a.size), a, residual, drop, st);
-  return forward_of<DT>(row_shape_of(kFwdShapes, a.size), a, residual, drop, st);
+  if (a.rows <= kFewRows) return forward_few<DT>(row_shape_of(kFewShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
+  return forward_of<DT>(row_shape_of(kFwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }
 
 }  // namespace gclip
