@@ -65,7 +65,7 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
       for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = db[k][j] = 0.0f;
     }
   }
-  const float count = (float)a.size;
+  const float count = (float)a.size, inverse = 1.0f / count;
   uint32_t turn = 0;
 
   while (base < a.rows) {
@@ -77,8 +77,8 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       settle<DT, LANES, SURE>(ny[k], lane, k, a.size);
-      if (r >= a.rows) ny[k] = u32x4{0u, 0u, 0u, 0u};
       settle<DT, LANES, SURE>(nx[k], lane, k, a.size);
+      if (r >= a.rows) ny[k] = nx[k] = u32x4{0u, 0u, 0u, 0u};
       unpack_unit<DT>(ny[k], g[k]);
       unpack_unit<DT>(nx[k], n[k]);
       if constexpr (RES && !kLate) {
@@ -148,8 +148,8 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
       c1 = lanes_sum<LANES>(s1);
       c2 = lanes_sum<LANES>(s2);
     }
-    c1 /= count;  // exact for constant gradients
-    c2 /= count;
+    c1 = divided(c1, count, inverse);
+    c2 = divided(c2, count, inverse);
     if (r < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {

@@ -119,39 +119,34 @@ __device__ __forceinline__ void store8(uint64_t a, const Raw8<DT>& r) {
   }
 }
 
-// 128 bits moved down by sh (16 to 112) places, zeros after them.
-__device__ __forceinline__ u32x4 shifted128(const u32x4& q, uint32_t sh) {
-  uint64_t lo = (uint64_t)q[0] | ((uint64_t)q[1] << 32);
-  uint64_t hi = (uint64_t)q[2] | ((uint64_t)q[3] << 32);
-  if (sh >= 64) {
-    lo = hi >> (sh - 64);
-    hi = 0;
-  } else {
-    lo = (lo >> sh) | (hi << (64 - sh));
-    hi >>= sh;
-  }
-  return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+// The elements of 16 or 32 bytes moved down by n places, zeros after them.
+// n is the same in every lane (what a row's ragged end lacks), and moves by
+// words and half words: a 64-bit shift by a vector register gave wrong bits
+// on gfx950 when that register was the last one of the wave's allocation.
+template <int DT>
+__device__ __forceinline__ u32x4 moved_down(u32x4 q, uint32_t n) {
+  const uint32_t bits = __builtin_amdgcn_readfirstlane(n * 8u * kElem<DT>);
+  if (bits & 64u) q = u32x4{q[2], q[3], 0u, 0u};
+  if (bits & 32u) q = u32x4{q[1], q[2], q[3], 0u};
+  if (DT != GCLIP_F32 && (bits & 16u))
+    q = u32x4{(q[0] >> 16) | (q[1] << 16), (q[1] >> 16) | (q[2] << 16), (q[2] >> 16) | (q[3] << 16), q[3] >> 16};
+  return q;
 }
 
-// The elements of r moved down by n (1 to 7) places, zeros after them.
 template <int DT>
-__device__ __forceinline__ Raw8<DT> shifted_down(const Raw8<DT>& s, uint32_t n) {
-  Raw8<DT> r;
+__device__ __forceinline__ Raw8<DT> moved_down(Raw8<DT> r, uint32_t n) {
   if constexpr (DT == GCLIP_F32) {
-    uint32_t v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = s.q[k >> 2][k & 3];
-#pragma unroll
-    for (uint32_t b = 4; b > 0; b >>= 1) {
-      if (n & b) {
-#pragma unroll
-        for (uint32_t k = 0; k < 8; ++k) v[k] = k + b < 8 ? v[k + b < 8 ? k + b : 0] : 0u;
-      }
+    if (__builtin_amdgcn_readfirstlane(n) & 4u) {
+      r.q[0] = r.q[1];
+      r.q[1] = u32x4{0u, 0u, 0u, 0u};
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = v[k];
+    const uint32_t by = __builtin_amdgcn_readfirstlane(n) & 3u;
+    const uint32_t v[8] = {r.q[0][0], r.q[0][1], r.q[0][2], r.q[0][3], r.q[1][0], r.q[1][1], r.q[1][2], r.q[1][3]};
+    if (by == 1) r = Raw8<DT>{{u32x4{v[1], v[2], v[3], v[4]}, u32x4{v[5], v[6], v[7], 0u}}};
+    if (by == 2) r = Raw8<DT>{{u32x4{v[2], v[3], v[4], v[5]}, u32x4{v[6], v[7], 0u, 0u}}};
+    if (by == 3) r = Raw8<DT>{{u32x4{v[3], v[4], v[5], v[6]}, u32x4{v[7], 0u, 0u, 0u}}};
   } else {
-    r.q[0] = shifted128(s.q[0], 16u * n);
+    r.q[0] = moved_down<DT>(r.q[0], n);
   }
   return r;
 }
@@ -162,7 +157,7 @@ __device__ __forceinline__ Raw8<DT> shifted_down(const Raw8<DT>& s, uint32_t n) 
 // one by one.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load_tail(uint64_t a, uint32_t n, bool front) {
-  if (front) return shifted_down<DT>(load8<DT, false>(a - (uint64_t)(kGroup - n) * kElem<DT>), kGroup - n);
+  if (front) return moved_down<DT>(load8<DT, false>(a - (uint64_t)(kGroup - n) * kElem<DT>), kGroup - n);
   Raw8<DT> r = zero8<DT>();
 #pragma unroll
   for (uint32_t k = 0; k < 7; ++k) {
@@ -413,7 +408,7 @@ __device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t 
   if (k < SURE) return;
   const uint32_t c = column_of<DT>(lane, LANES, k);
   if (c + kUnit<DT> > size)
-    q = c < size ? shifted128(q, 8u * kElem<DT> * (c + kUnit<DT> - size)) : u32x4{0u, 0u, 0u, 0u};
+    q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
 }
 
 template <int DT, int LANES, int SURE, bool NT>
@@ -435,7 +430,7 @@ __device__ __forceinline__ void weight_columns(uint64_t w, int wdt, uint32_t lan
       const uint32_t c = column_of<DT>(lane, LANES, k);
       Raw8<GCLIP_F32> r = load8<GCLIP_F32, false>(w + (k < SURE || c + kGroup <= size ? c : size - kGroup) * 4ull);
       if (k >= SURE && c + kGroup > size)
-        r = c < size ? shifted_down<GCLIP_F32>(r, c + kGroup - size) : zero8<GCLIP_F32>();
+        r = c < size ? moved_down<GCLIP_F32>(r, kGroup - size % kGroup) : zero8<GCLIP_F32>();
       unpack<GCLIP_F32>(r, v);
     }
   } else {
@@ -487,6 +482,13 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     for (int i = 1; i < kWavesOfRow; ++i) v += own[i];
   }
   return v;
+}
+
+// t / n by n's reciprocal and one correction, exact where n divides t (a
+// constant row's mean is its value), in a quarter of a division's operations.
+__device__ __forceinline__ float divided(float t, float n, float inverse) {
+  const float q = t * inverse;
+  return __builtin_fmaf(__builtin_fmaf(-q, n, t), inverse, q);
 }
 
 // Sum over the lanes of a wave that hold the same column of its 64 / LANES rows.

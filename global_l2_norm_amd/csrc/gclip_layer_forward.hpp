@@ -52,7 +52,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
     weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
     weight_columns<DT, LANES, SURE>(a.bias, a.wdt, lane, k, a.size, 0.0f, b[k]);
   }
-  const float count = (float)a.size;
+  const float count = (float)a.size, inverse = 1.0f / count;
 
   while (base < a.rows) {
     const uint32_t r = base + slot;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (uint32_t j = 0; j < kUnit<DT>; ++j) s = __builtin_fmaf(v[k][j], scale, s);
-      mean = row_sum<LANES>(s, red[0]) / count;  // exact for a constant row
+      mean = divided(row_sum<LANES>(s, red[0]), count, inverse);
       s = 0.0f;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
           }
         }
       }
-      var = row_sum<LANES>(s, red[1]) / count;
+      var = divided(row_sum<LANES>(s, red[1]), count, inverse);
       const bool over = !(var <= 0x1.fffffep+127f) && scale == 1.0f;
       if (!(LANES > 64 ? over : __any(over))) break;
       if (over) scale = 0x1p-96f;

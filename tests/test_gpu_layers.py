@@ -107,6 +107,15 @@ def test_every_number_of_rows(rows, size, dtype):
     run_all(rows, size, dtype, "f32", "plain" if rows % 2 else "padded", seed=1)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [64, 128, 256, 512, 768, 1024, 1536, 2048, 4096, 6144, 8192, 12288])
+def test_ragged_ends_in_every_wave(shape, dtype):
+    """Rows that a few columns make too long for a register shape: the end of
+    each lies alone in a unit, in every wave of a workgroup."""
+    for extra in (1, 3, 6):
+        run_all(37, shape + extra, dtype, "f32", "padded", seed=6)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_short_rows(dtype):
     run_all(150001, 9, dtype, "f32", "plain", seed=2)
@@ -533,3 +542,20 @@ def test_bad_tensors_are_refused():
         with pytest.raises(error):
             call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_the_example_learns(dtype):
+    """examples/residual_lm.py: the loss of a uniform guess falls by more than
+    half."""
+    import importlib.util
+    import os
+
+    import torch
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "residual_lm.py")
+    spec = importlib.util.spec_from_file_location("residual_lm", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    losses, norms = mod.train(steps=60, dtype=getattr(torch, dtype))
+    assert abs(losses[0] - np.log(257)) < 0.5 and losses[-1] < 0.5 * losses[0], losses
+    assert all(np.isfinite(norms))
