@@ -38,17 +38,19 @@ struct BwdArgs {
   const float *mean, *rstd;
   uint64_t weight, dweight, dbias;
   float* partials;  // [parts][2][size]: sums of dy * n, then of dy
+  float* sums;      // [rows][2], long rows: their means of dy * weight and of that times n
   uint32_t rows, size;
   int32_t wdt, gdt, accumulate;
   uint32_t parts;
   int32_t streamed;  // see kStreamBytes
 };
 
-// The norms' kernels hold a row of kRegistersMin to kRegistersMax columns in
-// registers, `lanes` lanes with `units` units of 16 bytes each: the least of
-// these shapes that holds the row.  Other rows go through the kernels of
+// The norms' kernels hold a row in registers, `lanes` lanes with `units` units
+// of 16 bytes each: the least of the shapes below that holds the row.  The
+// backward kernel keeps the columns' sums there too, for rows of half the
+// length.  Shorter and longer rows go through the kernels of
 // gclip_layer_any.hip.
-constexpr uint32_t kRegistersMin = 8, kRegistersMax = 16384;
+constexpr uint32_t kRegistersMin = 8, kFwdMax = 16384, kBwdMax = 8192;
 struct RowShape {
   uint32_t lanes, units;
 };
@@ -58,26 +60,23 @@ constexpr RowShape kFwdShapes[] = {{8, 1},  {16, 1}, {32, 1},  {64, 1},  {32, 3}
 template <>
 inline constexpr RowShape kFwdShapes<GCLIP_F32>[] = {{16, 1}, {32, 1},  {64, 1},  {64, 2},  {64, 3},  {64, 4}, {64, 6},
                                                      {64, 8}, {256, 4}, {256, 6}, {256, 8}, {512, 6}, {512, 8}};
-// Few rows: more lanes each.
-#ifndef GCLIP_FEW_ROWS
-#define GCLIP_FEW_ROWS 512
-#endif
-constexpr uint32_t kFewRows = GCLIP_FEW_ROWS;
+// Few rows: more lanes each, which shortens the way from a row's loads to its
+// stores while compute units are idle anyway.  256 x 2048 in bfloat16 takes
+// 3.4 us (3.8 with a wave a row), 512 rows 3.6 (4.0), but 1024 rows 4.4 (4.3)
+// and 2048 rows 6.5 (5.8).
+constexpr uint32_t kFewRows = 512;
 template <int DT>
 constexpr RowShape kFewShapes[] = {{8, 1},   {16, 1},  {32, 1},   {64, 1},  {128, 1},
                                    {256, 1}, {512, 1}, {1024, 1}, {1024, 2}};
 template <>
 inline constexpr RowShape kFewShapes<GCLIP_F32>[] = {{16, 1},  {32, 1},  {64, 1},   {128, 1}, {256, 1},
                                                      {512, 1}, {1024, 1}, {1024, 2}, {1024, 4}};
-#ifndef GCLIP_BWD_F32
-#define GCLIP_BWD_F32 {64, 3}, {64, 4}, {128, 3}, {128, 4}
-#endif
 template <int DT>
 constexpr RowShape kBwdShapes[] = {{8, 1},   {16, 1},  {32, 1},  {64, 1},  {64, 2},
-                                   {128, 2}, {256, 2}, {512, 2}, {1024, 2}};
+                                   {128, 2}, {256, 2}, {512, 2}};
 template <>
-inline constexpr RowShape kBwdShapes<GCLIP_F32>[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, GCLIP_BWD_F32,
-                                                     {256, 4}, {512, 4}, {1024, 4}};
+inline constexpr RowShape kBwdShapes<GCLIP_F32>[] = {{16, 1},  {32, 1},  {64, 1},  {64, 2},  {64, 3},
+                                                     {64, 4}, {128, 3}, {128, 4}, {256, 4}, {512, 4}};
 template <int N>
 constexpr int row_shape_of(const RowShape (&shapes)[N], uint32_t unit, uint32_t size) {
   int i = 0;
@@ -89,29 +88,31 @@ template <int N>
 constexpr int sure_units(const RowShape (&shapes)[N], int i) {
   return i == 0 ? 0 : (int)(shapes[i - 1].lanes * shapes[i - 1].units / shapes[i].lanes);
 }
-inline bool in_registers(uint32_t size) { return size >= kRegistersMin && size <= kRegistersMax; }
+inline bool in_registers(uint32_t size, uint32_t most) { return size >= kRegistersMin && size <= most; }
 
 // Threads of a workgroup of the backward kernel: all that a compute unit's
 // registers hold, so that each unit leaves one partial sum of the weights'
 // gradients, of kBwdParts at most.
-constexpr uint32_t bwd_threads(uint32_t lanes, uint32_t columns) { return columns <= 8 || lanes > 512 ? 1024 : 512; }
+constexpr uint32_t bwd_threads(uint32_t columns) { return columns <= 8 ? 1024 : 512; }
 constexpr uint32_t kBwdParts = 256;
 template <int DT>
 inline uint32_t bwd_parts(uint32_t rows, uint32_t size) {
   const uint32_t unit = DT == GCLIP_F32 ? 4 : 8;
   const RowShape s = kBwdShapes<DT>[row_shape_of(kBwdShapes<DT>, unit, size)];
-  const uint32_t at_once = bwd_threads(s.lanes, s.units * unit) / s.lanes, need = (rows - 1) / at_once + 1;
+  const uint32_t at_once = bwd_threads(s.units * unit) / s.lanes, need = (rows - 1) / at_once + 1;
   return need < kBwdParts ? need : kBwdParts;
 }
 
 // What a call moves decides how.  Up to kStreamBytes the matrices may lie in
 // the 256 MB cache before memory, where the kernel before has left them:
-// ordinary loads find them there, and nontemporal stores leave them there.
-// Above, nontemporal loads and ordinary stores are faster.
-#ifndef GCLIP_STREAM_MB
-#define GCLIP_STREAM_MB 144
-#endif
-constexpr uint64_t kStreamBytes = (uint64_t)GCLIP_STREAM_MB << 20;
+// ordinary loads find them there, and nontemporal stores, which pass the L2
+// by, are written there.  Above, nontemporal loads and ordinary stores are
+// faster.  Measured in bfloat16 (in turn streamed, not): norm 16384 x 2048,
+// 134 MB, 26.4 and 23.4 us; residual step 8192 x 2048, 134 MB, 28.2 and 23.5;
+// norm gradient 12288 x 2048, 151 MB, 32.3 and 34.0; residual gradient
+// 8192 x 2048, 168 MB, 36.8 and 37.8; residual step 16384 x 2048, 268 MB, 46.6
+// and 49.6.
+constexpr uint64_t kStreamBytes = 144ull << 20;
 
 // The most partial sums of the weights' gradients for a matrix of this shape
 // in any format.

@@ -1,5 +1,5 @@
-// gclip_layer_any.hip -- the layer calls for rows of any length: a workgroup
-// goes through a row in passes, and through the caches again in each.
+// gclip_layer_any.hip -- the norms of rows that the kernels with rows in
+// registers do not take, shorter and longer ones, and dropout.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -12,6 +12,8 @@ namespace {
 
 constexpr int kAnyThreads = 256;
 constexpr int kAnyWaves = kAnyThreads / 64;
+constexpr int kRowThreads = 512;
+constexpr int kRowWaves = kRowThreads / 64;
 
 // Sum over the workgroup, the same bits in every thread.
 __device__ __forceinline__ double any_sum(double v, double* red) {
@@ -22,23 +24,25 @@ __device__ __forceinline__ double any_sum(double v, double* red) {
   __syncthreads();
   double t = red[0];
 #pragma unroll
-  for (int i = 1; i < kAnyWaves; ++i) t += red[i];
+  for (int i = 1; i < kRowWaves; ++i) t += red[i];
   return t;
 }
 
-// Three passes over a row: h and the sum, the squares, y.  A thread reads in
-// a later pass only the groups that it wrote itself.  The sums are binary64,
-// so no finite row overflows them.
+// Three passes over a row: h and the sum, the squares, y; the later ones find
+// the row in the caches.  A thread reads there only the groups that it wrote
+// itself.  The sums are binary64, so no finite row overflows them.  Bound by
+// the passes' latency: 512 x 40000 in bfloat16 takes 28.9 us, 2.8 TB/s of the
+// row's one read and one write (1024 lanes a row: 33.0).
 template <int DT, bool RES, bool DROP>
-__global__ __launch_bounds__(kAnyThreads) void k_norm_any(FwdArgs a, DropArgs d) {
-  __shared__ double red[kAnyWaves];
+__global__ __launch_bounds__(kRowThreads) void k_norm_any(FwdArgs a, DropArgs d) {
+  __shared__ double red[kRowWaves];
   const uint32_t groups = (a.size + kGroup - 1) / kGroup;
   const uint32_t step = DROP ? drop_step(d) : 0u;
   for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const uint64_t x = a.x.at + r * a.x.ld, y = a.y.at + r * a.y.ld;
     const uint64_t h = RES ? a.h.at + r * a.h.ld : x;
     double s = 0.0;
-    for (uint32_t g = threadIdx.x; g < groups; g += kAnyThreads) {
+    for (uint32_t g = threadIdx.x; g < groups; g += kRowThreads) {
       float v[8];
       unpack<DT>(load_group8<DT, false>(x, g, a.size), v);
       if constexpr (RES) {
@@ -56,7 +60,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_any(FwdArgs a, DropArgs d)
     }
     const double mean = any_sum(s, red) / (double)a.size;
     double ss = 0.0;
-    for (uint32_t g = threadIdx.x; g < groups; g += kAnyThreads) {
+    for (uint32_t g = threadIdx.x; g < groups; g += kRowThreads) {
       float v[8];
       unpack<DT>(load_group8<DT, false>(h, g, a.size), v);
 #pragma unroll
@@ -67,7 +71,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_any(FwdArgs a, DropArgs d)
     }
     const float rstd = (float)(1.0 / sqrt(any_sum(ss, red) / (double)a.size + (double)a.eps));
     const float m = (float)mean;
-    for (uint32_t g = threadIdx.x; g < groups; g += kAnyThreads) {
+    for (uint32_t g = threadIdx.x; g < groups; g += kRowThreads) {
       float v[8], w[8], b[8];
       unpack<DT>(load_group8<DT, false>(h, g, a.size), v);
       weight_group<DT>(a.weight, a.wdt, g, a.size, 1.0f, w);
@@ -83,89 +87,280 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_any(FwdArgs a, DropArgs d)
   }
 }
 
-// The rows' gradients: a pass for the two sums, a pass for the result.
-template <int DT, bool DROP>
-__global__ __launch_bounds__(kAnyThreads) void k_norm_rows_grad_any(BwdArgs a, DropArgs d) {
-  __shared__ double red[kAnyWaves];
-  const uint32_t groups = (a.size + kGroup - 1) / kGroup;
-  const uint32_t step = DROP ? drop_step(d) : 0u;
+// ---------------------------------------------------------------- gradients of long rows
+// Two passes, for rows whose columns' sums would fill a compute unit's
+// registers and more: with a workgroup a row, each of 256 workgroups would
+// leave partial sums as long as the row (2048 x 16384 in bfloat16: 34 MB
+// written and read again, 68 us).  The first pass leaves a row's two means;
+// the second takes strips of columns down many rows, whose sums stay in
+// registers, and reads the matrices again, mostly from the cache before
+// memory.
+constexpr int kLongThreads = 512;
+constexpr int kLongWaves = kLongThreads / 64;
+// Workgroups of the second pass: 512, two for each compute unit, took 63.3 us
+// for 2048 x 16384 in bfloat16, 1024 of them 65.6 and 2048 of them 67.1.
+constexpr uint32_t kLongStrips = 512;
+
+template <int DT>
+__device__ __forceinline__ void unit_settled(u32x4& q, uint32_t c, uint32_t size) {
+  if (c + kUnit<DT> > size)
+    q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
+}
+template <int DT>
+__device__ __forceinline__ u32x4 unit_clamped(uint64_t row, uint32_t c, uint32_t size) {
+  return load16<DT, false>(row + (uint64_t)(c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>);
+}
+template <int DT>
+__device__ __forceinline__ void weight_unit(uint64_t w, int wdt, uint32_t c, uint32_t size, float (&v)[kUnit<DT>]) {
+  if constexpr (DT == GCLIP_F32) {
+    if (w == 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = 1.0f;
+    } else {
+      u32x4 q = unit_clamped<DT>(w, c, size);
+      unit_settled<DT>(q, c, size);
+      unpack_unit<DT>(q, v);
+    }
+  } else {
+    weight_group<DT>(w, wdt, c / kGroup, size, 1.0f, v);
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kLongThreads) void k_row_means_long(BwdArgs a) {
+  __shared__ double red[2][kLongWaves];
+  const uint32_t units = (a.size + kUnit<DT> - 1) / kUnit<DT>;
   for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld;
     const float mean = a.mean[r], rstd = a.rstd[r];
-    double s1 = 0.0, s2 = 0.0;
-    for (uint32_t g = threadIdx.x; g < groups; g += kAnyThreads) {
-      float u[8], v[8], w[8];
-      unpack<DT>(load_group8<DT, false>(dy, g, a.size), u);
-      unpack<DT>(load_group8<DT, false>(x, g, a.size), v);
-      weight_group<DT>(a.weight, a.wdt, g, a.size, 1.0f, w);
+    double s1 = 0.0, s2 = 0.0;  // of each unit's binary32 sums
+    for (uint32_t u = threadIdx.x; u < units; u += kLongThreads) {
+      const uint32_t c = u * kUnit<DT>;
+      u32x4 p = unit_clamped<DT>(dy, c, a.size), q = unit_clamped<DT>(x, c, a.size);
+      float g[kUnit<DT>], n[kUnit<DT>], w[kUnit<DT>];
+      weight_unit<DT>(a.weight, a.wdt, c, a.size, w);
+      unit_settled<DT>(p, c, a.size);
+      unit_settled<DT>(q, c, a.size);
+      unpack_unit<DT>(p, g);
+      unpack_unit<DT>(q, n);
+      float t1 = 0.0f, t2 = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (g * kGroup + k < a.size) {
-          const float t = u[k] * w[k];
-          s1 += (double)t;
-          s2 += (double)(t * ((v[k] - mean) * rstd));
-        }
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+        const float t = g[j] * w[j];
+        t1 += t;
+        t2 = __builtin_fmaf(t, (n[j] - mean) * rstd, t2);
       }
+      s1 += (double)t1;
+      s2 += (double)t2;
     }
-    const float c1 = (float)(any_sum(s1, red) / (double)a.size);
-    const float c2 = (float)(any_sum(s2, red) / (double)a.size);
-    for (uint32_t g = threadIdx.x; g < groups; g += kAnyThreads) {
-      float u[8], v[8], w[8];
-      unpack<DT>(load_group8<DT, false>(dy, g, a.size), u);
-      unpack<DT>(load_group8<DT, false>(x, g, a.size), v);
-      weight_group<DT>(a.weight, a.wdt, g, a.size, 1.0f, w);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = rstd * (u[k] * w[k] - c1 - (v[k] - mean) * rstd * c2);
-      if (a.dh.at) {
-        unpack<DT>(load_group8<DT, false>(a.dh.at + r * a.dh.ld, g, a.size), u);
+    for (int off = 32; off > 0; off >>= 1) {
+      s1 += __shfl_xor(s1, off, 64);
+      s2 += __shfl_xor(s2, off, 64);
+    }
+    __syncthreads();  // red may still be read for the row before
+    if ((threadIdx.x & 63) == 0) {
+      red[0][threadIdx.x >> 6] = s1;
+      red[1][threadIdx.x >> 6] = s2;
+    }
+    __syncthreads();
+    if (threadIdx.x < 2) {
+      double t = red[threadIdx.x][0];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += u[k];
-      }
-      store_group8<DT, false>(a.dres.at + r * a.dres.ld, g, a.size, pack<DT>(v));
-      if constexpr (DROP) {
-        drop_group(d, step, r, g, v);
-        store_group8<DT, false>(a.dx.at + r * a.dx.ld, g, a.size, pack<DT>(v));
-      }
+      for (int i = 1; i < kLongWaves; ++i) t += red[threadIdx.x][i];
+      a.sums[2 * (uint64_t)r + threadIdx.x] = (float)(t / (double)a.size);
     }
   }
 }
 
-// Part p of the weights' gradients: the rows r with r mod parts == p, in a
-// fixed order.  A wave takes 64 groups of columns, the workgroup's waves
-// share the part's rows.
-template <int DT>
-__global__ __launch_bounds__(kAnyThreads) void k_norm_cols_grad_any(BwdArgs a) {
-  __shared__ float red[kAnyWaves][64][17];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = blockIdx.x * 64 + lane;
-  float dw[8] = {}, db[8] = {};
-  if (g * kGroup < a.size) {
-    for (uint64_t r = blockIdx.y + (uint64_t)wave * a.parts; r < a.rows; r += (uint64_t)kAnyWaves * a.parts) {
-      float u[8], v[8];
-      unpack<DT>(load_group8<DT, false>(a.dy.at + r * a.dy.ld, g, a.size), u);
-      unpack<DT>(load_group8<DT, false>(a.x.at + r * a.x.ld, g, a.size), v);
-      const float mean = a.mean[r], rstd = a.rstd[r];
+// A workgroup takes a strip of 64 units of columns and part blockIdx.y of the
+// rows, its waves in turn; a row's loads are under way while the one before
+// is worked on.
+template <int DT, bool RES, bool DROP>
+__global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, DropArgs d) {
+  __shared__ float red[kLongWaves][64 * kUnit<DT> + 1];
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t c = (blockIdx.x * 64 + lane) * kUnit<DT>;
+  const uint32_t step = DROP ? drop_step(d) : 0u;
+  const uint32_t stride = gridDim.y * kLongWaves;
+  float w[kUnit<DT>], dw[kUnit<DT>] = {}, db[kUnit<DT>] = {};
+  weight_unit<DT>(a.weight, a.wdt, c, a.size, w);
+  u32x4 ny, nx, nh{0u, 0u, 0u, 0u};
+  float nmean = 0.0f, nrstd = 0.0f, nc1 = 0.0f, nc2 = 0.0f;
+  const auto fetch = [&](uint32_t r) {
+    ny = unit_clamped<DT>(a.dy.at + r * a.dy.ld, c, a.size);
+    nx = unit_clamped<DT>(a.x.at + r * a.x.ld, c, a.size);
+    if (RES && a.dh.at) nh = unit_clamped<DT>(a.dh.at + r * a.dh.ld, c, a.size);
+    nmean = a.mean[r];
+    nrstd = a.rstd[r];
+    nc1 = a.sums[2 * (uint64_t)r];
+    nc2 = a.sums[2 * (uint64_t)r + 1];
+  };
+  uint32_t r = blockIdx.y * kLongWaves + wave;
+  if (r < a.rows) fetch(r);
+  while (r < a.rows) {
+    float g[kUnit<DT>], n[kUnit<DT>], h[kUnit<DT>];
+    const float mean = nmean, rstd = nrstd, c1 = nc1, c2 = nc2;
+    unit_settled<DT>(ny, c, a.size);
+    unit_settled<DT>(nx, c, a.size);
+    unpack_unit<DT>(ny, g);
+    unpack_unit<DT>(nx, n);
+    if constexpr (RES) {
+      unit_settled<DT>(nh, c, a.size);
+      unpack_unit<DT>(nh, h);
+    }
+    const uint32_t next = r + stride;
+    if (next < a.rows) fetch(next);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dw[k] += u[k] * ((v[k] - mean) * rstd);
-        db[k] += u[k];
+    for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+      n[j] = (n[j] - mean) * rstd;
+      dw[j] = __builtin_fmaf(g[j], n[j], dw[j]);
+      db[j] += g[j];
+      n[j] = rstd * (g[j] * w[j] - c1 - n[j] * c2);
+      if constexpr (RES) n[j] += h[j];
+    }
+    if (c < a.size) {
+      store_unit<DT, true>(a.dres.at + r * a.dres.ld, c / kUnit<DT>, a.size, pack_unit<DT>(n));
+      if constexpr (DROP) {
+        drop_unit<DT>(d, step, r, c, n);
+        store_unit<DT, true>(a.dx.at + r * a.dx.ld, c / kUnit<DT>, a.size, pack_unit<DT>(n));
       }
     }
+    r = next;
   }
+  if (!a.dweight && !a.dbias) return;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    red[wave][lane][k] = dw[k];
-    red[wave][lane][8 + k] = db[k];
+  for (uint32_t which = 0; which < 2; ++which) {
+    __syncthreads();
+#pragma unroll
+    for (uint32_t j = 0; j < kUnit<DT>; ++j) red[wave][lane * kUnit<DT> + j] = which ? db[j] : dw[j];
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 64 * kUnit<DT>; i += kLongThreads) {
+      const uint32_t col = blockIdx.x * 64 * kUnit<DT> + i;
+      float t = red[0][i];
+#pragma unroll
+      for (int k = 1; k < kLongWaves; ++k) t += red[k][i];
+      if (col < a.size) a.partials[((uint64_t)blockIdx.y * 2 + which) * a.size + col] = t;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- rows of fewer than eight columns
+// A lane takes a row, element by element.
+template <int DT>
+__device__ __forceinline__ void load_short(uint64_t row, uint32_t size, float (&v)[8]) {
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) v[k] = k < size && k < 7 ? elem_float<DT>(load_elem<DT>(row + k * kElem<DT>)) : 0.0f;
+}
+template <int DT>
+__device__ __forceinline__ void store_short(uint64_t row, uint32_t size, const float (&v)[8]) {
+#pragma unroll
+  for (uint32_t k = 0; k < 7; ++k)
+    if (k < size) store_elem<DT>(row + k * kElem<DT>, elem_bits<DT>(v[k]));
+}
+template <int DT>
+__device__ __forceinline__ void weight_short(uint64_t w, int wdt, uint32_t size, float def, float (&v)[8]) {
+  if (w == 0) {
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) v[k] = def;
+  } else if (DT == GCLIP_F32 || wdt == GCLIP_F32) {
+    load_short<GCLIP_F32>(w, size, v);
+  } else {
+    load_short<DT>(w, size, v);
+  }
+}
+
+template <int DT, bool RES, bool DROP>
+__global__ __launch_bounds__(kAnyThreads) void k_norm_short(FwdArgs a, DropArgs d) {
+  const uint32_t r = blockIdx.x * kAnyThreads + threadIdx.x;
+  if (r >= a.rows) return;
+  float v[8], w[8], b[8];
+  load_short<DT>(a.x.at + r * a.x.ld, a.size, v);
+  if constexpr (RES) {
+    float q[8];
+    if constexpr (DROP) drop_group(d, drop_step(d), r, 0, v);
+    load_short<DT>(a.residual.at + r * a.residual.ld, a.size, q);
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) v[k] = k < a.size ? elem_float<DT>(elem_bits<DT>(v[k] + q[k])) : 0.0f;
+    store_short<DT>(a.h.at + r * a.h.ld, a.size, v);
+  }
+  weight_short<DT>(a.weight, a.wdt, a.size, 1.0f, w);
+  weight_short<DT>(a.bias, a.wdt, a.size, 0.0f, b);
+  double s = 0.0, ss = 0.0;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) s += (double)v[k];
+  const double mean = s / (double)a.size;
+#pragma unroll
+  for (uint32_t k = 0; k < 7; ++k) {
+    const double t = k < a.size ? (double)v[k] - mean : 0.0;
+    ss += t * t;
+  }
+  const float rstd = (float)(1.0 / sqrt(ss / (double)a.size + (double)a.eps)), m = (float)mean;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) v[k] = __builtin_fmaf((v[k] - m) * rstd, w[k], b[k]);
+  store_short<DT>(a.y.at + r * a.y.ld, a.size, v);
+  if (a.mean) {
+    a.mean[r] = m;
+    a.rstd[r] = rstd;
+  }
+}
+
+template <int DT, bool RES, bool DROP>
+__global__ __launch_bounds__(kAnyThreads) void k_norm_grad_short(BwdArgs a, DropArgs d) {
+  __shared__ float red[kAnyWaves][16];
+  const uint32_t step = DROP ? drop_step(d) : 0u;
+  float w[8], dw[8] = {}, db[8] = {};
+  weight_short<DT>(a.weight, a.wdt, a.size, 1.0f, w);
+  for (uint32_t r = blockIdx.x * kAnyThreads + threadIdx.x; r < a.rows; r += gridDim.x * kAnyThreads) {
+    float g[8], n[8];
+    load_short<DT>(a.dy.at + r * a.dy.ld, a.size, g);
+    load_short<DT>(a.x.at + r * a.x.ld, a.size, n);
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) {
+      n[k] = (n[k] - mean) * rstd;
+      dw[k] = __builtin_fmaf(g[k], n[k], dw[k]);
+      db[k] += g[k];
+      g[k] *= w[k];
+      c1 += g[k];
+      c2 = __builtin_fmaf(g[k], n[k], c2);
+    }
+    c1 /= (float)a.size;
+    c2 /= (float)a.size;
+#pragma unroll
+    for (int k = 0; k < 7; ++k) n[k] = rstd * (g[k] - c1 - n[k] * c2);
+    if (RES && a.dh.at) {
+      load_short<DT>(a.dh.at + r * a.dh.ld, a.size, g);
+#pragma unroll
+      for (int k = 0; k < 7; ++k) n[k] += g[k];
+    }
+    store_short<DT>(a.dres.at + r * a.dres.ld, a.size, n);
+    if constexpr (DROP) {
+      drop_group(d, step, r, 0, n);
+      store_short<DT>(a.dx.at + r * a.dx.ld, a.size, n);
+    }
+  }
+  if (!a.dweight && !a.dbias) return;
+#pragma unroll
+  for (int k = 0; k < 7; ++k) {
+    const float p = lanes_sum<64>(dw[k]), q = lanes_sum<64>(db[k]);
+    if ((threadIdx.x & 63) == 0) {
+      red[threadIdx.x >> 6][k] = p;
+      red[threadIdx.x >> 6][8 + k] = q;
+    }
   }
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < 64 * 16; i += kAnyThreads) {
-    const uint32_t which = i / 512, l = (i % 512) / 8, k = i % 8, c = (blockIdx.x * 64 + l) * kGroup + k;
-    float t = red[0][l][8 * which + k];
+  if (threadIdx.x < 2 * a.size) {
+    const uint32_t which = threadIdx.x >= a.size, col = threadIdx.x - which * a.size;
+    float t = red[0][8 * which + col];
 #pragma unroll
-    for (int w = 1; w < kAnyWaves; ++w) t += red[w][l][8 * which + k];
-    if (c < a.size) a.partials[((uint64_t)blockIdx.y * 2 + which) * a.size + c] = t;
+    for (int i = 1; i < kAnyWaves; ++i) t += red[i][8 * which + col];
+    a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + col] = t;
   }
 }
 
+// ---------------------------------------------------------------- dropout
 // A lane takes a unit of 16 bytes.  A unit of a 16-bit format is a group; of
 // binary32 half of one, whose two lanes run the generator both: a wave's
 // accesses are adjacent then, and there is twice the time for it.  Bound by
@@ -187,29 +382,37 @@ __global__ __launch_bounds__(kAnyThreads) void k_dropout(Rows x, Rows y, uint32_
 
 template <int DT>
 hipError_t forward_any(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  const dim3 grid(std::min<uint32_t>(a.rows, 1u << 20)), block(kAnyThreads);
-  if (!residual) hipLaunchKernelGGL((k_norm_any<DT, false, false>), grid, block, 0, st, a, DropArgs{});
-  else if (!drop) hipLaunchKernelGGL((k_norm_any<DT, true, false>), grid, block, 0, st, a, DropArgs{});
-  else hipLaunchKernelGGL((k_norm_any<DT, true, true>), grid, block, 0, st, a, *drop);
+  const dim3 block(kAnyThreads);
+  if (a.size < kRegistersMin) {
+    const dim3 grid((a.rows - 1) / kAnyThreads + 1);
+    if (!residual) hipLaunchKernelGGL((k_norm_short<DT, false, false>), grid, block, 0, st, a, DropArgs{});
+    else if (!drop) hipLaunchKernelGGL((k_norm_short<DT, true, false>), grid, block, 0, st, a, DropArgs{});
+    else hipLaunchKernelGGL((k_norm_short<DT, true, true>), grid, block, 0, st, a, *drop);
+    return hipGetLastError();
+  }
+  const dim3 grid(std::min<uint32_t>(a.rows, 1u << 20)), row(kRowThreads);
+  if (!residual) hipLaunchKernelGGL((k_norm_any<DT, false, false>), grid, row, 0, st, a, DropArgs{});
+  else if (!drop) hipLaunchKernelGGL((k_norm_any<DT, true, false>), grid, row, 0, st, a, DropArgs{});
+  else hipLaunchKernelGGL((k_norm_any<DT, true, true>), grid, row, 0, st, a, *drop);
   return hipGetLastError();
 }
 
-// The weights' gradients first: dx may be written over dy or x.
 template <int DT>
-hipError_t backward_any(const BwdArgs& a, const DropArgs* drop, hipStream_t st) {
-  const dim3 block(kAnyThreads);
-  const uint32_t groups = (a.size + kGroup - 1) / kGroup;
-  if (a.dweight || a.dbias) {
-    hipLaunchKernelGGL((k_norm_cols_grad_any<DT>), dim3((groups + 63) / 64, a.parts), block, 0, st, a);
-    const hipError_t e = join_weight_grads<DT>(a, st);
-    if (e != hipSuccess) return e;
+hipError_t backward_any(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if (a.rows > 0 && a.size < kRegistersMin) {
+    const dim3 grid(a.parts), block(kAnyThreads);
+    if (!residual) hipLaunchKernelGGL((k_norm_grad_short<DT, false, false>), grid, block, 0, st, a, DropArgs{});
+    else if (!drop) hipLaunchKernelGGL((k_norm_grad_short<DT, true, false>), grid, block, 0, st, a, DropArgs{});
+    else hipLaunchKernelGGL((k_norm_grad_short<DT, true, true>), grid, block, 0, st, a, *drop);
+  } else if (a.rows > 0) {
+    const dim3 block(kLongThreads), strips((a.size - 1) / (64 * kUnit<DT>) + 1, a.parts);
+    hipLaunchKernelGGL((k_row_means_long<DT>), dim3(std::min<uint32_t>(a.rows, 1u << 20)), block, 0, st, a);
+    if (!residual) hipLaunchKernelGGL((k_norm_grad_long<DT, false, false>), strips, block, 0, st, a, DropArgs{});
+    else if (!drop) hipLaunchKernelGGL((k_norm_grad_long<DT, true, false>), strips, block, 0, st, a, DropArgs{});
+    else hipLaunchKernelGGL((k_norm_grad_long<DT, true, true>), strips, block, 0, st, a, *drop);
   }
-  if (a.rows > 0) {
-    const dim3 grid(std::min<uint32_t>(a.rows, 1u << 20));
-    if (drop) hipLaunchKernelGGL((k_norm_rows_grad_any<DT, true>), grid, block, 0, st, a, *drop);
-    else hipLaunchKernelGGL((k_norm_rows_grad_any<DT, false>), grid, block, 0, st, a, DropArgs{});
-  }
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  return e != hipSuccess || (!a.dweight && !a.dbias) ? e : join_weight_grads<DT>(a, st);
 }
 
 template <int DT>
@@ -223,21 +426,20 @@ hipError_t dropout(const Rows& x, const Rows& y, uint32_t rows, uint32_t size, c
 
 }  // namespace
 
-// A part for each workgroup of the kernel with rows in registers.  Else as
-// many as leave each at least 16 rows, at most 256, and at most 64 MiB of
-// them for long rows.
+// Rows in registers: a part for each workgroup.  Shorter rows: as many as
+// leave each lane four rows.  Longer ones: as many as make kLongStrips
+// workgroups of strips of 512 columns, and leave each wave two rows.
 uint32_t layer_parts(int64_t rows, int64_t size) {
-  if (rows > 0 && in_registers((uint32_t)size)) {
-    const uint32_t n = (uint32_t)rows;
-    return std::max(bwd_parts<GCLIP_F32>(n, (uint32_t)size), bwd_parts<GCLIP_BF16>(n, (uint32_t)size));
-  }
-  const int64_t by_rows = std::max<int64_t>(1, (rows + 15) / 16);
-  const int64_t by_bytes = std::max<int64_t>(1, (64ll << 20) / (8 * size));
-  return (uint32_t)std::min<int64_t>({by_rows, by_bytes, 256});
+  if (rows == 0) return 0;
+  const uint32_t n = (uint32_t)rows, c = (uint32_t)size;
+  if (in_registers(c, kBwdMax)) return std::max(bwd_parts<GCLIP_F32>(n, c), bwd_parts<GCLIP_BF16>(n, c));
+  if (c < kRegistersMin) return std::min<uint32_t>((n - 1) / (4 * kAnyThreads) + 1, kBwdParts);
+  const uint32_t strips = (c - 1) / 512 + 1;
+  return std::min<uint32_t>({std::max<uint32_t>(kLongStrips / strips, 1), (n - 1) / (2 * kLongWaves) + 1, kBwdParts});
 }
 
 hipError_t launch_layer_forward(const FwdArgs& a, int32_t dtype, bool residual, const DropArgs* drop, hipStream_t st) {
-  const bool regs = in_registers(a.size);
+  const bool regs = in_registers(a.size, kFwdMax);
   switch (dtype) {
     case GCLIP_F32:
       return regs ? forward_rows<GCLIP_F32>(a, residual, drop, st) : forward_any<GCLIP_F32>(a, residual, drop, st);
@@ -249,14 +451,14 @@ hipError_t launch_layer_forward(const FwdArgs& a, int32_t dtype, bool residual, 
 }
 
 hipError_t launch_layer_backward(const BwdArgs& a, int32_t dtype, bool residual, const DropArgs* drop, hipStream_t st) {
-  const bool regs = a.rows > 0 && in_registers(a.size);
+  const bool regs = a.rows > 0 && in_registers(a.size, kBwdMax);
   switch (dtype) {
     case GCLIP_F32:
-      return regs ? backward_rows<GCLIP_F32>(a, residual, drop, st) : backward_any<GCLIP_F32>(a, drop, st);
+      return regs ? backward_rows<GCLIP_F32>(a, residual, drop, st) : backward_any<GCLIP_F32>(a, residual, drop, st);
     case GCLIP_F16:
-      return regs ? backward_rows<GCLIP_F16>(a, residual, drop, st) : backward_any<GCLIP_F16>(a, drop, st);
+      return regs ? backward_rows<GCLIP_F16>(a, residual, drop, st) : backward_any<GCLIP_F16>(a, residual, drop, st);
     default:
-      return regs ? backward_rows<GCLIP_BF16>(a, residual, drop, st) : backward_any<GCLIP_BF16>(a, drop, st);
+      return regs ? backward_rows<GCLIP_BF16>(a, residual, drop, st) : backward_any<GCLIP_BF16>(a, residual, drop, st);
   }
 }
 

@@ -90,6 +90,9 @@ int32_t streamed(int64_t rows, int64_t size, uint64_t es, uint64_t matrices) {
   return (__uint128_t)(uint64_t)rows * (uint64_t)size * es * matrices > gclip::kStreamBytes ? 1 : 0;
 }
 
+// A workspace begins with the partial sums; the long rows' means follow.
+inline int64_t partial_floats(int64_t rows, int64_t size) { return (int64_t)gclip::layer_parts(rows, size) * 2 * size; }
+
 gclip_status status_of(hipError_t e) { return e == hipSuccess ? GCLIP_OK : gclip::hip_fail(e); }
 
 gclip_status forward(const gclip_layer_forward* a, bool residual, const gclip_dropout* drop, void* stream) {
@@ -142,15 +145,15 @@ gclip_status backward(const gclip_layer_backward* a, bool residual, const gclip_
   if (a->dh && !matrix(a->dh, a->lddh, a->rows, a->size, es, false, &dh)) return GCLIP_EINVAL;
   if (residual && !matrix(a->dresidual, a->lddresidual, a->rows, a->size, es, true, &dr)) return GCLIP_EINVAL;
   if ((!residual || two) && !matrix(a->dx, a->lddx, a->rows, a->size, es, true, &dx)) return GCLIP_EINVAL;
-  if (a->dweight || a->dbias) {
-    if (!a->workspace || a->workspace_bytes < gclip_layer_workspace(a->rows, a->size)) return GCLIP_EINVAL;
-    if (!vector(a->workspace, a->workspace_bytes, 1, true, &wk) || address(a->workspace) % 16 != 0) return GCLIP_EINVAL;
-  }
+  const int64_t need = gclip_layer_workspace(a->rows, a->size);
+  if ((need > 0 && !a->workspace) || a->workspace_bytes < need || address(a->workspace) % 16 != 0) return GCLIP_EINVAL;
+  if (!vector(a->workspace, need, 1, true, &wk)) return GCLIP_EINVAL;
   if (!apart({dy, dh, x, dr, dx, w, dw, db, m, s, wk})) return GCLIP_EINVAL;
   if (a->rows == 0 && ((!a->dweight && !a->dbias) || a->accumulate)) return GCLIP_OK;
   const Operand& out = residual ? dr : dx;
   const gclip::BwdArgs k{{dy.at, dy.ld}, {dh.at, dh.ld}, {x.at, x.ld}, {out.at, out.ld}, {dx.at, dx.ld}, a->mean, a->rstd,
                          address(a->weight), address(a->dweight), address(a->dbias), static_cast<float*>(a->workspace),
+                         static_cast<float*>(a->workspace) + partial_floats(a->rows, a->size),
                          (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, a->grad_dtype, a->accumulate ? 1 : 0,
                          gclip::layer_parts(a->rows, a->size),
                          streamed(a->rows, a->size, es, 3 + (a->dh ? 1 : 0) + (two ? 1 : 0))};
@@ -194,7 +197,7 @@ gclip_status gclip_dropout_apply(const void* x, int64_t ldx, void* y, int64_t ld
 
 int64_t gclip_layer_workspace(int64_t rows, int64_t size) {
   if (!extents_ok(rows, size, 1)) return 0;
-  return (int64_t)gclip::layer_parts(rows, size) * 2 * size * 4;
+  return 4 * (partial_floats(rows, size) + (size > gclip::kBwdMax ? 2 * rows : 0));
 }
 
 }  // extern "C"

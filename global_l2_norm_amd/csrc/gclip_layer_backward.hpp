@@ -14,19 +14,13 @@ namespace gclip {
 // meet in shared memory at the end.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
 template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
-__global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
-  constexpr uint32_t kBwdThreads = bwd_threads(LANES, NV * kUnit<DT>);
+__global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
+  constexpr uint32_t kBwdThreads = bwd_threads(NV * kUnit<DT>);
   constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
-  // sixteen waves' registers do not hold two groups' sums beside the row: they
-  // lie in shared memory, each lane's its own, and the weights are read again
-  // for each row, from the caches
-  constexpr bool kLong = LANES > 512 && NV * kUnit<DT> > 8;
-  constexpr bool kLate = kLong;  // nor dh of the next row: a row's own is loaded while its sums meet
-  static_assert(!kLong || kRows == 1, "a long row has its workgroup to itself");
   constexpr uint32_t kCols = LANES * NV * kUnit<DT>;
   constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
   __shared__ float red[2][2][kBwdThreads / 64];
-  __shared__ __align__(16) float sums[kLong ? 2 * kCols : kMeet > 1 ? kMeet * kCols : 1];
+  __shared__ float sums[kMeet > 1 ? kMeet * kCols : 1];
   const uint32_t lane = threadIdx.x % LANES;
   uint32_t slot = threadIdx.x / LANES;
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
@@ -45,25 +39,17 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
     for (int k = 0; k < NV; ++k) {
       ny[k] = load_columns<DT, LANES, SURE, STREAMED>(dy, lane, k, a.size);
       nx[k] = load_columns<DT, LANES, SURE, STREAMED>(x, lane, k, a.size);
-      if constexpr (RES && !kLate)
+      if constexpr (RES)
         nh[k] = a.dh.at ? load_columns<DT, LANES, SURE, STREAMED>(dh, lane, k, a.size) : u32x4{0u, 0u, 0u, 0u};
     }
   };
   fetch(base);
-  float w[kLong ? 1 : NV][kUnit<DT>], dw[kLong ? 1 : NV][kUnit<DT>], db[kLong ? 1 : NV][kUnit<DT>];
-  typedef float f32x4 __attribute__((ext_vector_type(4)));
-  constexpr uint32_t kQuads = kUnit<DT> / 4;
-  f32x4* const own = reinterpret_cast<f32x4*>(sums) + threadIdx.x;  // [dw, db][NV][kQuads], kBwdThreads apart
-  if constexpr (kLong) {
+  float w[NV][kUnit<DT>], dw[NV][kUnit<DT>], db[NV][kUnit<DT>];
 #pragma unroll
-    for (uint32_t k = 0; k < 2 * NV * kQuads; ++k) own[k * kBwdThreads] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  } else {
+  for (int k = 0; k < NV; ++k) {
+    weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
-#pragma unroll
-      for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = db[k][j] = 0.0f;
-    }
+    for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = db[k][j] = 0.0f;
   }
   const float count = (float)a.size, inverse = 1.0f / count;
   uint32_t turn = 0;
@@ -81,46 +67,18 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
       if (r >= a.rows) ny[k] = nx[k] = u32x4{0u, 0u, 0u, 0u};
       unpack_unit<DT>(ny[k], g[k]);
       unpack_unit<DT>(nx[k], n[k]);
-      if constexpr (RES && !kLate) {
+      if constexpr (RES) {
         settle<DT, LANES, SURE>(nh[k], lane, k, a.size);
         hh[k] = nh[k];
       }
 #pragma unroll
-      for (uint32_t j = 0; j < kUnit<DT>; ++j) n[k][j] = (n[k][j] - mean) * rstd;
-      float wk[kUnit<DT>];
-      if constexpr (kLong) {
-#pragma unroll
-        for (uint32_t i = 0; i < kQuads; ++i) {
-          f32x4 t = own[(k * kQuads + i) * kBwdThreads], u = own[((NV + k) * kQuads + i) * kBwdThreads];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            t[j] = __builtin_fmaf(g[k][4 * i + j], n[k][4 * i + j], t[j]);
-            u[j] += g[k][4 * i + j];
-          }
-          own[(k * kQuads + i) * kBwdThreads] = t;
-          own[((NV + k) * kQuads + i) * kBwdThreads] = u;
-        }
-        weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, wk);
-      } else {
-#pragma unroll
-        for (uint32_t j = 0; j < kUnit<DT>; ++j) {
-          dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
-          db[k][j] += g[k][j];
-          wk[j] = w[k][j];
-        }
-      }
-#pragma unroll
       for (uint32_t j = 0; j < kUnit<DT>; ++j) {
-        g[k][j] *= wk[j];
+        n[k][j] = (n[k][j] - mean) * rstd;
+        dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
+        db[k][j] += g[k][j];
+        g[k][j] *= w[k][j];
         s1 += g[k][j];
         s2 = __builtin_fmaf(g[k][j], n[k][j], s2);
-      }
-    }
-    if constexpr (RES && kLate) {
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        hh[k] = a.dh.at ? load_columns<DT, LANES, SURE, STREAMED>(a.dh.at + r * a.dh.ld, lane, k, a.size)
-                        : u32x4{0u, 0u, 0u, 0u};
       }
     }
     const uint32_t next = base + gridDim.x * kRows;
@@ -159,7 +117,6 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
         for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = rstd * (g[k][j] - c1 - n[k][j] * c2);
         if constexpr (RES) {
           float q[kUnit<DT>];
-          if constexpr (kLate) settle<DT, LANES, SURE>(hh[k], lane, k, a.size);
           unpack_unit<DT>(hh[k], q);
 #pragma unroll
           for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] += q[j];
@@ -178,23 +135,8 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
   if (!a.dweight && !a.dbias) return;
 #pragma unroll
   for (uint32_t which = 0; which < 2; ++which) {
-    if constexpr (kLong) {
-#pragma unroll
-      for (uint32_t k = 0; k < NV * kQuads; ++k) {
-        const f32x4 t = own[(which * NV * kQuads + k) * kBwdThreads];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t c = column_of<DT>(lane, LANES, k / kQuads) + k % kQuads * 4 + j;
-          if (c < a.size) {
-            if (a.parts == 1) store_weight_grad<DT>(a, which, c, t[j]);
-            else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t[j];
-          }
-        }
-      }
-      continue;
-    }
-    float(&v)[kLong ? 1 : NV][kUnit<DT>] = which ? db : dw;
-    if constexpr (kMeet > 1 && !kLong) {
+    float(&v)[NV][kUnit<DT>] = which ? db : dw;
+    if constexpr (kMeet > 1) {
       const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
       __syncthreads();
 #pragma unroll
@@ -213,7 +155,7 @@ __global__ __launch_bounds__(bwd_threads(LANES, NV * kUnit<DT>)) void k_norm_row
         if (a.parts == 1) store_weight_grad<DT>(a, which, c, t);
         else a.partials[((uint64_t)blockIdx.x * 2 + which) * a.size + c] = t;
       }
-    } else if constexpr (!kLong) {
+    } else {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
@@ -262,7 +204,7 @@ hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
 template <int DT, int LANES, int NV, int SURE, bool STREAMED>
 hipError_t backward_shape(BwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
   a.parts = bwd_parts<DT>(a.rows, a.size);
-  const dim3 grid(a.parts), block(bwd_threads(LANES, NV * kUnit<DT>));
+  const dim3 grid(a.parts), block(bwd_threads(NV * kUnit<DT>));
   if (!residual)
     hipLaunchKernelGGL((k_norm_rows_grad<DT, LANES, NV, SURE, false, false, STREAMED>), grid, block, 0, st, a, DropArgs{});
   else if (!drop)

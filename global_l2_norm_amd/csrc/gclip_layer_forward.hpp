@@ -12,12 +12,13 @@ namespace gclip {
 template <int LANES>
 constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
 
-#ifndef GCLIP_FWD_WGS
-#define GCLIP_FWD_WGS 4
-#endif
-#ifndef GCLIP_FWD_WGS1
-#define GCLIP_FWD_WGS1 8
-#endif
+// Workgroups of four waves for each compute unit, by the columns that a lane
+// holds: as many as its registers let run at once, so that each goes through
+// its rows with the next one's loads under way.  Measured: 2 for 32 columns
+// (4096 x 2048 binary32 residual 21.4 us; 3: 24.0, 4: 27.4), 4 for 12 to 24
+// (8192 x 1024 bfloat16 norm 7.3 us; 2: 7.9), 8 for up to 8 (131072 x 64:
+// 7.8 us; 4: 8.1, 16: 8.4).
+constexpr uint32_t fwd_workgroups(uint32_t columns) { return columns <= 8 ? 8 : columns <= 24 ? 4 : 2; }
 
 // One pass: a row's elements are read once, into the registers of LANES
 // lanes, where its mean, its squared deviations from it and y are taken from
@@ -149,7 +150,7 @@ hipError_t forward_shape(const FwdArgs& a, bool residual, const DropArgs* drop, 
   // workgroups of a wave until there are four for each compute unit
   const uint32_t threads = LANES <= 64 && a.rows < 1024 * (64 / LANES) ? 64 : kFwdThreads<LANES>;
   const uint32_t at_once = threads / LANES;
-  const uint32_t most = 256u * (NV * kUnit<DT> <= 8 ? GCLIP_FWD_WGS1 : GCLIP_FWD_WGS) * 256 / threads;
+  const uint32_t most = 256u * fwd_workgroups(NV * kUnit<DT>) * 256 / threads;
   const uint32_t need = (a.rows + at_once - 1) / at_once;
   const dim3 grid(need < most ? need : most), block(threads);
   if (!residual)
@@ -181,7 +182,7 @@ hipError_t forward_few(int shape, const FwdArgs& a, bool residual, const DropArg
 
 template <int DT>
 hipError_t forward_rows(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  static_assert(GCLIP_STREAM_MB < 100 || (uint64_t)kFewRows * kRegistersMax * 4 * 4 <= kStreamBytes, "few rows are not streamed");
+  static_assert((uint64_t)kFewRows * kFwdMax * 4 * 4 <= kStreamBytes, "few rows are not streamed");
   if (a.rows <= kFewRows) return forward_few<DT>(row_shape_of(kFewShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
   return forward_of<DT>(row_shape_of(kFwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }

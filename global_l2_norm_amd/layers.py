@@ -97,6 +97,8 @@ def _matrix(x, name):
 def _ld(t, name):
     """Distance of a matrix's rows in elements."""
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2 and stride[1] == 1 and shape[0] > 1:
+        return stride[0]
     if t.is_contiguous() or t.numel() == 0:
         return shape[-1]
     lead = [(n, s) for n, s in zip(shape[:-1], stride[:-1]) if n != 1]
@@ -296,8 +298,9 @@ def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, acc
     lddy, hp, lddh = _like(dy, x, "dy"), None, 0
     if dh is not None:
         hp, lddh = dh.data_ptr(), _like(dh, x, "dh")
-    wgp = bgp = wsp = None
-    nbytes = 0
+    wgp = bgp = None
+    nbytes = gclip_layer_workspace(rows, size)
+    workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
     if want_w or want_b:
         if dweight is not None:
             gt = dweight.dtype
@@ -313,9 +316,6 @@ def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, acc
             if dbias is None:
                 dbias = torch.empty(size, dtype=gt, device=x.device)
             bgp = _vector(dbias, size, x, "dbias")
-        nbytes = gclip_layer_workspace(rows, size)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-        wsp = workspace.data_ptr()
     second = not residual or mask is not None  # dx apart from dresidual
     if not second:
         if dx is not None and dres is not None and dx is not dres:
@@ -338,7 +338,8 @@ def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, acc
             ldds = _like(dres, x, "out_residual")
         sp = dres.data_ptr()
     args = GclipLayerBackward(rows, size, code, wdt, _CODES[gt], 1 if accumulate else 0, dy.data_ptr(), lddy, hp, lddh,
-                              x.data_ptr(), ld, mp, rp, wp, sp, ldds, xp, lddx, wgp, bgp, wsp, nbytes)
+                              x.data_ptr(), ld, mp, rp, wp, sp, ldds, xp, lddx, wgp, bgp, workspace.data_ptr(),
+                              nbytes)
     if residual:
         gclip_residual_backward(args, mask.args if mask is not None else None, _raw_stream(device))
     else:

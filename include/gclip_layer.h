@@ -119,7 +119,7 @@ typedef struct gclip_layer_backward {
   void* dweight; /* size elements, or NULL: not wanted */
   void* dbias;   /* size elements, or NULL: not wanted */
   void* workspace; /* 16-byte aligned device memory, for this call alone until it has run */
-  int64_t workspace_bytes; /* at least gclip_layer_workspace(rows, size) when dweight or dbias is wanted */
+  int64_t workspace_bytes; /* at least gclip_layer_workspace(rows, size) */
 } gclip_layer_backward;
 
 /* y = norm(x). */
@@ -138,8 +138,8 @@ gclip_status gclip_residual_backward(const gclip_layer_backward* a, const gclip_
 gclip_status gclip_dropout_apply(const void* x, int64_t ldx, void* y, int64_t ldy, int64_t rows, int64_t size,
                                  int32_t dtype, const gclip_dropout* drop, void* stream);
 
-/* Bytes of workspace that a backward call of this shape needs for dweight
- * and dbias; 0 for arguments that such a call would refuse.  Host only. */
+/* Bytes of workspace that a backward call of this shape needs; 0 without
+ * rows, and for arguments that such a call would refuse.  Host only. */
 int64_t gclip_layer_workspace(int64_t rows, int64_t size);
 
 #ifdef __cplusplus

@@ -132,7 +132,10 @@ def test_workspace():
     for rows in (0, 1, 17, 4096, MOST):
         for size in (1, 7, 768, 16384, 1 << 22, MOST):
             n = L.gclip_layer_workspace(rows, size)
-            assert n >= 8 * size and n % (8 * size) == 0 and n <= max(8 * size, 512 << 20)
+            if rows == 0:
+                assert n == 0
+            else:
+                assert 8 * size <= n <= max(8 * size, 64 << 20) + 8 * rows and n % 8 == 0
 
 
 def _bytes_of(at, ld, rows, size, es=4):
