@@ -117,7 +117,8 @@ gclip_status forward(const gclip_layer_forward* a, bool residual, const gclip_dr
   if (a->rows == 0) return GCLIP_OK;
   const gclip::FwdArgs k{{x.at, x.ld}, {r.at, r.ld}, {h.at, h.ld}, {y.at, y.ld}, address(a->weight), address(a->bias),
                          a->mean, a->rstd, (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, (float)a->eps,
-                         (float)(1.0 / std::sqrt((double)(float)a->eps)), streamed(a->rows, a->size, es, residual ? 4 : 2)};
+                         (float)(1.0 / std::sqrt((double)(float)a->eps)),
+                         streamed(a->rows, a->size, es, residual ? 4 : 2)};
   return status_of(gclip::launch_layer_forward(k, a->dtype, residual, drops ? &d : nullptr,
                                                static_cast<hipStream_t>(stream)));
 }
@@ -151,13 +152,15 @@ gclip_status backward(const gclip_layer_backward* a, bool residual, const gclip_
   if (!apart({dy, dh, x, dr, dx, w, dw, db, m, s, wk})) return GCLIP_EINVAL;
   if (a->rows == 0 && ((!a->dweight && !a->dbias) || a->accumulate)) return GCLIP_OK;
   const Operand& out = residual ? dr : dx;
-  const gclip::BwdArgs k{{dy.at, dy.ld}, {dh.at, dh.ld}, {x.at, x.ld}, {out.at, out.ld}, {dx.at, dx.ld}, a->mean, a->rstd,
+  const gclip::BwdArgs k{{dy.at, dy.ld}, {dh.at, dh.ld}, {x.at, x.ld}, {out.at, out.ld}, {dx.at, dx.ld},
+                         a->mean, a->rstd,
                          address(a->weight), address(a->dweight), address(a->dbias), static_cast<float*>(a->workspace),
                          static_cast<float*>(a->workspace) + partial_floats(a->rows, a->size),
                          (uint32_t)a->rows, (uint32_t)a->size, a->weight_dtype, a->grad_dtype, a->accumulate ? 1 : 0,
                          gclip::layer_parts(a->rows, a->size),
                          streamed(a->rows, a->size, es, 3 + (a->dh ? 1 : 0) + (two ? 1 : 0))};
-  return status_of(gclip::launch_layer_backward(k, a->dtype, residual, two ? &d : nullptr, static_cast<hipStream_t>(stream)));
+  return status_of(gclip::launch_layer_backward(k, a->dtype, residual, two ? &d : nullptr,
+                                                static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

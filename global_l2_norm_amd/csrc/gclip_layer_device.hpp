@@ -153,7 +153,7 @@ __device__ __forceinline__ Raw8<DT> moved_down(Raw8<DT> r, uint32_t n) {
 
 // The n (1 to 7) elements at a, zeros after them.  Elements in front of a
 // belong to the same row when front is set: then one vector ending at the
-// row's end is read and shifted; a row of fewer than eight elements is read
+// row's end is read and moved down; a row of fewer than eight elements is read
 // one by one.
 template <int DT>
 __device__ __forceinline__ Raw8<DT> load_tail(uint64_t a, uint32_t n, bool front) {
@@ -294,7 +294,8 @@ __device__ __forceinline__ Words4 philox(uint32_t c0, uint32_t c1, uint32_t c2, 
 __device__ __forceinline__ uint32_t drop_step(const DropArgs& d) { return d.step + (d.d_step ? *d.d_step : 0u); }
 
 // The generator's halves for one half of a group.
-__device__ __forceinline__ uint64_t philox_half(const DropArgs& d, uint32_t step, uint32_t row, uint32_t g, uint32_t h) {
+__device__ __forceinline__ uint64_t philox_half(const DropArgs& d, uint32_t step, uint32_t row, uint32_t g,
+                                                uint32_t h) {
   const Words4 b = philox(g, row, d.site, step, d.k0, d.k1);
   const uint64_t lo = (uint64_t)b.w[0] | ((uint64_t)b.w[1] << 32), hi = (uint64_t)b.w[2] | ((uint64_t)b.w[3] << 32);
   return h ? hi : lo;

@@ -20,10 +20,19 @@ constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
 // 7.8 us; 4: 8.1, 16: 8.4).
 constexpr uint32_t fwd_workgroups(uint32_t columns) { return columns <= 8 ? 8 : columns <= 24 ? 4 : 2; }
 
-// One pass: a row's elements are read once, into the registers of LANES
-// lanes, where its mean, its squared deviations from it and y are taken from
-// them in turn.  While a row is worked on, the loads of the workgroup's next
-// one are under way; weight and bias stay in registers.
+// y = (x - mean) rstd weight + bias, in one pass: a row's elements are read
+// once, into the registers of LANES lanes, where its mean, its squared
+// deviations from it (of the mean, not of zero: no cancellation) and y are
+// taken from them in turn.  While a row is worked on, the loads of the
+// workgroup's next one are under way; weight and bias stay in registers.
+//
+// Bound by memory: 16384 x 2048 in bfloat16 takes 22.2 us, 6.0 TB/s of one
+// read and one write (a copy of such size: 5.4), the residual step with
+// dropout 44.5 us, 6.0 TB/s; 8192 x 768 in binary32 9.4 us, 5.4 TB/s.  With a
+// workgroup a row and three passes through the caches the first took 45.9 us.
+// Reading rows past the end as the last one, rather than not, keeps the loads
+// of the next row out of a branch, which would be waited for at its end
+// (residual step: 53.7 us against 46.0).
 template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
   constexpr int kThreads = kFwdThreads<LANES>;
@@ -177,13 +186,15 @@ hipError_t forward_few(int shape, const FwdArgs& a, bool residual, const DropArg
   if constexpr (I + 1 < (int)(sizeof(kFewShapes<DT>) / sizeof(RowShape))) {
     if (shape != I) return forward_few<DT, I + 1>(shape, a, residual, drop, st);
   }
-  return forward_shape<DT, kFewShapes<DT>[I].lanes, kFewShapes<DT>[I].units, sure_units(kFewShapes<DT>, I), false>(a, residual, drop, st);
+  constexpr RowShape s = kFewShapes<DT>[I];
+  return forward_shape<DT, s.lanes, s.units, sure_units(kFewShapes<DT>, I), false>(a, residual, drop, st);
 }
 
 template <int DT>
 hipError_t forward_rows(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   static_assert((uint64_t)kFewRows * kFwdMax * 4 * 4 <= kStreamBytes, "few rows are not streamed");
-  if (a.rows <= kFewRows) return forward_few<DT>(row_shape_of(kFewShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
+  if (a.rows <= kFewRows)
+    return forward_few<DT>(row_shape_of(kFewShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
   return forward_of<DT>(row_shape_of(kFwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }
 

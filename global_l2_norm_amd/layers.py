@@ -12,7 +12,8 @@ serve as device memory and streams: every step runs in the HIP kernels.
   buffers of the caller's, added to what the microbatches before left there
   when ``accumulate`` is set, from where a ``GradList`` clips them.
 - ``layer_norm``, ``dropout`` and ``residual_norm`` are the same under
-  autograd.
+  autograd.  To capture a training step into a graph, capture the passes; a
+  captured autograd backward needs leaves that no eager graph holds.
 
 A matrix is a tensor whose last dimension is adjacent in memory and whose
 other dimensions lie at one distance (a contiguous tensor, a slice of the
@@ -68,6 +69,13 @@ if torch is not None:
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _counted(mask, device):
+    """The mask's structure; its counter has to be on the device that reads it."""
+    if mask.counter is not None and mask.counter.get_device() != device:
+        raise ValueError(f"the mask's counter is on {mask.counter.device}")
+    return mask.args
 
 
 def _matrix(x, name):
@@ -195,7 +203,8 @@ def dropout_forward(x, mask, out=None, stream=None):
         ldo = size
     else:
         ldo = _like(out, x, "out")
-    gclip_dropout_apply(x.data_ptr(), ld, out.data_ptr(), ldo, rows, size, code, mask.args, _raw_stream(device))
+    gclip_dropout_apply(x.data_ptr(), ld, out.data_ptr(), ldo, rows, size, code, _counted(mask, device),
+                        _raw_stream(device))
     return out
 
 
@@ -251,7 +260,7 @@ def _forward(x, residual, weight, bias, eps, mask, h, y, stats):
         ldh = _like(h, x, "out_h")
     gclip_residual_forward(GclipLayerForward(rows, size, code, wdt, eps, x.data_ptr(), ld, residual.data_ptr(), ldr,
                                              wp, bp, h.data_ptr(), ldh, y.data_ptr(), ldy, mp, rp),
-                           mask.args if mask is not None and mask.drops else None, _raw_stream(device))
+                           _counted(mask, device) if mask is not None and mask.drops else None, _raw_stream(device))
     return h, y, mean, rstd
 
 
@@ -341,7 +350,7 @@ def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, acc
                               x.data_ptr(), ld, mp, rp, wp, sp, ldds, xp, lddx, wgp, bgp, workspace.data_ptr(),
                               nbytes)
     if residual:
-        gclip_residual_backward(args, mask.args if mask is not None else None, _raw_stream(device))
+        gclip_residual_backward(args, _counted(mask, device) if mask is not None else None, _raw_stream(device))
     else:
         gclip_layernorm_backward(args, _raw_stream(device))
     return dx if second else dres, dres, dweight, dbias

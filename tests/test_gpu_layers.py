@@ -101,8 +101,9 @@ def test_every_row_length(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("rows,size", [(2, 64), (15, 768), (16, 96), (17, 8), (64, 300), (255, 64), (257, 33), (1000, 17),
-                                       (513, 768), (4099, 8), (2053, 128), (300, 2048), (100, 5000), (40, 16384)])
+@pytest.mark.parametrize("rows,size", [(2, 64), (15, 768), (16, 96), (17, 8), (64, 300), (255, 64), (257, 33),
+                                       (1000, 17), (513, 768), (4099, 8), (2053, 128), (300, 2048), (100, 5000),
+                                       (40, 16384)])
 def test_every_number_of_rows(rows, size, dtype):
     run_all(rows, size, dtype, "f32", "plain" if rows % 2 else "padded", seed=1)
 
@@ -209,8 +210,10 @@ def test_masks_differ_by_every_argument_and_counter():
     g = G()
     x = torch.ones(50, 300, device="cuda")
     counter = torch.tensor([4], dtype=torch.int32, device="cuda")
-    for m, k in ((mask(step=9), dict(step=9)), (mask(site=4), dict(site=4)), (mask(counter=counter), dict(step=STEP + 4)),
-                 (mask(step=0xFFFFFFFE, counter=counter), dict(step=2)), (mask().at(step=1, site=2), dict(step=1, site=2))):
+    for m, k in ((mask(step=9), dict(step=9)), (mask(site=4), dict(site=4)),
+                 (mask(counter=counter), dict(step=STEP + 4)),
+                 (mask(step=0xFFFFFFFE, counter=counter), dict(step=2)),
+                 (mask().at(step=1, site=2), dict(step=1, site=2))):
         assert np.array_equal(lu.values(g.dropout_forward(x, m)), factors(50, 300, **k))
 
 
@@ -520,7 +523,8 @@ def test_bad_tensors_are_refused():
         (v, lambda: g.layer_norm_forward(x, w[:31], w)), (v, lambda: g.layer_norm_forward(x, w.cpu())),
         (ty, lambda: g.layer_norm_forward(x, w.half(), w)), (ty, lambda: g.layer_norm_forward(x, w.half(), w.half())),
         (v, lambda: g.layer_norm_forward(x, torch.ones(64, device="cuda")[::2])),
-        (v, lambda: g.layer_norm_forward(x, w, w, out=y[:5])), (ty, lambda: g.layer_norm_forward(x, w, w, out=y.half())),
+        (v, lambda: g.layer_norm_forward(x, w, w, out=y[:5])),
+        (ty, lambda: g.layer_norm_forward(x, w, w, out=y.half())),
         (v, lambda: g.layer_norm_forward(torch.tensor(1.0, device="cuda"))),
         (g.GclipError, lambda: g.layer_norm_forward(x, w, w, 0.0)),
         (g.GclipError, lambda: g.layer_norm_forward(torch.ones(3, 0, device="cuda"))),
