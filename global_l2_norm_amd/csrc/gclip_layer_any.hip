@@ -107,8 +107,12 @@ __device__ __forceinline__ void unit_settled(u32x4& q, uint32_t c, uint32_t size
     q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
 }
 template <int DT>
+__device__ __forceinline__ uint64_t unit_place(uint32_t c, uint32_t size) {
+  return (uint64_t)(c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>;
+}
+template <int DT>
 __device__ __forceinline__ u32x4 unit_clamped(uint64_t row, uint32_t c, uint32_t size) {
-  return load16<DT, false>(row + (uint64_t)(c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>);
+  return load16<DT, false>(row + unit_place<DT>(c, size));
 }
 template <int DT>
 __device__ __forceinline__ void weight_unit(uint64_t w, int wdt, uint32_t c, uint32_t size, float (&v)[kUnit<DT>]) {
@@ -374,8 +378,17 @@ __global__ __launch_bounds__(kAnyThreads) void k_dropout(Rows x, Rows y, uint32_
   const uint64_t row = i / units;
   if (row >= rows) return;
   const uint32_t r = (uint32_t)row, u = (uint32_t)(i % units);
+  u32x4 q;
+  if (size % kUnit<DT> == 0) {
+    q = load16<DT, STREAMED>(x.at + r * x.ld + u * 16ull);
+  } else if (size >= kGroup) {
+    q = load16<DT, STREAMED>(x.at + r * x.ld + unit_place<DT>(u * kUnit<DT>, size));
+    unit_settled<DT>(q, u * kUnit<DT>, size);
+  } else {
+    q = load_unit<DT, STREAMED>(x.at + r * x.ld, u, size);
+  }
   float v[kUnit<DT>];
-  unpack_unit<DT>(load_unit<DT, STREAMED>(x.at + r * x.ld, u, size), v);
+  unpack_unit<DT>(q, v);
   drop_unit<DT>(d, drop_step(d), r, u * kUnit<DT>, v);
   store_unit<DT, true>(y.at + r * y.ld, u, size, pack_unit<DT>(v));
 }

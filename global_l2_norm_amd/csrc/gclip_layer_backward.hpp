@@ -63,6 +63,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
     for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = db[k][j] = 0.0f;
   }
   const float count = (float)a.size, inverse = 1.0f / count;
+  const bool full = a.size == kCols;
   uint32_t turn = 0;
 
   while (base < a.rows) {
@@ -73,13 +74,13 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      settle<DT, LANES, SURE>(ny[k], lane, k, a.size);
-      settle<DT, LANES, SURE>(nx[k], lane, k, a.size);
+      settle<DT, LANES, SURE>(ny[k], lane, k, a.size, full);
+      settle<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
       if (r >= a.rows) ny[k] = nx[k] = u32x4{0u, 0u, 0u, 0u};
       unpack_unit<DT>(ny[k], g[k]);
       unpack_unit<DT>(nx[k], n[k]);
       if constexpr (RES) {
-        settle<DT, LANES, SURE>(nh[k], lane, k, a.size);
+        settle<DT, LANES, SURE>(nh[k], lane, k, a.size, full);
         hh[k] = nh[k];
       }
 #pragma unroll
@@ -118,14 +119,14 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
       c2 = lanes_sum<LANES>(s2);
     }
     c1 = divided(c1, count, inverse);
-    c2 = divided(c2, count, inverse);
+    c2 = rstd * divided(c2, count, inverse);
     if (r < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const uint32_t c = column_of<DT>(lane, LANES, k);
         float v[kUnit<DT>];
 #pragma unroll
-        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = rstd * (g[k][j] - c1 - n[k][j] * c2);
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = __builtin_fmaf(rstd, g[k][j] - c1, -(n[k][j] * c2));
         if constexpr (RES) {
           float q[kUnit<DT>];
           unpack_unit<DT>(hh[k], q);
@@ -239,8 +240,22 @@ hipError_t backward_of(int shape, const BwdArgs& a, bool residual, const DropArg
                     : backward_shape<DT, s.lanes, s.units, sure_units(kBwdShapes<DT>, I), false>(a, residual, drop, st);
 }
 
+template <int DT, int I = 0>
+hipError_t backward_few(int shape, const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kFewBwdShapes) / sizeof(RowShape))) {
+    if (shape != I) return backward_few<DT, I + 1>(shape, a, residual, drop, st);
+  }
+  static_assert((uint64_t)kFewBwdRows * kFewBwdMax * 2 * 5 <= kStreamBytes, "few rows are not streamed");
+  constexpr RowShape s = kFewBwdShapes[I];
+  return backward_shape<DT, s.lanes, s.units, sure_units(kFewBwdShapes, I), false>(a, residual, drop, st);
+}
+
 template <int DT>
 hipError_t backward_rows(const BwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (DT != GCLIP_F32) {
+    if (few_bwd<DT>(a.rows, a.size))
+      return backward_few<DT>(row_shape_of(kFewBwdShapes, kUnit<DT>, a.size), a, residual, drop, st);
+  }
   return backward_of<DT>(row_shape_of(kBwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }
 

@@ -47,6 +47,19 @@ __device__ __forceinline__ uint32_t elem_bits(float v) {
   else return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Two values rounded to a 16-bit format, in one conversion.
+template <int DT>
+__device__ __forceinline__ uint32_t pair_bits(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  if constexpr (DT == GCLIP_F16) {
+    typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), f16x2));
+  } else {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+  }
+}
+
 template <int DT>
 __device__ __forceinline__ void unpack(const Raw8<DT>& r, float (&v)[8]) {
   if constexpr (DT == GCLIP_F32) {
@@ -69,7 +82,7 @@ __device__ __forceinline__ Raw8<DT> pack(const float (&v)[8]) {
     for (int k = 0; k < 8; ++k) r.q[k >> 2][k & 3] = __float_as_uint(v[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r.q[0][k] = elem_bits<DT>(v[2 * k]) | (elem_bits<DT>(v[2 * k + 1]) << 16);
+    for (int k = 0; k < 4; ++k) r.q[0][k] = pair_bits<DT>(v[2 * k], v[2 * k + 1]);
   }
   return r;
 }
@@ -362,7 +375,7 @@ __device__ __forceinline__ u32x4 pack_unit(const float (&v)[kUnit<DT>]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if constexpr (DT == GCLIP_F32) q[k] = __float_as_uint(v[k]);
-    else q[k] = elem_bits<DT>(v[2 * k]) | (elem_bits<DT>(v[2 * k + 1]) << 16);
+    else q[k] = pair_bits<DT>(v[2 * k], v[2 * k + 1]);
   }
   return q;
 }
@@ -404,9 +417,10 @@ __device__ __forceinline__ u32x4 load_columns(uint64_t row, uint32_t lane, int k
   return load16<DT, NT>(row + (c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>);
 }
 
+// full: the row fills its shape, the same for a whole launch.
 template <int DT, int LANES, int SURE>
-__device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t size) {
-  if (k < SURE) return;
+__device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t size, bool full = false) {
+  if (k < SURE || full) return;
   const uint32_t c = column_of<DT>(lane, LANES, k);
   if (c + kUnit<DT> > size)
     q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
@@ -492,10 +506,14 @@ __device__ __forceinline__ float divided(float t, float n, float inverse) {
   return __builtin_fmaf(__builtin_fmaf(-q, n, t), inverse, q);
 }
 
-// Sum over the lanes of a wave that hold the same column of its 64 / LANES rows.
+// Sum over the lanes of a wave that hold the same column of its 64 / LANES
+// rows, in the first LANES lanes.
 template <int LANES>
 __device__ __forceinline__ float across_rows(float v) {
-  if constexpr (LANES <= 8) v += permuted<0x128>(v);  // row_ror 8
+  if constexpr (LANES <= 1) v += permuted<0x121>(v);  // row_ror 1, 2, 4, 8
+  if constexpr (LANES <= 2) v += permuted<0x122>(v);
+  if constexpr (LANES <= 4) v += permuted<0x124>(v);
+  if constexpr (LANES <= 8) v += permuted<0x128>(v);
   if constexpr (LANES <= 16) {
     const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     v = __uint_as_float(s[0]) + __uint_as_float(s[1]);

@@ -63,6 +63,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
     weight_columns<DT, LANES, SURE>(a.bias, a.wdt, lane, k, a.size, 0.0f, b[k]);
   }
   const float count = (float)a.size, inverse = 1.0f / count;
+  const bool full = a.size == LANES * NV * kUnit<DT>;
 
   while (base < a.rows) {
     const uint32_t r = base + slot;
@@ -71,11 +72,11 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const uint32_t c = column_of<DT>(lane, LANES, k);
-      settle<DT, LANES, SURE>(nx[k], lane, k, a.size);
+      settle<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
       unpack_unit<DT>(nx[k], v[k]);
       if constexpr (RES) {
         float q[kUnit<DT>];
-        settle<DT, LANES, SURE>(nr[k], lane, k, a.size);
+        settle<DT, LANES, SURE>(nr[k], lane, k, a.size, full);
         unpack_unit<DT>(nr[k], q);
         if constexpr (DROP) drop_unit<DT>(d, step, r, c, v[k]);
 #pragma unroll
@@ -109,7 +110,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const uint32_t c = column_of<DT>(lane, LANES, k);
-        if (k < SURE || c + kUnit<DT> <= a.size) {
+        if (k < SURE || full || c + kUnit<DT> <= a.size) {
 #pragma unroll
           for (uint32_t j = 0; j < kUnit<DT>; ++j) {
             const float t = __builtin_fmaf(v[k][j], scale, -mean);

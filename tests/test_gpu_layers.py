@@ -109,12 +109,27 @@ def test_every_number_of_rows(rows, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("shape", [64, 128, 256, 512, 768, 1024, 1536, 2048, 4096, 6144, 8192, 12288])
+@pytest.mark.parametrize("shape", [8, 16, 32, 64, 128, 192, 256, 384, 512, 768, 1024, 1536, 2048, 4096, 6144, 8192,
+                                   12288])
 def test_ragged_ends_in_every_wave(shape, dtype):
     """Rows that a few columns make too long for a register shape: the end of
     each lies alone in a unit, in every wave of a workgroup."""
     for extra in (1, 3, 6):
         run_all(37, shape + extra, dtype, "f32", "padded", seed=6)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", [8, 15, 24, 33, 64, 97, 128, 129, 190, 193, 256, 257, 380, 385, 512, 513, 700, 768, 769,
+                                  1024, 1025, 1300, 1537, 2040])
+def test_shapes_of_many_rows(size, dtype):
+    """Above the numbers of rows that take other shapes."""
+    run_all(2085, size, dtype, "f32", "padded" if size % 2 else "plain", seed=7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [2049, 2500, 3100, 4097, 5001, 6145, 8192])
+def test_long_shapes_of_many_rows(size, dtype):
+    run_all(530, size, dtype, dtype, "padded" if size % 2 else "plain", seed=8)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -344,6 +359,44 @@ def test_rows_that_lie_past_4_gib(dtype):
         assert torch.equal(u, v)
     assert torch.equal(g.dropout_forward(small[0], mask()),
                        g.dropout_forward(far[0].copy_(small[0]), mask(), out=far[0]))
+
+
+@pytest.mark.parametrize("rows,size,dtype", [(16384, 2048, "bf16"), (16400, 2047, "f16"), (9000, 2048, "f32"),
+                                             (13000, 1537, "f32"), (300000, 64, "bf16"), (2300, 8192, "f32")])
+def test_calls_that_stream(rows, size, dtype):
+    """Calls that move more than the caches hold take other loads and stores:
+    the same bits as calls on parts of the rows, the weights' gradients as in
+    binary64 (any order: rows u of the absolute values each)."""
+    import torch
+    g = G()
+    t = lu.torch_type(dtype)
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x, r, dy, dh = (torch.randn(rows, size, generator=gen, device="cuda").to(t) for _ in range(4))
+    w, b = vectors(size, "f32", np.random.default_rng(1))
+    m = mask()
+    f = g.dropout_forward(torch.ones(rows, size, device="cuda"), m)
+    h, y, mean, rstd = g.residual_norm_forward(x, r, w, b, EPS, m)
+    assert torch.equal(h, (r.float() + torch.where(f != 0, x.float() * f, 0)).to(t))
+    dx, dres, dw, db = g.residual_norm_backward(dy, dh, h, mean, rstd, w, m)
+    one, _, _, _ = g.residual_norm_backward(dy, dh, h, mean, rstd, w)
+    assert torch.equal(one, dres)
+    near = 2.1 * lu.HALF[dtype] * (f * dres.float()).abs() + 2 * lu.TINY[dtype]
+    assert ((dx.float() - f * dres.float()).abs() <= near).all() and not dx[f == 0].any()
+    at = 0
+    while at < rows:  # parts of the rows, none of them few
+        to = rows if rows - at < 2 * (rows // 5) else at + rows // 5
+        part = slice(at, to)
+        py, pm, ps = g.layer_norm_forward(h[part], w, b, EPS)
+        assert torch.equal(py, y[part]) and torch.equal(pm, mean[part]) and torch.equal(ps, rstd[part]), at
+        pd, _, _, _ = g.residual_norm_backward(dy[part], dh[part], h[part], mean[part], rstd[part], w)
+        assert torch.equal(pd, dres[part]), at
+        at = to
+    n = (h.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    for got, terms in ((dw, dy.double() * n), (db, dy.double())):
+        tol = (rows + 4) * lu.U * terms.abs().sum(0)
+        assert ((got.double() - terms.sum(0)).abs() <= tol).all()
+    big = g.dropout_forward(torch.cat([x, x, x]), m)
+    assert torch.equal(big[:rows], g.dropout_forward(x, m))
 
 
 @pytest.mark.parametrize("rows,size,dtype", [(4099, 768, "f32"), (20000, 64, "bf16"), (3000, 2048, "bf16"),
