@@ -167,3 +167,26 @@ def test_structures_have_the_sizes_of_the_header():
     assert ctypes.sizeof(_lib.GclipDropout) == 32
     assert ctypes.sizeof(_lib.GclipLayerForward) == 17 * 8 - 8
     assert ctypes.sizeof(_lib.GclipLayerBackward) == 23 * 8 - 16
+
+
+def test_tensors_and_masks_that_no_gpu_sees_are_refused():
+    import torch
+
+    import global_l2_norm_amd as G
+    x, w = torch.ones(4, 16), torch.ones(16)
+    m = G.DropoutMask(0.5, 1, step=3, site=4)
+    for call in (lambda: G.layer_norm_forward(x, w), lambda: G.residual_norm_forward(x, x, w),
+                 lambda: G.layer_norm_backward(x, x, w[:4], w[:4], w), lambda: G.dropout_forward(x, m),
+                 lambda: G.layer_norm(x, w), lambda: G.dropout(x.requires_grad_(), m)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        G.layer_norm_forward(x.double())
+    for p, seed, kw in ((-1e-9, 0, {}), (1.0 + 1e-9, 0, {}), (float("nan"), 0, {}), (0.5, -1, {}), (0.5, 1 << 64, {}),
+                        (0.5, 0, dict(step=-1)), (0.5, 0, dict(step=1 << 32)), (0.5, 0, dict(site=1 << 32)),
+                        (0.5, 0, dict(counter=torch.zeros(1, dtype=torch.int32)))):
+        with pytest.raises(ValueError):
+            G.DropoutMask(p, seed, **kw)
+    other = m.at(site=9)
+    assert (other.p, other.seed, other.step, other.site) == (0.5, 1, 3, 9)
+    assert G.DropoutMask(2.0 ** -17, 0).drops and not G.DropoutMask(2.0 ** -17 - 1e-9, 0).drops
