@@ -18,12 +18,12 @@ namespace gclip {
 // unit -- leaves one part of them.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
 //
-// Bound by memory: 16384 x 2048 in bfloat16 takes 35.3 us, 5.7 TB/s of two
-// reads and a write, and 4.6 us for the join of the parts (4 MB written and
-// read); the residual step's with dropout 57.2 us, 5.9 TB/s; 8192 x 768 in
-// binary32 14.0 us and 3.9.  Two workgroups a unit leave twice the parts: 22.6
-// -> 26.7 us for the last in all.  Rows that fill half of a wave's lanes
-// (131071 x 64: 11.9 us, 4.2 TB/s) are bound by the operations of a row.
+// Bound by memory: 16384 x 2048 in bfloat16 takes 34.7 us, 5.8 TB/s of two
+// reads and a write, and 4.8 us for the join of the parts (4 MB written and
+// read); the residual step's with dropout 54.3 us, 6.2 TB/s; 8192 x 768 in
+// binary32 13.8 us and 4.0.  Two workgroups a unit leave twice the parts: 22.6
+// -> 26.7 us for the last in all, then.  Rows that share a wave
+// (131071 x 64: 11.1 us, 4.5 TB/s) are bound by the operations of a row.
 template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
   constexpr uint32_t kBwdThreads = bwd_threads(NV * kUnit<DT>);
