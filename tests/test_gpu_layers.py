@@ -144,6 +144,28 @@ def test_one_row_for_all(rows, size, dtype):
     run_all(rows, size, dtype, "f32", "one row", seed=3)
 
 
+@pytest.mark.parametrize("seed", range(60))
+def test_random_cases(seed):
+    """Seeded shapes, formats, layouts and probabilities over the whole range;
+    the weights' gradients also into buffers of the rows' format, added to."""
+    rng = np.random.default_rng(1000 + seed)
+    size = int(round(np.exp(rng.uniform(0, np.log(20000)))))
+    rows = int(round(np.exp(rng.uniform(0, np.log(min(60000, max(2, 600000 // size)))))))
+    dtype = str(rng.choice(["f32", "f16", "bf16"]))
+    layout = str(rng.choice(["plain", "padded", "shifted", "one row"]))
+    run_all(rows, size, dtype, str(rng.choice(["f32", dtype])), layout, p=float(rng.uniform(0, 1)), seed=seed,
+            scale=float(rng.uniform(0.2, 3)), shift=float(rng.uniform(-3, 3)))
+    g = G()
+    x, dy = (lu.matrix(rng.standard_normal((rows, size)), dtype, layout) for _ in range(2))
+    w, b = vectors(size, dtype, rng)
+    y, mean, rstd = g.layer_norm_forward(x, w, b, EPS)
+    buf = vectors(size, dtype, rng)
+    start = [lu.values(t) for t in buf]
+    dx, dw, db = g.layer_norm_backward(dy, x, mean, rstd, w, dweight=buf[0], dbias=buf[1], accumulate=True)
+    lu.check_norm_gradient(lu.values(dx), lu.values(dw), lu.values(db), lu.values(dy), lu.values(x), lu.values(mean),
+                           lu.values(rstd), lu.values(w), dtype, dtype, "added", dw0=start[0], db0=start[1])
+
+
 @pytest.mark.parametrize("p", [0.0, 1e-6, 2.0 ** -16, 0.5, 0.999999, 1.0])
 def test_probabilities(p):
     for size in (100, 3001):
