@@ -95,31 +95,10 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
     }
     const uint32_t next = base + gridDim.x * kRows;
     if (next < a.rows) fetch(next);
-    float c1, c2;
-    if constexpr (LANES > 64) {
-      // both sums behind one barrier; the next row's use the other words
-      const uint32_t wave = threadIdx.x >> 6, own = wave / (LANES / 64) * (LANES / 64);
-      s1 = lanes_sum<64>(s1);
-      s2 = lanes_sum<64>(s2);
-      if ((threadIdx.x & 63) == 0) {
-        red[turn][0][wave] = s1;
-        red[turn][1][wave] = s2;
-      }
-      __syncthreads();
-      c1 = red[turn][0][own];
-      c2 = red[turn][1][own];
-#pragma unroll
-      for (uint32_t i = 1; i < LANES / 64; ++i) {
-        c1 += red[turn][0][own + i];
-        c2 += red[turn][1][own + i];
-      }
-      turn ^= 1u;
-    } else {
-      c1 = lanes_sum<LANES>(s1);
-      c2 = lanes_sum<LANES>(s2);
-    }
-    c1 = divided(c1, count, inverse);
-    c2 = rstd * divided(c2, count, inverse);
+    // the next row's sums use the other words
+    row_sums<LANES>(s1, s2, red[turn][0], red[turn][1]);
+    turn ^= 1u;
+    const float c1 = divided(s1, count, inverse), c2 = rstd * divided(s2, count, inverse);
     if (r < a.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {

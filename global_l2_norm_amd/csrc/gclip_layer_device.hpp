@@ -499,6 +499,29 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
+// Two of them behind one barrier.
+template <int LANES>
+__device__ __forceinline__ void row_sums(float& p, float& q, float* redp, float* redq) {
+  p = lanes_sum<(LANES < 64 ? LANES : 64)>(p);
+  q = lanes_sum<(LANES < 64 ? LANES : 64)>(q);
+  if constexpr (LANES > 64) {
+    constexpr int kWavesOfRow = LANES / 64;
+    const uint32_t wave = threadIdx.x >> 6, own = wave / kWavesOfRow * kWavesOfRow;
+    if ((threadIdx.x & 63) == 0) {
+      redp[wave] = p;
+      redq[wave] = q;
+    }
+    __syncthreads();
+    p = redp[own];
+    q = redq[own];
+#pragma unroll
+    for (int i = 1; i < kWavesOfRow; ++i) {
+      p += redp[own + i];
+      q += redq[own + i];
+    }
+  }
+}
+
 // t / n by n's reciprocal and one correction, exact where n divides t (a
 // constant row's mean is its value), in a quarter of a division's operations.
 __device__ __forceinline__ float divided(float t, float n, float inverse) {

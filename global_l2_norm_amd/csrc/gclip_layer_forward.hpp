@@ -37,7 +37,7 @@ template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAME
 __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
   constexpr int kThreads = kFwdThreads<LANES>;
   const uint32_t at_once = LANES > 64 ? kThreads / LANES : blockDim.x / LANES;  // rows of a workgroup
-  __shared__ float red[2][kThreads / 64];
+  __shared__ float red[3][kThreads / 64];
   const uint32_t lane = threadIdx.x % LANES;
   uint32_t slot = threadIdx.x / LANES;
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
@@ -95,9 +95,13 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
       }
     }
 
-    // the mean, then the squares of what is left of it; rows whose sums leave
-    // binary32 go through this again, scaled by a power of two (so does a row
-    // with a NaN or an infinity, to no effect)
+    // the mean, then the squares of what is left of it and, where the sum may
+    // round, what is left itself, which takes the sum's own error off: a
+    // constant row's mean is its value, and its y the bias (a row's sum of
+    // equal bfloat16 elements is exact up to 2^16 of them, of binary16 ones up
+    // to 2^13); rows whose sums leave binary32 go through this again, scaled
+    // by a power of two (so does a row with a NaN or an infinity, to no effect)
+    constexpr bool kRounds = DT == GCLIP_F32 || (DT == GCLIP_F16 && LANES * NV * kUnit<DT> > 8192);
     float scale = 1.0f, mean, var;
     for (;;) {
       float s = 0.0f;
@@ -107,6 +111,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
         for (uint32_t j = 0; j < kUnit<DT>; ++j) s = __builtin_fmaf(v[k][j], scale, s);
       mean = divided(row_sum<LANES>(s, red[0]), count, inverse);
       s = 0.0f;
+      float rest = 0.0f;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const uint32_t c = column_of<DT>(lane, LANES, k);
@@ -114,6 +119,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
           for (uint32_t j = 0; j < kUnit<DT>; ++j) {
             const float t = __builtin_fmaf(v[k][j], scale, -mean);
+            if (kRounds) rest += t;
             s = __builtin_fmaf(t, t, s);
           }
         } else {
@@ -124,11 +130,20 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 #pragma unroll
           for (uint32_t j = 0; j < kUnit<DT>; ++j) {
             const float t = j < left ? __builtin_fmaf(v[k][j], scale, -mean) : 0.0f;
+            if (kRounds) rest += t;
             s = __builtin_fmaf(t, t, s);
           }
         }
       }
-      var = divided(row_sum<LANES>(s, red[1]), count, inverse);
+      if constexpr (kRounds) {
+        row_sums<LANES>(s, rest, red[1], red[2]);
+        rest = divided(rest, count, inverse);
+        mean += rest;
+        var = __builtin_fmaf(-rest, rest, divided(s, count, inverse));
+        if (var < 0.0f) var = 0.0f;  // of a constant row, by rounding
+      } else {
+        var = divided(row_sum<LANES>(s, red[1]), count, inverse);
+      }
       const bool over = !(var <= 0x1.fffffep+127f) && scale == 1.0f;
       if (!(LANES > 64 ? over : __any(over))) break;
       if (over) scale = 0x1p-96f;

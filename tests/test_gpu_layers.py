@@ -205,6 +205,33 @@ def test_rows_without_spread(dtype, size):
     assert not dx.any() and not dw.any() and (db == 4).all()
 
 
+@pytest.mark.parametrize("value", [0.1, 12345.678, -1e6 / 3, 3e38])
+@pytest.mark.parametrize("size", [5, 64, 100, 768, 3001, 8192, 40000])
+def test_constant_rows_of_any_value(value, size):
+    """The mean is the value itself, whatever its binary32 sums round to, so y
+    is the bias exactly."""
+    import torch
+    g = G()
+    w, b = vectors(size, "f32", np.random.default_rng(2))
+    for rows in (3, 600):
+        x = torch.full((rows, size), value, device="cuda")
+        y, mean, _ = g.layer_norm_forward(x, w, b, EPS)
+        assert torch.equal(y, b.expand_as(y)) and (mean == x[0, 0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("value", [0.1, 333.25, 60000.0])
+@pytest.mark.parametrize("size", [5, 100, 768, 2047, 8192, 12287, 16384, 40000])
+def test_constant_rows_of_16_bits(value, dtype, size):
+    import torch
+    g = G()
+    w, b = vectors(size, "f32", np.random.default_rng(2))
+    for rows in (3, 600):
+        x = torch.full((rows, size), value, dtype=lu.torch_type(dtype), device="cuda")
+        y, mean, _ = g.layer_norm_forward(x, w, b, EPS)
+        assert torch.equal(y, b.to(y.dtype).expand_as(y)) and (mean == x[0, 0].float()).all()
+
+
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("size", [9, 64, 777, 3000, 40000])
 def test_nan_and_infinity_stay_in_their_rows(dtype, size):
