@@ -106,6 +106,11 @@ __device__ __forceinline__ void unit_settled(u32x4& q, uint32_t c, uint32_t size
   if (c + kUnit<DT> > size)
     q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
 }
+// Past the row's end other elements of the row, see settle_round().
+template <int DT>
+__device__ __forceinline__ void unit_settled_round(u32x4& q, uint32_t c, uint32_t size) {
+  if (c < size && c + kUnit<DT> > size) q = moved_down<DT, true>(q, kUnit<DT> - size % kUnit<DT>);
+}
 template <int DT>
 __device__ __forceinline__ uint64_t unit_place(uint32_t c, uint32_t size) {
   return (uint64_t)(c + kUnit<DT> <= size ? c : size - kUnit<DT>) * kElem<DT>;
@@ -144,7 +149,7 @@ __global__ __launch_bounds__(kLongThreads) void k_row_means_long(BwdArgs a) {
       float g[kUnit<DT>], n[kUnit<DT>], w[kUnit<DT>];
       weight_unit<DT>(a.weight, a.wdt, c, a.size, w);
       unit_settled<DT>(p, c, a.size);
-      unit_settled<DT>(q, c, a.size);
+      unit_settled_round<DT>(q, c, a.size);
       unpack_unit<DT>(p, g);
       unpack_unit<DT>(q, n);
       float t1 = 0.0f, t2 = 0.0f;
@@ -322,8 +327,8 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_grad_short(BwdArgs a, Drop
     const float mean = a.mean[r], rstd = a.rstd[r];
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 7; ++k) {
-      n[k] = (n[k] - mean) * rstd;
+    for (uint32_t k = 0; k < 7; ++k) {
+      n[k] = k < a.size ? (n[k] - mean) * rstd : 0.0f;  // past the end: see settle_round()
       dw[k] = __builtin_fmaf(g[k], n[k], dw[k]);
       db[k] += g[k];
       g[k] *= w[k];

@@ -41,7 +41,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
   float nmean, nrstd;
   uint32_t base = blockIdx.x * kRows;
   const auto fetch = [&](uint32_t first) {
-    // rows past the end are read as the last one; they count for nothing
+    // rows past the end are read as the last one, with a dy of zeros
     const uint32_t r = min(first + slot, a.rows - 1);
     const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld, dh = a.dh.at + r * a.dh.ld;
     nmean = a.mean[r];
@@ -75,8 +75,8 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       settle<DT, LANES, SURE>(ny[k], lane, k, a.size, full);
-      settle<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
-      if (r >= a.rows) ny[k] = nx[k] = u32x4{0u, 0u, 0u, 0u};
+      settle_round<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
+      if (r >= a.rows) ny[k] = u32x4{0u, 0u, 0u, 0u};  // n stays the last row's
       unpack_unit<DT>(ny[k], g[k]);
       unpack_unit<DT>(nx[k], n[k]);
       if constexpr (RES) {

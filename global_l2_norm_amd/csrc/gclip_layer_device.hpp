@@ -132,17 +132,18 @@ __device__ __forceinline__ void store8(uint64_t a, const Raw8<DT>& r) {
   }
 }
 
-// The elements of 16 or 32 bytes moved down by n places, zeros after them.
-// n is the same in every lane (what a row's ragged end lacks), and moves by
+// The elements of 16 or 32 bytes moved down by n places, zeros after them or,
+// with ROUND, those that were moved out.  n is the same in every lane (what a row's ragged end lacks), and moves by
 // words and half words: a 64-bit shift by a vector register gave wrong bits
 // on gfx950 when that register was the last one of the wave's allocation.
-template <int DT>
+template <int DT, bool ROUND = false>
 __device__ __forceinline__ u32x4 moved_down(u32x4 q, uint32_t n) {
   const uint32_t bits = __builtin_amdgcn_readfirstlane(n * 8u * kElem<DT>);
-  if (bits & 64u) q = u32x4{q[2], q[3], 0u, 0u};
-  if (bits & 32u) q = u32x4{q[1], q[2], q[3], 0u};
+  if (bits & 64u) q = u32x4{q[2], q[3], ROUND ? q[0] : 0u, ROUND ? q[1] : 0u};
+  if (bits & 32u) q = u32x4{q[1], q[2], q[3], ROUND ? q[0] : 0u};
   if (DT != GCLIP_F32 && (bits & 16u))
-    q = u32x4{(q[0] >> 16) | (q[1] << 16), (q[1] >> 16) | (q[2] << 16), (q[2] >> 16) | (q[3] << 16), q[3] >> 16};
+    q = u32x4{(q[0] >> 16) | (q[1] << 16), (q[1] >> 16) | (q[2] << 16), (q[2] >> 16) | (q[3] << 16),
+              (q[3] >> 16) | (ROUND ? q[0] << 16 : 0u)};
   return q;
 }
 
@@ -424,6 +425,17 @@ __device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t 
   const uint32_t c = column_of<DT>(lane, LANES, k);
   if (c + kUnit<DT> > size)
     q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
+}
+
+// As settle(), but past the row's end are other elements of the row, not
+// zeros: for the matrix that was normed, where a zero's (0 - mean) rstd may
+// be infinite though every element's is finite, and nothing times that is NaN
+// in the row's sums.
+template <int DT, int LANES, int SURE>
+__device__ __forceinline__ void settle_round(u32x4& q, uint32_t lane, int k, uint32_t size, bool full) {
+  if (k < SURE || full) return;
+  const uint32_t c = column_of<DT>(lane, LANES, k);
+  if (c < size && c + kUnit<DT> > size) q = moved_down<DT, true>(q, kUnit<DT> - size % kUnit<DT>);
 }
 
 template <int DT, int LANES, int SURE, bool NT>
