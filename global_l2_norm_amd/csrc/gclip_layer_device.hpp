@@ -491,6 +491,15 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// The sum of a row's waves, from the words that they left.
+template <int LANES>
+__device__ __forceinline__ float waves_sum(const float* own) {
+  float v = own[0];
+#pragma unroll
+  for (int i = 1; i < LANES / 64; ++i) v += own[i];
+  return v;
+}
+
 // Sum over the LANES lanes of a row, the same bits in all of them.  Rows of
 // more than a wave meet in `red`, a word for each wave of the workgroup; one
 // barrier, so two sums in a row need two `red`s, and the third may use the
@@ -503,10 +512,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     const uint32_t wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0) red[wave] = v;
     __syncthreads();
-    const float* own = red + wave / kWavesOfRow * kWavesOfRow;
-    v = own[0];
-#pragma unroll
-    for (int i = 1; i < kWavesOfRow; ++i) v += own[i];
+    v = waves_sum<LANES>(red + wave / kWavesOfRow * kWavesOfRow);
   }
   return v;
 }

@@ -8,9 +8,12 @@
 namespace gclip {
 
 // The most threads of a workgroup: four waves, of which rows of up to a wave
-// share one; workgroups of a wave each where the rows are few.
-template <int LANES>
-constexpr int kFwdThreads = LANES > 256 ? LANES : 256;
+// share one; workgroups of a wave each where the rows are few.  Two rows of
+// 128 lanes share one in 16-bit formats (2000 x 2500 residual with dropout
+// 11.7 us, 512 x 1000 4.0; a workgroup each: 12.5 and 4.2), and have one each
+// in binary32 (256 x 384 norm 3.1 us; shared: 3.2).
+template <int DT, int LANES>
+constexpr int kFwdThreads = LANES > 256 || (LANES == 128 && DT == GCLIP_F32) ? LANES : 256;
 
 // Workgroups of four waves for each compute unit, by the columns that a lane
 // holds: as many as its registers let run at once, so that each goes through
@@ -34,8 +37,8 @@ constexpr uint32_t fwd_workgroups(uint32_t columns) { return columns <= 8 ? 8 : 
 // of the next row out of a branch, which would be waited for at its end
 // (residual step: 53.7 us against 46.0).
 template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
-__global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, DropArgs d) {
-  constexpr int kThreads = kFwdThreads<LANES>;
+__global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs a, DropArgs d) {
+  constexpr int kThreads = kFwdThreads<DT, LANES>;
   const uint32_t at_once = LANES > 64 ? kThreads / LANES : blockDim.x / LANES;  // rows of a workgroup
   __shared__ float red[3][kThreads / 64];
   const uint32_t lane = threadIdx.x % LANES;
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
     // by a power of two (so does a row with a NaN or an infinity, to no effect)
     constexpr bool kRounds = DT == GCLIP_F32 || (DT == GCLIP_F16 && LANES * NV * kUnit<DT> > 8192);
     float scale = 1.0f, mean, var;
-    for (;;) {
+    for (bool first = true;; first = false) {
       float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
@@ -144,9 +147,22 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
       } else {
         var = divided(row_sum<LANES>(s, red[1]), count, inverse);
       }
-      const bool over = !(var <= 0x1.fffffep+127f) && scale == 1.0f;
-      if (!(LANES > 64 ? over : __any(over))) break;
-      if (over) scale = 0x1p-96f;
+      if (!first) break;
+      // rows that meet go through it again together, if one of them has to:
+      // those of a wave, or of a workgroup, whose barriers all of its waves
+      // have to reach equally often
+      const auto leaves = [](float t) { return !(t <= 0x1.fffffep+127f); };
+      bool again = leaves(var);
+      if constexpr (LANES > 64) {
+        static_assert(kThreads == LANES || !kRounds, "the sum of squares alone decides");
+        for (int i = 0; kThreads > LANES && i < kThreads / 64; i += LANES / 64)
+          again |= leaves(divided(waves_sum<LANES>(red[1] + i), count, inverse));
+        again = __builtin_amdgcn_readfirstlane(again);
+      } else {
+        again = __any(again);
+      }
+      if (!again) break;
+      if (leaves(var)) scale = 0x1p-96f;
     }
     float rstd = scale / sqrtf(var + a.eps * scale * scale);
     if (scale != 1.0f) {
@@ -173,7 +189,7 @@ __global__ __launch_bounds__(kFwdThreads<LANES>) void k_norm_rows(FwdArgs a, Dro
 template <int DT, int LANES, int NV, int SURE, bool STREAMED>
 hipError_t forward_shape(const FwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   // workgroups of a wave until there are four for each compute unit
-  const uint32_t threads = LANES <= 64 && a.rows < 1024 * (64 / LANES) ? 64 : kFwdThreads<LANES>;
+  const uint32_t threads = LANES <= 64 && a.rows < 1024 * (64 / LANES) ? 64 : kFwdThreads<DT, LANES>;
   const uint32_t at_once = threads / LANES;
   const uint32_t most = 256u * fwd_workgroups(NV * kUnit<DT>) * 256 / threads;
   const uint32_t need = (a.rows + at_once - 1) / at_once;

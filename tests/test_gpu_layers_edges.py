@@ -41,3 +41,34 @@ def test_gradients_of_rows_without_spread(size, rows, dtype):
         assert not dw.any(), what + " residual dweight"
         lu.check_norm_gradient(lu.values(dx), lu.values(dw), lu.values(db), dyv, xv, mv, sv, wv, dtype, "f32",
                                what + " residual", dhv, f, lu.values(dres))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [9, 40, 64, 300, 1000, 2500, 5000, 9001, 16000])
+def test_some_rows_overflow_among_many(size, dtype):
+    """Rows whose squares leave binary32 and rows with a NaN among thousands,
+    so that they share a wave or a workgroup with rows that do neither, over
+    several turns: those keep their bits, the former are right."""
+    import torch
+    g, rng = G(), np.random.default_rng(size)
+    rows = max(2100, min(20000, 12_000_000 // size))
+    gen = torch.Generator(device="cuda").manual_seed(size)
+    good = torch.randn(rows, size, generator=gen, device="cuda").to(lu.torch_type(dtype))
+    x = good.clone()
+    big = torch.from_numpy(rng.permutation(rows)[:rows // 5]).cuda()
+    x[big] *= 2.0 ** 90
+    bad = torch.from_numpy(rng.permutation(rows)[:rows // 50]).cuda()
+    x[bad, size // 2] = float("nan")
+    w, b = vectors(size, "f32", rng)
+    y0, m0, s0 = g.layer_norm_forward(good, w, b, EPS)
+    y, m, s = g.layer_norm_forward(x, w, b, EPS)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    rest[big] = rest[bad] = False
+    assert torch.equal(y[rest], y0[rest]) and torch.equal(m[rest], m0[rest]) and torch.equal(s[rest], s0[rest])
+    assert y[bad].isnan().all() and m[bad].isnan().all()
+    kept = torch.zeros_like(rest)
+    kept[big] = True
+    kept[bad] = False
+    at = kept.nonzero()[:, 0][:300]
+    lu.check_norm(lu.values(x[at]), lu.values(y[at]), lu.values(m[at]), lu.values(s[at]), lu.values(w), lu.values(b),
+                  EPS, dtype, f"{rows} x {size} {dtype}")
