@@ -99,11 +99,12 @@ __global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs 
     }
 
     // the mean, then the squares of what is left of it and, where the sum may
-    // round, what is left itself, which takes the sum's own error off: a
-    // constant row's mean is its value, and its y the bias (a row's sum of
-    // equal bfloat16 elements is exact up to 2^16 of them, of binary16 ones up
-    // to 2^13); rows whose sums leave binary32 go through this again, scaled
-    // by a power of two (so does a row with a NaN or an infinity, to no effect)
+    // round, what is left itself: in a row of little spread it takes the sum's
+    // own error off, so a constant row's mean is its value, and its y the bias
+    // (a row's sum of equal bfloat16 elements is exact up to 2^16 of them, of
+    // binary16 ones up to 2^13); rows whose sums leave binary32 go through
+    // this again, scaled by a power of two (so does a row with a NaN or an
+    // infinity, to no effect)
     constexpr bool kRounds = DT == GCLIP_F32 || (DT == GCLIP_F16 && LANES * NV * kUnit<DT> > 8192);
     float scale = 1.0f, mean, var;
     for (bool first = true;; first = false) {
@@ -141,9 +142,16 @@ __global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs 
       if constexpr (kRounds) {
         row_sums<LANES>(s, rest, red[1], red[2]);
         rest = divided(rest, count, inverse);
-        mean += rest;
-        var = __builtin_fmaf(-rest, rest, divided(s, count, inverse));
-        if (var < 0.0f) var = 0.0f;  // of a constant row, by rounding
+        var = divided(s, count, inverse);
+        // little: at most an eighth of the mean, where the subtractions are
+        // exact but for outliers.  Elsewhere their roundings are more than
+        // what the sum's own come to (twice the mean's error in rows around
+        // zero).
+        if (var <= mean * (mean * 0x1p-6f)) {
+          mean += rest;
+          var = __builtin_fmaf(-rest, rest, var);
+          if (var < 0.0f) var = 0.0f;  // of a constant row, by rounding
+        }
       } else {
         var = divided(row_sum<LANES>(s, red[1]), count, inverse);
       }

@@ -72,3 +72,55 @@ def test_some_rows_overflow_among_many(size, dtype):
     at = kept.nonzero()[:, 0][:300]
     lu.check_norm(lu.values(x[at]), lu.values(y[at]), lu.values(m[at]), lu.values(s[at]), lu.values(w), lu.values(b),
                   EPS, dtype, f"{rows} x {size} {dtype}")
+
+
+@pytest.mark.parametrize("size,lanes,chain", [(768, 64, 12), (64, 16, 4), (512, 64, 8)])
+def test_mean_of_binary32_rows_around_zero(size, lanes, chain):
+    """A row's mean is off by the roundings of its sum alone.  Each of them is
+    at most u times its partial sum and taken as uniform there, so their
+    root mean square is at most that of all the partial sums times u / sqrt 3
+    (lanes add `chain` elements each, then pairs); the division adds one.
+    4000 rows give the root mean square to 1.1 % (one deviation): 1.06 stands
+    for five of them."""
+    g, rng = G(), np.random.default_rng(size)
+    rows = 4000
+    x = lu.matrix(rng.standard_normal((rows, size)), "f32")
+    _, mean, _ = g.layer_norm_forward(x, eps=EPS)
+    v = lu.values(x)
+    part = np.cumsum(v.reshape(rows, chain // 4, lanes, 4).transpose(0, 2, 1, 3).reshape(rows, lanes, chain), axis=2)
+    squares = (part[:, :, 1:] ** 2).sum((1, 2))
+    s = part[:, :, -1]
+    while s.shape[1] > 1:
+        s = s[:, 0::2] + s[:, 1::2]
+        squares += (s ** 2).sum(1)
+    exact = v.mean(1)
+    unit = lu.U * np.sqrt(squares / size ** 2 + exact ** 2)
+    ratio = np.sqrt((((lu.values(mean) - exact) / unit) ** 2).mean())
+    assert ratio <= 1.06 / np.sqrt(3), ratio
+
+
+@pytest.mark.parametrize("rows", [3, 600])
+@pytest.mark.parametrize("size", [5, 8, 64, 100, 771, 1111, 2500, 8192, 10001, 40000])
+def test_spread_of_almost_constant_rows(size, rows):
+    """Binary32 rows whose elements are 0 to 3 steps above a large value.  The
+    stored mean is its nearest neighbour and off by half a step at most, the
+    subtractions from it are exact, and the squares are taken about the mean
+    that they have themselves, so rstd is off by the sum's roundings as of any
+    row (twice: the squares about the stored mean are at most twice those
+    about the mean, for a deviation of half a step or more).  A row without
+    spread has rstd = 1 / sqrt(eps) to four roundings."""
+    import torch
+    g, rng = G(), np.random.default_rng([size, rows])
+    for value, step in ((1e9, 64.0), (-123456.0, 2.0 ** -7), (1e30, 2.0 ** 76)):
+        base = np.full((rows, size), np.float64(np.float32(value)))
+        x = base + step * rng.integers(0, 4, (rows, size))
+        x[0] = base[0]
+        t = lu.matrix(x, "f32")
+        assert np.array_equal(lu.values(t), x)
+        _, mean, rstd = g.layer_norm_forward(t, eps=EPS)
+        _, wm, wr = L.norm(x, 1.0, 0.0, EPS)
+        lu.within(lu.values(mean), wm, step / 2 * (1 + 1e-6), f"{value} {size} mean")
+        spread = x.std(1)
+        ok = (spread >= step / 2) | (spread == 0)
+        tol = np.where(spread == 0, 4 * lu.U, (lu.PATH + 10) * lu.U) * wr
+        lu.within(lu.values(rstd)[ok], wr[ok], tol[ok], f"{value} {size} rstd")
