@@ -70,14 +70,14 @@ __global__ __launch_bounds__(kRowThreads) void k_norm_any(FwdArgs a, DropArgs d)
       }
     }
     const float rstd = (float)(1.0 / sqrt(any_sum(ss, red) / (double)a.size + (double)a.eps));
-    const float m = (float)mean;
+    const float m = (float)mean, hm = 0.5f * m, tr = 2.0f * rstd;
     for (uint32_t g = threadIdx.x; g < groups; g += kRowThreads) {
       float v[8], w[8], b[8];
       unpack<DT>(load_group8<DT, false>(h, g, a.size), v);
       weight_group<DT>(a.weight, a.wdt, g, a.size, 1.0f, w);
       weight_group<DT>(a.bias, a.wdt, g, a.size, 0.0f, b);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = (v[k] - m) * rstd * w[k] + b[k];
+      for (int k = 0; k < 8; ++k) v[k] = normed(v[k], hm, tr) * w[k] + b[k];
       store_group8<DT, false>(y, g, a.size, pack<DT>(v));
     }
     if (a.mean && threadIdx.x == 0) {
@@ -141,7 +141,7 @@ __global__ __launch_bounds__(kLongThreads) void k_row_means_long(BwdArgs a) {
   const uint32_t units = (a.size + kUnit<DT> - 1) / kUnit<DT>;
   for (uint32_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld;
-    const float mean = a.mean[r], rstd = a.rstd[r];
+    const float hm = 0.5f * a.mean[r], tr = 2.0f * a.rstd[r];
     double s1 = 0.0, s2 = 0.0;  // of each unit's binary32 sums
     for (uint32_t u = threadIdx.x; u < units; u += kLongThreads) {
       const uint32_t c = u * kUnit<DT>;
@@ -157,7 +157,7 @@ __global__ __launch_bounds__(kLongThreads) void k_row_means_long(BwdArgs a) {
       for (uint32_t j = 0; j < kUnit<DT>; ++j) {
         const float t = g[j] * w[j];
         t1 += t;
-        t2 = __builtin_fmaf(t, (n[j] - mean) * rstd, t2);
+        t2 = __builtin_fmaf(t, normed(n[j], hm, tr), t2);
       }
       s1 += (double)t1;
       s2 += (double)t2;
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, Drop
   if (r < a.rows) fetch(r);
   while (r < a.rows) {
     float g[kUnit<DT>], n[kUnit<DT>], h[kUnit<DT>];
-    const float mean = nmean, rstd = nrstd, c1 = nc1, c2 = nc2;
+    const float rstd = nrstd, hm = 0.5f * nmean, tr = 2.0f * rstd, c1 = nc1, c2 = nc2;
     unit_settled<DT>(ny, c, a.size);
     unit_settled<DT>(nx, c, a.size);
     unpack_unit<DT>(ny, g);
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, Drop
     if (next < a.rows) fetch(next);
 #pragma unroll
     for (uint32_t j = 0; j < kUnit<DT>; ++j) {
-      n[j] = (n[j] - mean) * rstd;
+      n[j] = normed(n[j], hm, tr);
       dw[j] = __builtin_fmaf(g[j], n[j], dw[j]);
       db[j] += g[j];
       n[j] = rstd * (g[j] * w[j] - c1 - n[j] * c2);
@@ -304,9 +304,10 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_short(FwdArgs a, DropArgs 
     const double t = k < a.size ? (double)v[k] - mean : 0.0;
     ss += t * t;
   }
-  const float rstd = (float)(1.0 / sqrt(ss / (double)a.size + (double)a.eps)), m = (float)mean;
+  const float rstd = (float)(1.0 / sqrt(ss / (double)a.size + (double)a.eps)), m = (float)mean, hm = 0.5f * m,
+              tr = 2.0f * rstd;
 #pragma unroll
-  for (int k = 0; k < 7; ++k) v[k] = __builtin_fmaf((v[k] - m) * rstd, w[k], b[k]);
+  for (int k = 0; k < 7; ++k) v[k] = __builtin_fmaf(normed(v[k], hm, tr), w[k], b[k]);
   store_short<DT>(a.y.at + r * a.y.ld, a.size, v);
   if (a.mean) {
     a.mean[r] = m;
@@ -324,11 +325,11 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_grad_short(BwdArgs a, Drop
     float g[8], n[8];
     load_short<DT>(a.dy.at + r * a.dy.ld, a.size, g);
     load_short<DT>(a.x.at + r * a.x.ld, a.size, n);
-    const float mean = a.mean[r], rstd = a.rstd[r];
+    const float rstd = a.rstd[r], hm = 0.5f * a.mean[r], tr = 2.0f * rstd;
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (uint32_t k = 0; k < 7; ++k) {
-      n[k] = k < a.size ? (n[k] - mean) * rstd : 0.0f;  // past the end: see settle_round()
+      n[k] = k < a.size ? normed(n[k], hm, tr) : 0.0f;  // past the end: see settle_round()
       dw[k] = __builtin_fmaf(g[k], n[k], dw[k]);
       db[k] += g[k];
       g[k] *= w[k];

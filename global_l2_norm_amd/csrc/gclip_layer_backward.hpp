@@ -68,7 +68,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
 
   while (base < a.rows) {
     const uint32_t r = base + slot;
-    const float mean = nmean, rstd = nrstd;
+    const float rstd = nrstd, hm = 0.5f * nmean, tr = 2.0f * rstd;
     float g[NV][kUnit<DT>], n[NV][kUnit<DT>];
     u32x4 hh[NV];
     float s1 = 0.0f, s2 = 0.0f;
@@ -85,7 +85,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
       }
 #pragma unroll
       for (uint32_t j = 0; j < kUnit<DT>; ++j) {
-        n[k][j] = (n[k][j] - mean) * rstd;
+        n[k][j] = normed(n[k][j], hm, tr);
         dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
         db[k][j] += g[k][j];
         g[k][j] *= w[k][j];

@@ -547,6 +547,13 @@ __device__ __forceinline__ float divided(float t, float n, float inverse) {
   return __builtin_fmaf(__builtin_fmaf(-q, n, t), inverse, q);
 }
 
+// (x - mean) rstd, from half of the mean and twice rstd: x - mean alone may
+// leave binary32 (elements at both of its ends).  The same bits otherwise,
+// as both factors are powers of two.
+__device__ __forceinline__ float normed(float x, float half_mean, float twice_rstd) {
+  return __builtin_fmaf(x, 0.5f, -half_mean) * twice_rstd;
+}
+
 // Sum over the lanes of a wave that hold the same column of its 64 / LANES
 // rows, in the first LANES lanes.
 template <int LANES>

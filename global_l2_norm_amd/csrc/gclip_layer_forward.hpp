@@ -179,10 +179,11 @@ __global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs 
     }
 
     if (r < a.rows) {
+      const float hm = 0.5f * mean, tr = 2.0f * rstd;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
 #pragma unroll
-        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[k][j] = __builtin_fmaf((v[k][j] - mean) * rstd, w[k][j], b[k][j]);
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[k][j] = __builtin_fmaf(normed(v[k][j], hm, tr), w[k][j], b[k][j]);
         store_columns<DT, LANES, SURE, !STREAMED>(a.y.at + r * a.y.ld, lane, k, a.size, pack_unit<DT>(v[k]));
       }
       if (a.mean && lane == 0) {

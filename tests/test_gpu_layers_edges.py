@@ -124,3 +124,30 @@ def test_spread_of_almost_constant_rows(size, rows):
         ok = (spread >= step / 2) | (spread == 0)
         tol = np.where(spread == 0, 4 * lu.U, (lu.PATH + 10) * lu.U) * wr
         lu.within(lu.values(rstd)[ok], wr[ok], tol[ok], f"{value} {size} rstd")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [5, 8, 64, 100, 771, 3000, 8192, 16000, 40000])
+def test_elements_further_from_the_mean_than_binary32_reaches(size, dtype):
+    """All of a row at one end of the format but for one element at the other:
+    x - mean is above the largest binary32 value, y and the gradients are
+    not."""
+    g, rng = G(), np.random.default_rng(size)
+    for rows in (3, 600):
+        what = f"{rows} x {size} {dtype}"
+        print(what, flush=True)
+        x = np.full((rows, size), -3e38)
+        x[np.arange(rows), rng.integers(0, size, rows)] = 3e38
+        x[0] = -x[0]
+        x = lu.matrix(x, dtype)
+        w, b = vectors(size, "f32", rng)
+        xv, wv, bv = lu.values(x), lu.values(w), lu.values(b)
+        y, mean, rstd = g.layer_norm_forward(x, w, b, EPS)
+        lu.check_norm(xv, lu.values(y), lu.values(mean), lu.values(rstd), wv, bv, EPS, dtype, what)
+        dy = lu.matrix(rng.standard_normal((rows, size)), dtype)
+        # the exact statistics: the mean's own error is not the gradient's
+        _, m, r = L.norm(xv, 1.0, 0.0, EPS)
+        mean, rstd = f32(m), f32(r)
+        dx, dw, db = g.layer_norm_backward(dy, x, mean, rstd, w)
+        lu.check_norm_gradient(lu.values(dx), lu.values(dw), lu.values(db), lu.values(dy), xv, lu.values(mean),
+                               lu.values(rstd), wv, dtype, "f32", what)
