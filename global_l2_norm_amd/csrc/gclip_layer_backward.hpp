@@ -41,7 +41,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
   float nmean, nrstd;
   uint32_t base = blockIdx.x * kRows;
   const auto fetch = [&](uint32_t first) {
-    // rows past the end are read as the last one, with a dy of zeros
+    // rows past the end are read as the last one; they count for nothing
     const uint32_t r = min(first + slot, a.rows - 1);
     const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld, dh = a.dh.at + r * a.dh.ld;
     nmean = a.mean[r];
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
 
   while (base < a.rows) {
     const uint32_t r = base + slot;
-    const float rstd = nrstd, hm = 0.5f * nmean, tr = 2.0f * rstd;
+    const float rstd = nrstd, hm = r < a.rows ? 0.5f * nmean : 0.0f, tr = 2.0f * rstd;
     float g[NV][kUnit<DT>], n[NV][kUnit<DT>];
     u32x4 hh[NV];
     float s1 = 0.0f, s2 = 0.0f;
@@ -76,16 +76,18 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
     for (int k = 0; k < NV; ++k) {
       settle<DT, LANES, SURE>(ny[k], lane, k, a.size, full);
       settle_round<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
-      if (r >= a.rows) ny[k] = u32x4{0u, 0u, 0u, 0u};  // n stays the last row's
+      if (r >= a.rows) ny[k] = nx[k] = u32x4{0u, 0u, 0u, 0u};
       unpack_unit<DT>(ny[k], g[k]);
       unpack_unit<DT>(nx[k], n[k]);
       if constexpr (RES) {
         settle<DT, LANES, SURE>(nh[k], lane, k, a.size, full);
         hh[k] = nh[k];
       }
+      // past the row's end and the last row x is 0: n is too, from a mean of 0
+      const float hk = k < SURE || column_of<DT>(lane, LANES, k) < a.size ? hm : 0.0f;
 #pragma unroll
       for (uint32_t j = 0; j < kUnit<DT>; ++j) {
-        n[k][j] = normed(n[k][j], hm, tr);
+        n[k][j] = normed(n[k][j], hk, tr);
         dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
         db[k][j] += g[k][j];
         g[k][j] *= w[k][j];

@@ -427,15 +427,16 @@ __device__ __forceinline__ void settle(u32x4& q, uint32_t lane, int k, uint32_t 
     q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
 }
 
-// As settle(), but past the row's end are other elements of the row, not
-// zeros: for the matrix that was normed, where a zero's (0 - mean) rstd may
-// be infinite though every element's is finite, and nothing times that is NaN
-// in the row's sums.
+// As settle(), but in the unit of the row's end other elements of the row
+// come after it, not zeros: for the matrix that was normed, where a zero's
+// (0 - mean) rstd may be infinite though every element's is finite, and
+// nothing times that is NaN in the row's sums.
 template <int DT, int LANES, int SURE>
 __device__ __forceinline__ void settle_round(u32x4& q, uint32_t lane, int k, uint32_t size, bool full) {
   if (k < SURE || full) return;
   const uint32_t c = column_of<DT>(lane, LANES, k);
-  if (c < size && c + kUnit<DT> > size) q = moved_down<DT, true>(q, kUnit<DT> - size % kUnit<DT>);
+  if (c + kUnit<DT> > size)
+    q = c < size ? moved_down<DT, true>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
 }
 
 template <int DT, int LANES, int SURE, bool NT>
