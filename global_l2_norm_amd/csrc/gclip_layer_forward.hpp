@@ -102,9 +102,9 @@ __global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs 
     // round, what is left itself: in a row of little spread it takes the sum's
     // own error off, so a constant row's mean is its value, and its y the bias
     // (a row's sum of equal bfloat16 elements is exact up to 2^16 of them, of
-    // binary16 ones up to 2^13); rows whose sums leave binary32 go through
-    // this again, scaled by a power of two (so does a row with a NaN or an
-    // infinity, to no effect)
+    // binary16 ones up to 2^13); rows whose sums, or whose var + eps, leave
+    // binary32 go through this again, scaled by a power of two (so does a row
+    // with a NaN or an infinity, to no effect)
     constexpr bool kRounds = DT == GCLIP_F32 || (DT == GCLIP_F16 && LANES * NV * kUnit<DT> > 8192);
     float scale = 1.0f, mean, var;
     for (bool first = true;; first = false) {
@@ -159,7 +159,7 @@ __global__ __launch_bounds__((kFwdThreads<DT, LANES>)) void k_norm_rows(FwdArgs 
       // rows that meet go through it again together, if one of them has to:
       // those of a wave, or of a workgroup, whose barriers all of its waves
       // have to reach equally often
-      const auto leaves = [](float t) { return !(t <= 0x1.fffffep+127f); };
+      const auto leaves = [&](float t) { return !(t + a.eps <= 0x1.fffffep+127f); };
       bool again = leaves(var);
       if constexpr (LANES > 64) {
         static_assert(kThreads == LANES || !kRounds, "the sum of squares alone decides");

@@ -151,3 +151,14 @@ def test_elements_further_from_the_mean_than_binary32_reaches(size, dtype):
         dx, dw, db = g.layer_norm_backward(dy, x, mean, rstd, w)
         lu.check_norm_gradient(lu.values(dx), lu.values(dw), lu.values(db), lu.values(dy), xv, lu.values(mean),
                                lu.values(rstd), wv, dtype, "f32", what)
+
+
+@pytest.mark.parametrize("size", [5, 8, 64, 100, 771, 3000, 8192, 16000, 40000])
+def test_variance_and_eps_whose_sum_leaves_binary32(size):
+    g, rng = G(), np.random.default_rng(size)
+    for eps, scale in ((3e38, 1.4e19), (3.4e38, 1.0e18), (2e38, 2e19)):
+        for rows in (3, 600):
+            x = lu.matrix(scale * rng.choice([-1.0, 1.0], (rows, size)), "f32")
+            y, mean, rstd = g.layer_norm_forward(x, eps=eps)
+            lu.check_norm(lu.values(x), lu.values(y), lu.values(mean), lu.values(rstd), np.ones(size), np.zeros(size),
+                          float(np.float32(eps)), "f32", f"{size} {eps} {scale}")
