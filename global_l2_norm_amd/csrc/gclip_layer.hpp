@@ -132,6 +132,15 @@ inline uint32_t bwd_parts(uint32_t rows, uint32_t size) {
 // and 49.6.
 constexpr uint64_t kStreamBytes = 144ull << 20;
 
+// A dispatch counts its lanes in each direction in 32 bits, and the largest
+// matrices have more units than that: workgroups beyond kGridRow go into
+// further rows of the grid, whose end no work is left for.
+constexpr uint32_t kGridRow = 1u << 20;
+inline dim3 grid_of(uint64_t workgroups, uint32_t layers = 1) {
+  const uint64_t x = workgroups < kGridRow ? workgroups : kGridRow;
+  return dim3((uint32_t)x, (uint32_t)((workgroups + x - 1) / x), layers);
+}
+
 // The most partial sums of the weights' gradients for a matrix of this shape
 // in any format.
 uint32_t layer_parts(int64_t rows, int64_t size);

@@ -182,16 +182,18 @@ __global__ __launch_bounds__(kLongThreads) void k_row_means_long(BwdArgs a) {
   }
 }
 
-// A workgroup takes a strip of 64 units of columns and part blockIdx.y of the
+// A workgroup takes a strip of 64 units of columns and part blockIdx.z of the
 // rows, its waves in turn; a row's loads are under way while the one before
 // is worked on.
 template <int DT, bool RES, bool DROP>
 __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, DropArgs d) {
   __shared__ float red[kLongWaves][64 * kUnit<DT> + 1];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t c = (blockIdx.x * 64 + lane) * kUnit<DT>;
+  const uint64_t strip = workgroup_of_grid() * (64 * kUnit<DT>);
+  if (strip >= a.size) return;
+  const uint32_t c = (uint32_t)strip + lane * kUnit<DT>;
   const uint32_t step = DROP ? drop_step(d) : 0u;
-  const uint32_t stride = gridDim.y * kLongWaves;
+  const uint32_t stride = gridDim.z * kLongWaves;
   float w[kUnit<DT>], dw[kUnit<DT>] = {}, db[kUnit<DT>] = {};
   weight_unit<DT>(a.weight, a.wdt, c, a.size, w);
   u32x4 ny, nx, nh{0u, 0u, 0u, 0u};
@@ -205,7 +207,7 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, Drop
     nc1 = a.sums[2 * (uint64_t)r];
     nc2 = a.sums[2 * (uint64_t)r + 1];
   };
-  uint32_t r = blockIdx.y * kLongWaves + wave;
+  uint32_t r = blockIdx.z * kLongWaves + wave;
   if (r < a.rows) fetch(r);
   while (r < a.rows) {
     float g[kUnit<DT>], n[kUnit<DT>], h[kUnit<DT>];
@@ -245,11 +247,11 @@ __global__ __launch_bounds__(kLongThreads) void k_norm_grad_long(BwdArgs a, Drop
     for (uint32_t j = 0; j < kUnit<DT>; ++j) red[wave][lane * kUnit<DT> + j] = which ? db[j] : dw[j];
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < 64 * kUnit<DT>; i += kLongThreads) {
-      const uint32_t col = blockIdx.x * 64 * kUnit<DT> + i;
+      const uint32_t col = (uint32_t)strip + i;
       float t = red[0][i];
 #pragma unroll
       for (int k = 1; k < kLongWaves; ++k) t += red[k][i];
-      if (col < a.size) a.partials[((uint64_t)blockIdx.y * 2 + which) * a.size + col] = t;
+      if (col < a.size) a.partials[((uint64_t)blockIdx.z * 2 + which) * a.size + col] = t;
     }
   }
 }
@@ -380,7 +382,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_grad_short(BwdArgs a, Drop
 template <int DT, bool STREAMED>
 __global__ __launch_bounds__(kAnyThreads) void k_dropout(Rows x, Rows y, uint32_t rows, uint32_t size, DropArgs d) {
   const uint32_t units = (size + kUnit<DT> - 1) / kUnit<DT>;
-  const uint64_t i = (uint64_t)blockIdx.x * kAnyThreads + threadIdx.x;
+  const uint64_t i = workgroup_of_grid() * kAnyThreads + threadIdx.x;
   const uint64_t row = i / units;
   if (row >= rows) return;
   const uint32_t r = (uint32_t)row, u = (uint32_t)(i % units);
@@ -424,7 +426,7 @@ hipError_t backward_any(const BwdArgs& a, bool residual, const DropArgs* drop, h
     else if (!drop) hipLaunchKernelGGL((k_norm_grad_short<DT, true, false>), grid, block, 0, st, a, DropArgs{});
     else hipLaunchKernelGGL((k_norm_grad_short<DT, true, true>), grid, block, 0, st, a, *drop);
   } else if (a.rows > 0) {
-    const dim3 block(kLongThreads), strips((a.size - 1) / (64 * kUnit<DT>) + 1, a.parts);
+    const dim3 block(kLongThreads), strips = grid_of((a.size - 1) / (64 * kUnit<DT>) + 1, a.parts);
     hipLaunchKernelGGL((k_row_means_long<DT>), dim3(std::min<uint32_t>(a.rows, 1u << 20)), block, 0, st, a);
     if (!residual) hipLaunchKernelGGL((k_norm_grad_long<DT, false, false>), strips, block, 0, st, a, DropArgs{});
     else if (!drop) hipLaunchKernelGGL((k_norm_grad_long<DT, true, false>), strips, block, 0, st, a, DropArgs{});
@@ -437,7 +439,7 @@ hipError_t backward_any(const BwdArgs& a, bool residual, const DropArgs* drop, h
 template <int DT>
 hipError_t dropout(const Rows& x, const Rows& y, uint32_t rows, uint32_t size, const DropArgs& d, hipStream_t st) {
   const uint64_t total = (uint64_t)rows * ((size + kUnit<DT> - 1) / kUnit<DT>);
-  const dim3 grid((uint32_t)((total + kAnyThreads - 1) / kAnyThreads)), block(kAnyThreads);
+  const dim3 grid = grid_of((total + kAnyThreads - 1) / kAnyThreads), block(kAnyThreads);
   if (total * 32 > kStreamBytes) hipLaunchKernelGGL((k_dropout<DT, true>), grid, block, 0, st, x, y, rows, size, d);
   else hipLaunchKernelGGL((k_dropout<DT, false>), grid, block, 0, st, x, y, rows, size, d);
   return hipGetLastError();

@@ -173,7 +173,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_weight_grads(BwdArgs a) {
   constexpr uint32_t kWavesOf = kJoinThreads / 64;
   __shared__ float red[kWavesOf][64];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint64_t i = (uint64_t)blockIdx.x * 64 + lane, width = 2ull * a.size;
+  const uint64_t i = workgroup_of_grid() * 64 + lane, width = 2ull * a.size;
   float t = 0.0f;
   if (i < width) {
 #pragma unroll 16
@@ -190,8 +190,7 @@ __global__ __launch_bounds__(kJoinThreads) void k_join_weight_grads(BwdArgs a) {
 
 template <int DT>
 hipError_t join_weight_grads(const BwdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((k_join_weight_grads<DT>), dim3((uint32_t)((2ull * a.size + 63) / 64)), dim3(kJoinThreads), 0, st,
-                     a);
+  hipLaunchKernelGGL((k_join_weight_grads<DT>), grid_of((2ull * a.size + 63) / 64), dim3(kJoinThreads), 0, st, a);
   return hipGetLastError();
 }
 

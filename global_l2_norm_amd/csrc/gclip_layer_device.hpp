@@ -24,6 +24,9 @@ typedef uint64_t u64_any2 __attribute__((aligned(2)));
 typedef uint64_t u64_any4 __attribute__((aligned(4)));
 typedef uint32_t u32_any2 __attribute__((aligned(2)));
 
+// Number of this workgroup in a layer of a grid_of().
+__device__ __forceinline__ uint64_t workgroup_of_grid() { return (uint64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 template <int DT>
 constexpr uint32_t kElem = DT == GCLIP_F32 ? 4u : 2u;
 

@@ -162,3 +162,54 @@ def test_variance_and_eps_whose_sum_leaves_binary32(size):
             y, mean, rstd = g.layer_norm_forward(x, eps=eps)
             lu.check_norm(lu.values(x), lu.values(y), lu.values(mean), lu.values(rstd), np.ones(size), np.zeros(size),
                           float(np.float32(eps)), "f32", f"{size} {eps} {scale}")
+
+
+MOST = 0x7ffffff0  # the largest extent of a matrix
+
+
+def test_gradients_of_the_longest_row():
+    """One row of 2^31 - 16 columns: more columns than a dispatch of a lane a
+    column could count.  With mean 0 and rstd 1, n is x: dbias is dy and
+    dweight dy * x exactly, and the two means are at most 2^-11 here, so dx is
+    dy - c1 - x c2 to a few roundings."""
+    import torch
+    g = G()
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, dy = (torch.randn(1, MOST, generator=gen, device="cuda") for _ in range(2))
+    mean, rstd = torch.zeros(1, device="cuda"), torch.ones(1, device="cuda")
+    dx, dw, db = g.layer_norm_backward(dy, x, mean, rstd, weight_grad=True, bias_grad=True)
+    assert torch.equal(db, dy[0])
+    part = 1 << 28
+    c1 = c2 = 0.0
+    for i in range(0, MOST, part):
+        u, v = x[0, i:i + part], dy[0, i:i + part]
+        assert torch.equal(dw[i:i + part], u * v), i
+        c1 += float(v.sum(dtype=torch.float64)) / MOST
+        c2 += float((u.double() * v.double()).sum()) / MOST
+    assert abs(c1) < 2.0 ** -11 and abs(c2) < 2.0 ** -11
+    for i in range(0, MOST, part):
+        u, v = x[0, i:i + part].double(), dy[0, i:i + part].double()
+        off = (dx[0, i:i + part].double() - (v - c1 - u * c2)).abs()
+        # dx, dy - c1 and the product and sum with c2 round; c1 and c2 are
+        # binary64 sums of units' binary32 sums
+        assert bool((off <= 4 * lu.U * (v.abs() + u.abs() * 2.0 ** -11 + 2.0 ** -11)).all()), i
+
+
+def test_dropout_of_more_units_than_32_bits_count():
+    """In place over 17 rows of 2^31 - 16 bfloat16 elements, 68 GiB: the
+    groups at both ends of each row, and those about the 2^32nd unit."""
+    import torch
+    g = G()
+    rows = 17
+    x = torch.ones(rows, MOST, dtype=torch.bfloat16, device="cuda")
+    g.dropout_forward(x, mask(0.5), out=x)
+    units = MOST // 8
+    at = [(r, u) for r in range(rows) for u in (0, 1, units - 2, units - 1)]
+    at += [divmod((1 << 32) + k, units) for k in range(-300, 300) if (1 << 32) + k < rows * units]
+    at += [divmod((1 << 28) * k, units) for k in range(1, 17)]
+    r, u = (np.array(v) for v in zip(*at))
+    w = L.philox_words([u, r, np.full_like(u, 3), np.full_like(u, 7)], [0x90ABCDEF, 0x12345678])
+    half = np.stack([v for k in w for v in (k & 0xFFFF, k >> 16)], 1)
+    rt, ut = torch.from_numpy(r).cuda(), torch.from_numpy(u).cuda()
+    got = x.view(rows, units, 8)[rt, ut]
+    assert np.array_equal(lu.values(got), np.where(half >= 32768, 2.0, 0.0))
