@@ -12,8 +12,9 @@ serve as device memory and streams: every step runs in the HIP kernels.
   buffers of the caller's, added to what the microbatches before left there
   when ``accumulate`` is set, from where a ``GradList`` clips them.
 - ``layer_norm``, ``dropout`` and ``residual_norm`` are the same under
-  autograd.  To capture a training step into a graph, capture the passes; a
-  captured autograd backward needs leaves that no eager graph holds.
+  autograd, in its backward mode: tensors with a tangent are refused.  To
+  capture a training step into a graph, capture the passes; a captured
+  autograd backward needs leaves that no eager graph holds.
 
 A matrix is a tensor whose last dimension is adjacent in memory and whose
 other dimensions lie at one distance (a contiguous tensor, a slice of the
@@ -357,9 +358,18 @@ def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, acc
 
 
 # ---------------------------------------------------------------- under autograd
+def _without_tangent(*tensors):
+    """Refuse what a forward-mode derivative would be lost of."""
+    if _forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and _forward_ad.unpack_dual(t).tangent is not None:
+                raise NotImplementedError("the layers have no forward-mode derivatives")
+
+
 def _matrix_of(t):
     """A gradient from autograd in a form that the kernels take: an expanded
     or permuted one is copied."""
+    _without_tangent(t)
     try:
         _ld(t, "gradient")
         return t
@@ -368,6 +378,7 @@ def _matrix_of(t):
 
 
 if torch is not None:
+    import torch.autograd.forward_ad as _forward_ad
     from torch.autograd.function import once_differentiable
 
     class _Dropout(torch.autograd.Function):
@@ -432,6 +443,7 @@ def _grad_buffers(ctx, x, weight, at):
 
 
 def _tracked(*tensors):
+    _without_tangent(*tensors)
     return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
 
 

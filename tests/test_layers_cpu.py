@@ -190,3 +190,29 @@ def test_tensors_and_masks_that_no_gpu_sees_are_refused():
     other = m.at(site=9)
     assert (other.p, other.seed, other.step, other.site) == (0.5, 1, 3, 9)
     assert G.DropoutMask(2.0 ** -17, 0).drops and not G.DropoutMask(2.0 ** -17 - 1e-9, 0).drops
+
+
+def test_forward_mode_derivatives_are_refused():
+    """A tensor with a tangent has no gradient of its own; without a check the
+    result would come back without a tangent, as if it were constant."""
+    import torch
+    import torch.autograd.forward_ad as forward_ad
+
+    import global_l2_norm_amd as G
+    from global_l2_norm_amd import layers
+    m = G.DropoutMask(0.5, 1)
+    x, w = torch.ones(4, 16), torch.ones(16)
+    with forward_ad.dual_level():
+        dx, dw = forward_ad.make_dual(x, x), forward_ad.make_dual(w, w)
+        for call in (lambda: G.layer_norm(dx, w), lambda: G.layer_norm(x, dw), lambda: G.layer_norm(x, w, dw),
+                     lambda: G.dropout(dx, m), lambda: G.residual_norm(dx, x), lambda: G.residual_norm(x, dx, mask=m),
+                     lambda: layers._matrix_of(dx)):
+            for mode in (torch.enable_grad, torch.no_grad):
+                with mode(), pytest.raises(NotImplementedError):
+                    call()
+        for call in (lambda: G.layer_norm(x, w), lambda: G.dropout(x, m)):
+            with pytest.raises(ValueError, match="device"):  # no tangent: only that no GPU sees it
+                call()
+    for call in (lambda t: G.layer_norm(t, w), lambda t: G.dropout(t, m)):
+        with pytest.raises(NotImplementedError):
+            torch.func.jvp(call, (x,), (x,))
