@@ -83,6 +83,8 @@ def _matrix(x, name):
     """(device index, rows, size, ld, dtype code) of the matrix that a call
     goes by; its device has to be the current one: kernels are enqueued
     there."""
+    if torch._C._is_tracing():
+        raise RuntimeError("the layers cannot be traced: a trace records none of their kernels")
     code = _CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"{name}: unsupported dtype {x.dtype}")

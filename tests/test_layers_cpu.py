@@ -216,3 +216,19 @@ def test_forward_mode_derivatives_are_refused():
     for call in (lambda t: G.layer_norm(t, w), lambda t: G.dropout(t, m)):
         with pytest.raises(NotImplementedError):
             torch.func.jvp(call, (x,), (x,))
+
+
+def test_tracing_is_refused():
+    """torch.jit.trace records torch operations, not kernels that a C call
+    enqueues: the trace would return memory that nothing wrote."""
+    import torch
+
+    import global_l2_norm_amd as G
+    m = G.DropoutMask(0.5, 1)
+    x, w = torch.ones(4, 16), torch.ones(16)
+    grad = x.clone().requires_grad_()
+    for call, arg in ((lambda t: G.layer_norm(t, w), x), (lambda t: G.layer_norm(t, w), grad),
+                      (lambda t: G.dropout(t, m), x), (lambda t: G.residual_norm(t, x, mask=m)[1], x),
+                      (lambda t: G.layer_norm_backward(x, t, w[:4], w[:4], w)[0], x)):
+        with pytest.raises(RuntimeError, match="traced"):
+            torch.jit.trace(call, arg)
