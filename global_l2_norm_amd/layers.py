@@ -65,6 +65,7 @@ def gclip_layer_workspace(rows, size):
 if torch is not None:
     _CODES = {torch.float32: GCLIP_F32, torch.float16: GCLIP_F16, torch.bfloat16: GCLIP_BF16}
     _F32 = torch.float32
+    _increment_version = torch.autograd.graph.increment_version
     # a small call takes a few microseconds: torch.cuda.current_stream() alone
     # would be a third of it
     _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -155,6 +156,14 @@ def _there(stream, f, *args):
         return f(*args)
 
 
+def _wrote(*tensors):
+    """Autograd may have saved what a caller gives to be written: as after an
+    in-place operation of torch, its backward pass then refuses it."""
+    for t in tensors:
+        if t is not None:
+            _increment_version(t)
+
+
 # ---------------------------------------------------------------- dropout
 class DropoutMask:
     """Which elements a dropout keeps, as a function of its arguments alone:
@@ -200,6 +209,7 @@ def dropout_forward(x, mask, out=None, stream=None):
     """x where the mask keeps it, times 1 / (1 - p); else 0.  out may be x."""
     if stream is not None:
         return _there(stream, dropout_forward, x, mask, out)
+    given = out
     device, rows, size, ld, code = _matrix(x, "x")
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
@@ -208,6 +218,7 @@ def dropout_forward(x, mask, out=None, stream=None):
         ldo = _like(out, x, "out")
     gclip_dropout_apply(x.data_ptr(), ld, out.data_ptr(), ldo, rows, size, code, _counted(mask, device),
                         _raw_stream(device))
+    _wrote(given)
     return out
 
 
@@ -221,7 +232,9 @@ def layer_norm_forward(x, weight=None, bias=None, eps=1e-5, *, out=None, stats=T
     """(y, mean, rstd) of the norm over the last dimension.  mean and rstd are
     what the backward pass takes, and None without ``stats``."""
     args = x, None, weight, bias, eps, None, None, out, stats
-    return (_forward(*args) if stream is None else _there(stream, _forward, *args))[1:]
+    got = _forward(*args) if stream is None else _there(stream, _forward, *args)
+    _wrote(out)
+    return got[1:]
 
 
 def residual_norm_forward(x, residual, weight=None, bias=None, eps=1e-5, mask=None, *, out_h=None, out=None,
@@ -229,7 +242,9 @@ def residual_norm_forward(x, residual, weight=None, bias=None, eps=1e-5, mask=No
     """(h, y, mean, rstd) of h = residual + dropout(x), y = norm(h).  out_h
     may be residual or x (in place)."""
     args = x, residual, weight, bias, eps, mask, out_h, out, stats
-    return _forward(*args) if stream is None else _there(stream, _forward, *args)
+    got = _forward(*args) if stream is None else _there(stream, _forward, *args)
+    _wrote(out_h, out)
+    return got
 
 
 def _forward(x, residual, weight, bias, eps, mask, h, y, stats):
@@ -280,6 +295,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, *, dweight=None, dbias=N
     """
     args = dy, None, x, mean, rstd, weight, None, False, dweight, dbias, accumulate, weight_grad, bias_grad, out, None
     dx, _, dw, db = _backward(*args) if stream is None else _there(stream, _backward, *args)
+    _wrote(out, dweight, dbias)
     return dx, dw, db
 
 
@@ -292,7 +308,9 @@ def residual_norm_backward(dy, dh, h, mean, rstd, weight=None, mask=None, *, dwe
     dresidual, the same tensor.  Otherwise as ``layer_norm_backward``."""
     args = (dy, dh, h, mean, rstd, weight, mask if mask is not None and mask.drops else None, True, dweight, dbias,
             accumulate, weight_grad, bias_grad, out, out_residual)
-    return _backward(*args) if stream is None else _there(stream, _backward, *args)
+    got = _backward(*args) if stream is None else _there(stream, _backward, *args)
+    _wrote(out, out_residual, dweight, dbias)
+    return got
 
 
 def _backward(dy, dh, x, mean, rstd, weight, mask, residual, dweight, dbias, accumulate, weight_grad, bias_grad, dx,
@@ -407,8 +425,8 @@ if torch is not None:
         def backward(ctx, dy):
             x, mean, rstd, weight = ctx.saved_tensors
             dw, db = _grad_buffers(ctx, x, weight, 1)
-            dx, dw, db = layer_norm_backward(_matrix_of(dy), x, mean, rstd, weight, dweight=dw, dbias=db,
-                                             weight_grad=False, bias_grad=False)
+            dx, _, dw, db = _backward(_matrix_of(dy), None, x, mean, rstd, weight, None, False, dw, db, False, False,
+                                      False, None, None)
             return dx, dw, db, None
 
     class _ResidualNorm(torch.autograd.Function):
@@ -432,8 +450,9 @@ if torch is not None:
                     return (None,) * 6
                 return dropout_backward(dh, mask) if mask is not None else dh, dh, None, None, None, None
             dw, db = _grad_buffers(ctx, h, weight, 2)
-            dx, dres, dw, db = residual_norm_backward(_matrix_of(dy), dh, h, mean, rstd, weight, mask, dweight=dw,
-                                                      dbias=db, weight_grad=False, bias_grad=False)
+            dx, dres, dw, db = _backward(_matrix_of(dy), dh, h, mean, rstd, weight,
+                                         mask if mask is not None and mask.drops else None, True, dw, db, False, False,
+                                         False, None, None)
             return dx, dres, dw, db, None, None
 
 

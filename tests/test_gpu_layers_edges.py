@@ -213,3 +213,39 @@ def test_dropout_of_more_units_than_32_bits_count():
     rt, ut = torch.from_numpy(r).cuda(), torch.from_numpy(u).cuda()
     got = x.view(rows, units, 8)[rt, ut]
     assert np.array_equal(lu.values(got), np.where(half >= 32768, 2.0, 0.0))
+
+
+def test_written_buffers_are_seen_by_autograd():
+    """A tensor that autograd saved and that a pass then writes fails its
+    backward, as after any in-place operation; tensors that are only read keep
+    their version."""
+    import torch
+    g = G()
+    x, w = torch.randn(6, 32, device="cuda"), torch.ones(32, device="cuda")
+    side = torch.cuda.Stream()
+    y, mean, rstd = g.layer_norm_forward(x, w)
+    h = x.clone()
+    calls = [
+        (lambda t, s: g.dropout_forward(x, mask(), out=t, stream=s), x),
+        (lambda t, s: g.dropout_backward(x, mask(), out=t, stream=s), x),
+        (lambda t, s: g.layer_norm_forward(x, w, out=t, stream=s), x),
+        (lambda t, s: g.residual_norm_forward(x, h, w, out_h=t, stream=s), x),
+        (lambda t, s: g.residual_norm_forward(x, h, w, out=t, stream=s), x),
+        (lambda t, s: g.layer_norm_backward(x, h, mean, rstd, w, out=t, stream=s), x),
+        (lambda t, s: g.residual_norm_backward(x, None, h, mean, rstd, w, mask(), out=t, stream=s), x),
+        (lambda t, s: g.residual_norm_backward(x, None, h, mean, rstd, w, mask(), out_residual=t, stream=s), x),
+        (lambda t, s: g.layer_norm_backward(x, h, mean, rstd, w, dweight=t, stream=s), w),
+        (lambda t, s: g.layer_norm_backward(x, h, mean, rstd, w, dbias=t, weight_grad=False, stream=s), w),
+    ]
+    for stream in (None, side):
+        for i, (call, like) in enumerate(calls):
+            leaf = torch.ones_like(like).requires_grad_()
+            saved = torch.zeros_like(like)
+            read = [t._version for t in (x, h, w, mean, rstd)]
+            loss = (leaf * saved).sum()
+            torch.cuda.synchronize()
+            call(saved, stream)
+            torch.cuda.synchronize()
+            with pytest.raises(RuntimeError, match="inplace"):
+                loss.backward()
+            assert read == [t._version for t in (x, h, w, mean, rstd)], i
