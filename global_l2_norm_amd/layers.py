@@ -74,9 +74,14 @@ if torch is not None:
 
 
 def _counted(mask, device):
-    """The mask's structure; its counter has to be on the device that reads it."""
-    if mask.counter is not None and mask.counter.get_device() != device:
-        raise ValueError(f"the mask's counter is on {mask.counter.device}")
+    """The mask's structure; its counter has to be on the device that reads it,
+    and where it was when the mask was made."""
+    counter = mask.counter
+    if counter is not None:
+        if counter.get_device() != device:
+            raise ValueError(f"the mask's counter is on {counter.device}")
+        if counter.data_ptr() != mask.args.d_step or counter.numel() < 1:
+            raise ValueError("the mask's counter has another storage than when the mask was made")
     return mask.args
 
 
@@ -176,6 +181,8 @@ class DropoutMask:
     counter  optional device tensor whose first int32 is added to step: a
              captured graph takes it anew at each replay (``counter.add_(1)``
              between the replays, and not between a pass and its backward)
+
+    A mask does not change: ``at`` gives another one.
     """
 
     __slots__ = ("p", "seed", "step", "site", "counter", "args")
@@ -191,8 +198,15 @@ class DropoutMask:
             if counter.dtype != torch.int32 or not counter.is_cuda or counter.numel() < 1:
                 raise ValueError("counter must be an int32 device tensor")
             address = counter.data_ptr()
-        self.p, self.seed, self.step, self.site, self.counter = p, seed, step, site, counter
-        self.args = GclipDropout(p, seed, step, site, address)
+        values = p, seed, step, site, counter, GclipDropout(p, seed, step, site, address)
+        for name, value in zip(self.__slots__, values):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("a mask does not change; at() gives another one")
+
+    def __reduce__(self):
+        return DropoutMask, (self.p, self.seed, self.step, self.site, self.counter)
 
     def at(self, step=None, site=None):
         """The mask of another step or site."""

@@ -249,3 +249,26 @@ def test_written_buffers_are_seen_by_autograd():
             with pytest.raises(RuntimeError, match="inplace"):
                 loss.backward()
             assert read == [t._version for t in (x, h, w, mean, rstd)], i
+
+
+def test_a_counter_that_moved_is_refused():
+    """A mask holds its counter's address; another storage behind the same
+    tensor would leave it pointing to memory that may be given out again."""
+    import torch
+    g = G()
+    x = torch.ones(4, 64, device="cuda")
+    for change in (lambda t: t.set_(torch.tensor([9], dtype=torch.int32, device="cuda")),
+                   lambda t: setattr(t, "data", torch.tensor([9], dtype=torch.int32, device="cuda")),
+                   lambda t: t.resize_(0)):
+        counter = torch.zeros(1, dtype=torch.int32, device="cuda")
+        m = mask(counter=counter)
+        g.dropout_forward(x, m)
+        counter.add_(1)
+        assert np.array_equal(lu.values(g.dropout_forward(x, m)), factors(4, 64, step=8))
+        old = counter.untyped_storage()  # kept: the address stays taken
+        change(counter)
+        for call in (lambda: g.dropout_forward(x, m), lambda: g.residual_norm_forward(x, x, mask=m),
+                     lambda: g.dropout(x, m)):
+            with pytest.raises(ValueError, match="storage"):
+                call()
+        del old

@@ -232,3 +232,23 @@ def test_tracing_is_refused():
                       (lambda t: G.layer_norm_backward(x, t, w[:4], w[:4], w)[0], x)):
         with pytest.raises(RuntimeError, match="traced"):
             torch.jit.trace(call, arg)
+
+
+def test_masks_do_not_change():
+    """What the kernels take is fixed when a mask is made: a changed attribute
+    would be ignored."""
+    import copy
+    import pickle
+
+    import global_l2_norm_amd as G
+    m = G.DropoutMask(0.5, 1, step=3, site=4)
+    for name, value in (("p", 0.1), ("seed", 2), ("step", 5), ("site", 6), ("counter", None), ("args", None),
+                        ("other", 1)):
+        with pytest.raises(AttributeError):
+            setattr(m, name, value)
+    with pytest.raises(AttributeError):
+        m.step += 1
+    assert (m.p, m.seed, m.step, m.site, m.args.step, m.args.site) == (0.5, 1, 3, 4, 3, 4)
+    assert m.at(step=5).args.step == 5
+    for other in (copy.copy(m), copy.deepcopy(m), pickle.loads(pickle.dumps(m))):
+        assert bytes(other.args) == bytes(m.args) and other.site == 4
