@@ -78,7 +78,9 @@ bool dropout_args(const gclip_dropout* d, DropArgs* out, bool* any) {
   *any = false;
   if (!d) return true;
   if (!(d->p >= 0.0 && d->p <= 1.0) || address(d->d_step) % 4 != 0) return false;
-  const uint32_t t = (uint32_t)std::floor(65536.0 * d->p + 0.5);
+  // floor(65536 p + 1/2): the sum itself rounds up to 1 just below 1/2
+  const double q = 65536.0 * d->p;
+  const uint32_t t = (uint32_t)q + (q - std::floor(q) >= 0.5 ? 1u : 0u);
   *out = DropArgs{(uint32_t)d->seed, (uint32_t)(d->seed >> 32), d->step, d->site, d->d_step, t,
                   t < 65536u ? (float)(65536.0 / (65536.0 - t)) : 0.0f};
   *any = t > 0;

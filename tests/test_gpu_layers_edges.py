@@ -272,3 +272,23 @@ def test_a_counter_that_moved_is_refused():
             with pytest.raises(ValueError, match="storage"):
                 call()
         del old
+
+
+def test_probabilities_next_to_a_step():
+    """t = floor(65536 p + 1/2) for the neighbours of its steps, from exact
+    fractions: the scale 65536 / (65536 - t) tells t, or 0 for all dropped."""
+    from fractions import Fraction
+    from math import floor
+
+    import torch
+    g = G()
+    x = torch.ones(64, 512, device="cuda")
+    for k in (0, 1, 2, 3, 4, 1000, 32767, 32768, 65534, 65535):
+        step = (k + 0.5) / 65536
+        for p in (np.nextafter(step, 0.0), step, np.nextafter(step, 1.0)):
+            t = floor(Fraction(p) * 65536 + Fraction(1, 2))
+            y = lu.values(g.dropout_forward(x, mask(p)))
+            scale = np.float64(np.float32(65536 / (65536 - t))) if t < 65536 else 0.0
+            assert set(np.unique(y)) <= {0.0, scale}, (p, t)
+            assert t > 65000 or scale in y, (p, t)
+            assert mask(p).drops == (t > 0)
