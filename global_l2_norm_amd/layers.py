@@ -459,6 +459,8 @@ if torch is not None:
             h, mean, rstd, weight = ctx.saved_tensors
             mask = ctx.mask
             dh = _matrix_of(dh) if dh is not None else None
+            if not ctx.needs_input_grad[0]:
+                mask = None  # dx is not wanted, and dresidual does not depend on it
             if dy is None:  # y is not used: the residual sum alone
                 if dh is None:
                     return (None,) * 6

@@ -292,3 +292,33 @@ def test_probabilities_next_to_a_step():
             assert set(np.unique(y)) <= {0.0, scale}, (p, t)
             assert t > 65000 or scale in y, (p, t)
             assert mask(p).drops == (t > 0)
+
+
+def test_a_frozen_input_costs_no_dropout(monkeypatch):
+    """The backward pass of a residual step whose x needs no gradient runs
+    without the mask: one matrix less, the same other gradients."""
+    import torch
+    from global_l2_norm_amd import layers
+    g, rng = G(), np.random.default_rng(3)
+    x, r, dy, dh = (lu.matrix(rng.standard_normal((40, 300)), "bf16") for _ in range(4))
+    w, b = vectors(300, "f32", rng)
+    m = mask()
+    h, y, mean, rstd = g.residual_norm_forward(x, r, w, b, EPS, m)
+    want = g.residual_norm_backward(dy, dh, h, mean, rstd, w, m)
+    drops = []
+    call, apply = layers.gclip_residual_backward, layers.gclip_dropout_apply
+    monkeypatch.setattr(layers, "gclip_residual_backward",
+                        lambda args, drop, stream: (drops.append(drop is not None), call(args, drop, stream)))
+    monkeypatch.setattr(layers, "gclip_dropout_apply", lambda *args: (drops.append(True), apply(*args)))
+    leaf = [t.clone().requires_grad_() for t in (x, r, w, b)]
+    for frozen, expected in ((0, False), (1, True)):
+        part = [t.detach() if i == frozen else t for i, t in enumerate(leaf)]
+        rest = [t for i, t in enumerate(leaf) if i != frozen]
+        drops.clear()
+        got = torch.autograd.grad(g.residual_norm(*part, EPS, m), rest, [dh, dy])
+        assert drops == [expected]
+        assert all(torch.equal(p, q) for p, q in zip(got, [t for i, t in enumerate(want) if i != frozen]))
+        drops.clear()
+        got = torch.autograd.grad(g.residual_norm(*part, EPS, m)[0], rest[0], dh)[0]
+        assert drops == [True] * expected
+        assert torch.equal(got, dh if frozen == 0 else g.dropout_backward(dh, m))
