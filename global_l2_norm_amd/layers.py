@@ -431,7 +431,7 @@ if torch is not None:
         def forward(ctx, x, weight, bias, eps):
             y, mean, rstd = layer_norm_forward(x, weight, bias, eps)
             ctx.save_for_backward(x, mean, rstd, weight)
-            ctx.bias_dtype = bias.dtype if bias is not None else None
+            ctx.bias = (bias.shape, bias.dtype) if bias is not None else None
             return y
 
         @staticmethod
@@ -448,7 +448,7 @@ if torch is not None:
         def forward(ctx, x, residual, weight, bias, eps, mask):
             h, y, mean, rstd = residual_norm_forward(x, residual, weight, bias, eps, mask)
             ctx.save_for_backward(h, mean, rstd, weight)
-            ctx.bias_dtype = bias.dtype if bias is not None else None
+            ctx.bias = (bias.shape, bias.dtype) if bias is not None else None
             ctx.mask = mask
             ctx.set_materialize_grads(False)
             return h, y
@@ -474,9 +474,8 @@ if torch is not None:
 
 def _grad_buffers(ctx, x, weight, at):
     """New buffers for those weights' gradients that are asked for."""
-    new = lambda dtype: torch.empty(x.shape[-1], dtype=dtype, device=x.device)  # noqa: E731
-    return (new(weight.dtype) if ctx.needs_input_grad[at] else None,
-            new(ctx.bias_dtype) if ctx.needs_input_grad[at + 1] else None)
+    return (torch.empty(weight.shape, dtype=weight.dtype, device=x.device) if ctx.needs_input_grad[at] else None,
+            torch.empty(ctx.bias[0], dtype=ctx.bias[1], device=x.device) if ctx.needs_input_grad[at + 1] else None)
 
 
 def _tracked(*tensors):

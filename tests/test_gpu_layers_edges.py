@@ -322,3 +322,18 @@ def test_a_frozen_input_costs_no_dropout(monkeypatch):
         got = torch.autograd.grad(g.residual_norm(*part, EPS, m)[0], rest[0], dh)[0]
         assert drops == [True] * expected
         assert torch.equal(got, dh if frozen == 0 else g.dropout_backward(dh, m))
+
+
+def test_weights_of_another_shape_get_gradients_of_it():
+    """weight and bias are taken by their elements in any shape."""
+    import torch
+    g, rng = G(), np.random.default_rng(4)
+    x, dy = (lu.matrix(rng.standard_normal((20, 48)), "f32") for _ in range(2))
+    w, b = vectors(48, "f32", rng)
+    y, mean, rstd = g.layer_norm_forward(x, w, b, EPS)
+    want = g.layer_norm_backward(dy, x, mean, rstd, w)
+    for shape in ((48,), (1, 48), (6, 8)):
+        leaf = [w.view(shape).clone().requires_grad_(), b.view(shape).clone().requires_grad_()]
+        for out in (g.layer_norm(x, *leaf, EPS), g.residual_norm(x, torch.zeros_like(x), *leaf, EPS)[1]):
+            got = torch.autograd.grad(out, leaf, dy)
+            assert all(p.shape == shape and torch.equal(p.reshape(-1), q) for p, q in zip(got, want[1:]))
