@@ -337,3 +337,111 @@ def test_weights_of_another_shape_get_gradients_of_it():
         for out in (g.layer_norm(x, *leaf, EPS), g.residual_norm(x, torch.zeros_like(x), *leaf, EPS)[1]):
             got = torch.autograd.grad(out, leaf, dy)
             assert all(p.shape == shape and torch.equal(p.reshape(-1), q) for p, q in zip(got, want[1:]))
+
+
+@pytest.mark.parametrize("dtype,size", [("f32", 10001), ("f32", 16001), ("bf16", 10001), ("bf16", 16001), ("f16", 2500),
+                                        ("f16", 4001), ("f16", 5000), ("f16", 7001), ("f16", 10001), ("f16", 16001)])
+def test_the_longest_shapes_of_many_rows(size, dtype):
+    """Above the number of rows that takes other shapes, against the oracle."""
+    from tests.test_gpu_layers import run_all
+    run_all(521, size, dtype, "f32", "padded" if size % 2 else "plain", seed=9)
+
+
+# a size for each shape of the kernels with rows in registers (the longest
+# row of a shape is as long in every format), and one of the kernels beyond
+SHAPES = [8, 13, 30, 61, 120, 190, 250, 380, 511, 700, 1001, 1500, 2041, 2900, 4001, 6001, 8100, 12001, 16001, 20001]
+STREAM = 144 << 20  # bytes that a call moves, above which it streams
+
+
+def normals(gen, rows, size, t):
+    import torch
+    return torch.randn(rows, size, generator=gen, device="cuda").to(t)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", SHAPES)
+def test_every_shape_streams(size, dtype):
+    """Calls that stream against calls on a quarter of the rows, which do not
+    and have the same shape: the same bits.  With dropout the sum is that of
+    the mask, its norm the norm's, and a sample of the gradients the oracle's;
+    the weights' gradients are sums in any order."""
+    import torch
+    g = G()
+    t, es = lu.torch_type(dtype), 4 if dtype == "f32" else 2
+    part = max(2085 if es == 2 and size <= 2048 else 521, STREAM // (6 * size * es))
+    rows = 4 * part
+    assert size > 16384 or 2 * rows * size * es > STREAM >= 4 * part * size * es  # longer rows never stream
+    gen = torch.Generator(device="cuda").manual_seed(size)
+    x, r, dy, dh = (normals(gen, rows, size, t) for _ in range(4))
+    w, b = vectors(size, "f32", np.random.default_rng(size))
+    h, y, mean, rstd = g.residual_norm_forward(x, r, w, b, EPS)
+    yn, mn, sn = g.layer_norm_forward(h, w, b, EPS)
+    assert torch.equal(yn, y) and torch.equal(mn, mean) and torch.equal(sn, rstd)
+    dres, _, dw, db = g.residual_norm_backward(dy, dh, h, mean, rstd, w)
+    dn, dwn, dbn = g.layer_norm_backward(dy, h, mean, rstd, w)
+    assert torch.equal(dwn, dw) and torch.equal(dbn, db)
+    for at in range(0, rows, part):
+        p = slice(at, at + part)
+        for got, want in zip(g.residual_norm_forward(x[p], r[p], w, b, EPS), (h, y, mean, rstd)):
+            assert torch.equal(got, want[p]), at
+        got = g.layer_norm_forward(h[p], w, b, EPS)[0]
+        assert torch.equal(got, y[p]), at
+        if 5 * part * size * es <= STREAM or size > 8192:  # longer rows' gradients do not stream
+            assert torch.equal(g.residual_norm_backward(dy[p], dh[p], h[p], mean[p], rstd[p], w)[0], dres[p]), at
+            assert torch.equal(g.layer_norm_backward(dy[p], h[p], mean[p], rstd[p], w)[0], dn[p]), at
+    for got, terms in ((dw, lambda p: dy[p].double() * (h[p].double() - mean[p].double()[:, None])
+                        * rstd[p].double()[:, None]), (db, lambda p: dy[p].double())):
+        total, size_of = torch.zeros(2, size, dtype=torch.float64, device="cuda")
+        for at in range(0, rows, part):
+            v = terms(slice(at, at + part))
+            total += v.sum(0)
+            size_of += v.abs_().sum(0)
+        assert ((got.double() - total).abs() <= (rows + 4) * lu.U * size_of).all()
+    # with dropout
+    m = mask()
+    f = g.dropout_forward(torch.ones(rows, size, device="cuda"), m)
+    hd, yd, md, sd = g.residual_norm_forward(x, r, w, b, EPS, m)
+    assert torch.equal(hd, (r.float() + torch.where(f != 0, x.float() * f, 0)).to(t))
+    yn, mn, sn = g.layer_norm_forward(hd, w, b, EPS)
+    assert torch.equal(yn, yd) and torch.equal(mn, md) and torch.equal(sn, sd)
+    dx, dd, dwd, dbd = g.residual_norm_backward(dy, dh, h, mean, rstd, w, m)
+    assert torch.equal(dd, dres) and torch.equal(dwd, dw) and torch.equal(dbd, db) and not dx[f == 0].any()
+    some = slice(3, None, max(1, rows // max(2, 200_000 // size)))
+    lu.check_norm_gradient(lu.values(dx[some]), None, None, lu.values(dy[some]), lu.values(h[some]),
+                           lu.values(mean[some]), lu.values(rstd[some]), lu.values(w), dtype, "f32",
+                           f"{rows} x {size} {dtype}", lu.values(dh[some]), lu.values(f[some]), lu.values(dres[some]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [5, 48, 257, 768, 2041, 2500, 5000, 9001, 16001, 40000])
+def test_in_place_over_several_turns(size, dtype):
+    """So many rows that a workgroup loads its next one before it has stored
+    the present one."""
+    import torch
+    g = G()
+    t = lu.torch_type(dtype)
+    rows = 24_000_000 // size
+    gen = torch.Generator(device="cuda").manual_seed(size)
+    x, r, dy, dh = (normals(gen, rows, size, t) for _ in range(4))
+    w, b = vectors(size, "f32", np.random.default_rng(size))
+    m = mask()
+    h, y, mean, rstd = g.residual_norm_forward(x, r, w, b, EPS, m)
+    want = g.residual_norm_backward(dy, dh, h, mean, rstd, w, m)
+    for over in (("x", "r"), ("r", "x")):
+        s = dict(x=x.clone(), r=r.clone())
+        got = g.residual_norm_forward(s["x"], s["r"], w, b, EPS, m, out_h=s[over[0]], out=s[over[1]])
+        assert all(torch.equal(p, q) for p, q in zip(got, (h, y, mean, rstd))), over
+    for over in (("dy", "dh"), ("dh", "h"), ("h", "dy")):
+        s = dict(dy=dy.clone(), dh=dh.clone(), h=h.clone())
+        got = g.residual_norm_backward(s["dy"], s["dh"], s["h"], mean, rstd, w, m, out=s[over[0]],
+                                       out_residual=s[over[1]])
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), over
+    s = h.clone()
+    assert torch.equal(g.layer_norm_forward(s, w, b, EPS, out=s)[0], y)
+    want = g.layer_norm_backward(dy, h, mean, rstd, w)
+    for over in ("dy", "h"):
+        s = dict(dy=dy.clone(), h=h.clone())
+        got = g.layer_norm_backward(s["dy"], s["h"], mean, rstd, w, out=s[over])
+        assert all(torch.equal(p, q) for p, q in zip(got, want)), over
+    s = x.clone()
+    assert torch.equal(g.dropout_forward(s, m, out=s), g.dropout_forward(x, m))
