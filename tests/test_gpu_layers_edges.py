@@ -445,3 +445,30 @@ def test_in_place_over_several_turns(size, dtype):
         assert all(torch.equal(p, q) for p, q in zip(got, want)), over
     s = x.clone()
     assert torch.equal(g.dropout_forward(s, m, out=s), g.dropout_forward(x, m))
+
+
+def test_the_readme_runs():
+    """README.md's examples of the layers, each by itself."""
+    import os
+    import re
+
+    import torch
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        blocks = [b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "residual_norm" in b]
+    assert len(blocks) == 2
+    g, rng = G(), np.random.default_rng(5)
+    x, residual, dy, dh = (lu.matrix(rng.standard_normal((20, 64)), "bf16") for _ in range(4))
+    for block in blocks:
+        weight, bias = vectors(64, "f32", rng)
+        for t in (weight, bias):
+            t.grad = torch.ones_like(t)
+        env = dict(G=g, seed=1, step=2, layer=3, mask=mask(), x=x, residual=residual, weight=weight, bias=bias, dy=dy,
+                   dh=dh)
+        exec(block, env)
+        m = env["mask"]
+        h, y, mean, rstd = g.residual_norm_forward(x, residual, weight, bias, mask=m)
+        assert torch.equal(env["h"], h) and torch.equal(env["y"], y)
+        if "dx" in env:
+            want = g.residual_norm_backward(dy, dh, h, mean, rstd, weight, m)
+            assert torch.equal(env["dx"], want[0]) and torch.equal(env["dresidual"], want[1])
+            assert env["dw"] is weight.grad and torch.equal(weight.grad, 1 + want[2])
