@@ -12,9 +12,9 @@ serve as device memory and streams: every step runs in the HIP kernels.
   buffers of the caller's, added to what the microbatches before left there
   when ``accumulate`` is set, from where a ``GradList`` clips them.
 - ``layer_norm``, ``dropout`` and ``residual_norm`` are the same under
-  autograd, in its backward mode: tensors with a tangent are refused.  To
-  capture a training step into a graph, capture the passes; a captured
-  autograd backward needs leaves that no eager graph holds.
+  autograd, in its backward mode: tensors with a tangent are refused, and so
+  is tracing.  To capture a training step into a graph, capture the passes; a
+  captured autograd backward needs leaves that no eager graph holds.
 
 A matrix is a tensor whose last dimension is adjacent in memory and whose
 other dimensions lie at one distance (a contiguous tensor, a slice of the

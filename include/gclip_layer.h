@@ -35,9 +35,17 @@
  *   - What is written may be exactly a matrix that is read (same address and
  *     ld: in place), and otherwise overlaps nothing.  Two matrices that lie
  *     in one buffer as different columns of the same ld do not overlap.
- *   - Arithmetic is binary32, with one rounding to the storage format; the
- *     statistics of rows whose binary32 sums overflow are taken in binary64.
- *     Results are bit-identical from run to run.
+ *   - Arithmetic is binary32, with one rounding to the storage format.  The
+ *     statistics of rows of 8 to 16384 columns are binary32 sums, taken again
+ *     of the row scaled by 2^-96 where they overflow; those of shorter and
+ *     longer rows are binary64 sums.  So a finite row's y is finite unless it
+ *     leaves the format itself, and so are its gradients while its sums of
+ *     dy * weight, and of that times n, stay in binary32.
+ *   - Results are bit-identical from run to run.  They may differ in the last
+ *     bits between calls of other shapes: few rows take kernels that sum a row
+ *     in another order (up to 512 rows forward; up to 2048 rows of up to 2048
+ *     columns in a 16-bit format backward), so a token's y can depend on how
+ *     many rows are with it.  h and the masks never do.
  *   - A NaN or infinity stays in its row (dweight and dbias apart), and
  *     where dropout drops an element it is 0 whatever it held.
  *   - rows may be 0: nothing is written but dweight and dbias, whose sums

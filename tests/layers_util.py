@@ -5,8 +5,9 @@ Tolerances, with u = 2^-24 (half a step of binary32, in which everything is
 computed) and half(T) half a step of the storage format T, to which results
 are rounded once.  A sum of k terms in any order is off by at most
 (k - 1) u times the sum of their absolute values.  The kernels add a row's
-terms in chains of at most CHAIN before a tree of at most ten levels, so 64
-stands for the longest path of such a sum."""
+terms in chains of at most 32 in a lane, then by a tree of six levels over a
+wave, then the sums of at most 16 waves: a path of at most 31 + 6 + 15 = 52
+additions (rows of other lengths in binary64), for which 64 stands."""
 import numpy as np
 
 U = 2.0 ** -24
