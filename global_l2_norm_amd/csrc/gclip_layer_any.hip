@@ -31,8 +31,9 @@ __device__ __forceinline__ double any_sum(double v, double* red) {
 // Three passes over a row: h and the sum, the squares, y; the later ones find
 // the row in the caches.  A thread reads there only the groups that it wrote
 // itself.  The sums are binary64, so no finite row overflows them.  Bound by
-// the passes' latency: 512 x 40000 in bfloat16 takes 28.9 us, 2.8 TB/s of the
-// row's one read and one write (1024 lanes a row: 33.0).
+// the passes' latency: 512 x 40000 in bfloat16 takes 28.3 us, 2.9 TB/s of the
+// row's one read and one write, and fetches it 2.7 times into the L2 (1024
+// lanes a row: 33.0 us).
 template <int DT, bool RES, bool DROP>
 __global__ __launch_bounds__(kRowThreads) void k_norm_any(FwdArgs a, DropArgs d) {
   __shared__ double red[kRowWaves];
@@ -378,7 +379,7 @@ __global__ __launch_bounds__(kAnyThreads) void k_norm_grad_short(BwdArgs a, Drop
 // accesses are adjacent then, and there is twice the time for it.  Bound by
 // memory, with the generator's products (20 for eight elements, at a quarter
 // of the full rate) close behind in 16 bits: 1.3B's 16384 x 2048 in bfloat16
-// takes 22.6 us, 5.9 TB/s (two units a lane 0.6 us more, four 1.6).
+// takes 22.3 us, 6.0 TB/s (two units a lane 0.6 us more, four 1.6).
 template <int DT, bool STREAMED>
 __global__ __launch_bounds__(kAnyThreads) void k_dropout(Rows x, Rows y, uint32_t rows, uint32_t size, DropArgs d) {
   const uint32_t units = (size + kUnit<DT> - 1) / kUnit<DT>;

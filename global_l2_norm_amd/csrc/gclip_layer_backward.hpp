@@ -18,12 +18,14 @@ namespace gclip {
 // unit -- leaves one part of them.  While a row is worked on, the loads of
 // the workgroup's next one are under way.
 //
-// Bound by memory: 16384 x 2048 in bfloat16 takes 34.7 us, 5.8 TB/s of two
-// reads and a write, and 4.8 us for the join of the parts (4 MB written and
+// Bound by memory: 16384 x 2048 in bfloat16 takes 36.1 us, 5.6 TB/s of two
+// reads and a write, and 4.6 us for the join of the parts (4 MB written and
 // read); the residual step's with dropout 54.3 us, 6.2 TB/s; 8192 x 768 in
-// binary32 13.8 us and 4.0.  Two workgroups a unit leave twice the parts: 22.6
-// -> 26.7 us for the last in all, then.  Rows that share a wave
-// (131071 x 64: 11.1 us, 4.5 TB/s) are bound by the operations of a row.
+// binary32 13.9 us and 3.9.  Two workgroups a unit leave twice the parts: 22.6
+// -> 26.7 us for the last in all, then.  Rows that share a wave (131071 x 64:
+// 11.6 us, 4.3 TB/s) have vector instructions under way for 71 % of the time
+// that a SIMD's four waves are there; the rest is the first load and the
+// meeting at the end, with four rows' turns between them.
 template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool STREAMED>
 __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(BwdArgs a, DropArgs d) {
   constexpr uint32_t kBwdThreads = bwd_threads(NV * kUnit<DT>);
@@ -166,7 +168,8 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_norm_rows_grad(
 
 // The sum of the parts: a workgroup takes 64 columns, its sixteen waves share
 // the parts, in a fixed order, all loads of a wave under way at once.  Bound
-// by latency: 2.2 us for 256 parts of 128 columns, 4.0 us for 4096 columns.
+// by latency: 256 parts of 128 columns take 2.2 to 3.8 us, of 4096 columns 3.5
+// to 4.6.
 constexpr uint32_t kJoinThreads = 1024;
 template <int DT>
 __global__ __launch_bounds__(kJoinThreads) void k_join_weight_grads(BwdArgs a) {

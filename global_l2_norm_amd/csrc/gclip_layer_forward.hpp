@@ -29,9 +29,9 @@ constexpr uint32_t fwd_workgroups(uint32_t columns) { return columns <= 8 ? 8 : 
 // taken from them in turn.  While a row is worked on, the loads of the
 // workgroup's next one are under way; weight and bias stay in registers.
 //
-// Bound by memory: 16384 x 2048 in bfloat16 takes 21.8 us, 6.2 TB/s of one
-// read and one write (a copy of such size: 5.4), the residual step with
-// dropout 44.3 us, 6.1 TB/s; 8192 x 768 in binary32 9.6 us, 5.3 TB/s.  With a
+// Bound by memory: 16384 x 2048 in bfloat16 takes 22.0 us, 6.1 TB/s of one
+// read and one write (a copy of these bytes: 22.7), the residual step with
+// dropout 44.0 us, 6.1 TB/s; 8192 x 768 in binary32 9.3 us, 5.4 TB/s.  With a
 // workgroup a row and three passes through the caches the first took 45.9 us.
 // Reading rows past the end as the last one, rather than not, keeps the loads
 // of the next row out of a branch, which would be waited for at its end

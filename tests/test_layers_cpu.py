@@ -252,3 +252,21 @@ def test_masks_do_not_change():
     assert m.at(step=5).args.step == 5
     for other in (copy.copy(m), copy.deepcopy(m), pickle.loads(pickle.dumps(m))):
         assert bytes(other.args) == bytes(m.args) and other.site == 4
+
+
+def test_the_profile_summary_is_of_the_present_kernels():
+    """profiles/layers__trace_pmc.txt names the code it was taken on, without
+    its comments."""
+    import hashlib
+    import os
+    import re
+
+    import bench
+    csrc = os.path.join("global_l2_norm_amd", "csrc")
+    h = hashlib.sha256()
+    for f in sorted(os.listdir(os.path.join(bench.ROOT, csrc))):
+        if f.startswith("gclip_layer"):
+            with open(os.path.join(bench.ROOT, csrc, f), encoding="utf-8") as src:
+                h.update(bench._code_only(src.read()).encode())
+    with open(os.path.join(bench.PROFILES, "layers__trace_pmc.txt")) as f:
+        assert re.search(r"^kernel_source_sha256_16: (\w+)$", f.read(), re.M)[1] == h.hexdigest()[:16]
