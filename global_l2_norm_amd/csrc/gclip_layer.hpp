@@ -133,8 +133,9 @@ inline uint32_t bwd_parts(uint32_t rows, uint32_t size) {
 constexpr uint64_t kStreamBytes = 144ull << 20;
 
 // A dispatch counts its lanes in each direction in 32 bits, and the largest
-// matrices have more units than that: workgroups beyond kGridRow go into
-// further rows of the grid, whose end no work is left for.
+// matrices have more units than that (a dropout of 2^32 units left some of
+// them undone, with no error): workgroups beyond kGridRow go into further
+// rows of the grid, whose end no work is left for.
 constexpr uint32_t kGridRow = 1u << 20;
 inline dim3 grid_of(uint64_t workgroups, uint32_t layers = 1) {
   const uint64_t x = workgroups < kGridRow ? workgroups : kGridRow;
