@@ -19,10 +19,10 @@ With ``own`` false, ``run`` computes them in elementary torch operations; with `
   activation     y = act(gate) up, or act(gate); act = silu: x / (1 + exp(-x)); gelu: x (1 + erf(x / sqrt 2)) / 2;
                  gelu_tanh: x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2; relu.  dgate = dy up act'(gate),
                  dup = dy act(gate), and y again where the checkpoint stands in for it
-  log probs      lse = log(sum(exp(x))), logp = x[target] - lse, entropy = -sum(p log p) with p = exp(x - lse);
-                 dx = dlogp (1[target] - p) - dentropy p (log p + entropy); the k largest with their columns, of equal
-                 ones the lowest column first.  Rows whose target is -100 count for nothing: zeros, and columns -1 with
-                 log probabilities -inf.
+  log probs      m = max(x), s = log(sum(exp(x - m))), log p = x - m - s, logp = log p[target], entropy = -sum(p log p);
+                 dx = dlogp (1[target] - p) - dentropy p (log p + entropy), from m and s; the k largest with their
+                 columns, of equal ones the lowest column first.  Rows whose target is -100 count for nothing: zeros,
+                 and columns -1 with log probabilities -inf.
 """
 import math
 
@@ -42,7 +42,7 @@ OPS = ("norm_forward", "norm_backward", "residual_forward", "residual_backward",
 
 def _case(name, op, rows, size, dtype, weights="f32", p=0.0, stats=True, packed="", keep=False, pad=0, accumulate=False,
           kind="silu", gated=True, recompute=False, entropy=True, top=0, masked=False):
-    """weights: type of weight and its gradient; stats: keep rstd for a backward pass; packed: y in 8 bits, a scale for
+    """weights: type of weight and its gradient; stats: keep rstd, or m and s, for a backward pass; packed: y in 8 bits, a scale for
     each "row" or "block"; keep: also leave (forward), or start from (backward), a checkpoint in 8 bits; pad: columns
     between the end of a row and the next; recompute: y again in the backward pass; top: alternatives wanted; masked:
     logits of -inf (a padded vocabulary, and rows where few tokens are allowed) and rows that are not counted."""
@@ -52,7 +52,7 @@ def _case(name, op, rows, size, dtype, weights="f32", p=0.0, stats=True, packed=
     elif op.startswith("activation"):
         c.update(kind=kind, gated=gated, keep=keep, pad=pad, recompute=recompute)
     elif op.startswith("logp"):
-        c.update(entropy=entropy, top=top, masked=masked, pad=pad)
+        c.update(entropy=entropy, stats=stats, top=top, masked=masked, pad=pad)
     else:
         c.update(packed=packed or "block", pad=pad)
     return {"name": name, **c} if name else c
@@ -79,7 +79,7 @@ def listed():
         # ... and out of them
         _case("1.3B unpack", "unpack", 16384, 2048, "bf16"),
         # eight requests' next tokens with their alternatives, a padded vocabulary, some of it not allowed
-        _case("8 requests top 20", "logp_forward", 8, 131072, "bf16", top=20, masked=True),
+        _case("8 requests top 20", "logp_forward", 8, 131072, "bf16", stats=False, top=20, masked=True),
         # the loss of a microbatch of the 120M model: log probabilities and entropies, and their gradient
         _case("120M log probs step", "logp_step", 8192, 8449, "f32"),
         # their gradient in the 1.3B model, some tokens not counted
@@ -182,7 +182,7 @@ def prepare(case, seed):
         if op != "logp_forward":
             s["dlogp"], s["dentropy"] = -1.0 / rows + 0.1 / rows * normal(rows), 1e-2 / rows * normal(rows) if case["entropy"] else None
         if op == "logp_backward":
-            _, s["entropy"], s["lse"] = _logp_rows(x, s["targets"], True)
+            _, s["entropy"], s["stats"] = _logp_rows(x, s["targets"], True)
     elif op == "pack":
         s["x"] = matrix(1.0, *channels())
     else:
@@ -327,6 +327,7 @@ def _plain_activation(s):
 
 
 def _logp_rows(logits, targets, entropy):
+    """log p of the targets, entropy, and m and s of each row."""
     x = logits.float()
     m = x.amax(1)
     t = x - m[:, None]
@@ -334,31 +335,32 @@ def _logp_rows(logits, targets, entropy):
     total = e.sum(1)
     counted = targets != IGNORED
     zero = torch.zeros_like(m)
-    lse = m + torch.log(total)
-    logp = torch.where(counted, x.gather(1, targets.clamp(min=0)[:, None])[:, 0] - lse, zero)
+    logs = torch.log(total)
+    logp = torch.where(counted, t.gather(1, targets.clamp(min=0)[:, None])[:, 0] - logs, zero)
     h = None
     if entropy:
-        h = torch.log(total) - torch.where(e > 0.0, t * e, torch.zeros_like(t)).sum(1) / total
+        h = logs - torch.where(e > 0.0, t * e, torch.zeros_like(t)).sum(1) / total
         h = torch.where(counted, h, zero)
-    return logp, h, lse
+    return logp, h, torch.where(counted[:, None], torch.stack((m, logs), 1), zero[:, None])
 
 
 def _plain_logp(s):
     case, op, dt = s["case"], s["case"]["op"], DTYPES[s["case"]["dtype"]]
-    out, entropy, lse = (), s.get("entropy"), s.get("lse")
+    out, entropy, stats = (), s.get("entropy"), s.get("stats")
     counted = s["targets"] != IGNORED
     if op != "logp_backward":
-        logp, entropy, lse = _logp_rows(s["logits"], s["targets"], case["entropy"])
-        out = (logp, *((entropy,) if case["entropy"] else ()))
+        logp, entropy, stats = _logp_rows(s["logits"], s["targets"], case["entropy"])
+        out = (logp, *((entropy,) if case["entropy"] else ()), *((stats,) if case["stats"] else ()))
         if case["top"]:
             value, column = torch.sort(s["logits"].float(), dim=1, descending=True, stable=True)
-            value, column = value[:, :case["top"]] - lse[:, None], column[:, :case["top"]]
+            value, column = value[:, :case["top"]] - stats[:, :1] - stats[:, 1:], column[:, :case["top"]]
             out = (*out, torch.where(counted[:, None], value, torch.full_like(value, float("-inf"))),
                    torch.where(counted[:, None], column, torch.full_like(column, -1)))
     if op != "logp_forward":
-        z = s["logits"].float() - lse[:, None]
-        p = torch.exp(z)
+        z = s["logits"].float() - stats[:, :1] - stats[:, 1:]
         dlogp = torch.where(counted, s["dlogp"], torch.zeros_like(s["dlogp"]))
+        z = torch.where(counted[:, None], z, torch.zeros_like(z))
+        p = torch.exp(z)
         d = -p * dlogp[:, None]
         if case["entropy"]:
             dh = torch.where(counted, s["dentropy"], torch.zeros_like(s["dentropy"]))
@@ -432,13 +434,14 @@ def _activation_calls(G, s, case, op):
 
 
 def _logp_calls(G, s, case, op):
-    out, entropy, lse = (), s.get("entropy"), s.get("lse")
+    out, entropy, stats = (), s.get("entropy"), s.get("stats")
     if op != "logp_backward":
-        r = G.token_log_probs_forward(s["logits"], s["targets"], entropy=case["entropy"], top=case["top"])
-        entropy, lse = r.entropy, r.lse
-        out = (r.logp, *((entropy,) if case["entropy"] else ()), *((r.top_logp, r.top_ids) if case["top"] else ()))
+        r = G.token_log_probs_forward(s["logits"], s["targets"], entropy=case["entropy"], top=case["top"], stats=case["stats"])
+        entropy, stats = r.entropy, r.stats
+        out = (r.logp, *((entropy,) if case["entropy"] else ()), *((stats,) if case["stats"] else ()),
+               *((r.top_logp, r.top_ids) if case["top"] else ()))
     if op != "logp_forward":
-        out = (*out, G.token_log_probs_backward(s["dlogp"], s["dentropy"], s["logits"], s["targets"], lse, entropy))
+        out = (*out, G.token_log_probs_backward(s["dlogp"], s["dentropy"], s["logits"], s["targets"], stats, entropy))
     return out
 
 
@@ -456,7 +459,7 @@ def work(case):
     back, fore = not op.endswith("forward"), not op.endswith("backward")
     if op.startswith("logp"):
         # the logits once for each direction; a row's numbers
-        return {"bytes": n * e * (fore + 2 * back) + rows * (8 + 12 * fore + 16 * back + 12 * case["top"]),
+        return {"bytes": n * e * (fore + 2 * back) + rows * (8 + (8 + 8 * case["stats"]) * fore + 20 * back + 12 * case["top"]),
                 "flops": n * ((6 if case["entropy"] else 4) * fore + (8 if case["entropy"] else 4) * back)}
     if op.startswith("activation"):
         inputs = 2 if case["gated"] else 1
@@ -609,19 +612,20 @@ def _exact_logp(s, case, op):
         out.append(z.gather(1, target).squeeze(1).masked_fill(~counted, 0.0))
         if case["entropy"]:
             out.append(h)
+        if case["stats"]:
+            m = x.max(1).values
+            out.append(torch.stack((m, x.logsumexp(1) - m), 1).masked_fill(~counted.unsqueeze(1), 0.0))
         if case["top"]:
             out += [z.sort(1, descending=True).values[:, :case["top"]].masked_fill(~counted.unsqueeze(1), -math.inf), None]
     if op != "logp_forward":
-        lse = s["lse"].double().unsqueeze(1) if op == "logp_backward" else x.logsumexp(1, keepdim=True)
-        z = x - lse
-        p = z.exp()
         if op == "logp_backward":
-            h = s["entropy"].double()
+            z = x - s["stats"].double().sum(1, keepdim=True)
+            p, h = z.exp(), s["entropy"].double()
         onto = torch.zeros_like(p).scatter_(1, target, 1.0)
         d = (onto - p) * s["dlogp"].double().unsqueeze(1)
         if case["entropy"]:
             d -= torch.where(p.gt(0), p * (z + h.unsqueeze(1)), 0.0) * s["dentropy"].double().unsqueeze(1)
-        out.append(d * counted.unsqueeze(1))
+        out.append(torch.where(counted.unsqueeze(1), d, 0.0))
     return tuple(out)
 
 
