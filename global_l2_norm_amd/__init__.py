@@ -30,6 +30,13 @@ __all__ = ["GclipError", "GclipResult", "GradList", "clip_grad_norm_", "gclip_li
            "layer_norm_backward", "residual_norm", "residual_norm_forward", "residual_norm_backward",
            "gclip_layernorm_forward", "gclip_layernorm_backward", "gclip_residual_forward", "gclip_residual_backward",
            "gclip_dropout_apply", "gclip_layer_workspace",
+           "Packed8", "pack8", "unpack8", "rms_norm", "rms_norm_forward", "rms_norm_backward", "residual_rms_norm",
+           "residual_rms_norm_forward", "residual_rms_norm_backward", "activation", "activation_forward",
+           "activation_backward", "gclip_rmsnorm_forward", "gclip_rmsnorm_backward", "gclip_residual_rms_forward",
+           "gclip_residual_rms_backward", "gclip_rms_workspace", "gclip_activation_forward",
+           "gclip_activation_backward", "gclip_pack", "gclip_unpack",
+           "TokenLogProbs", "token_log_probs", "token_log_probs_forward", "token_log_probs_backward",
+           "gclip_logprob_forward", "gclip_logprob_backward", "gclip_logprob_workspace",
            "GCLIP_F32", "GCLIP_F16", "GCLIP_BF16", "GCLIP_PATH_AUTO", "GCLIP_PATH_FUSED", "GCLIP_PATH_SPLIT"]
 
 DTYPE_CODES = {"f32": GCLIP_F32, "f16": GCLIP_F16, "bf16": GCLIP_BF16}
@@ -511,3 +518,10 @@ from .layers import (DropoutMask, dropout, dropout_backward, dropout_forward, gc
                      gclip_layer_workspace, gclip_layernorm_backward, gclip_layernorm_forward,
                      gclip_residual_backward, gclip_residual_forward, layer_norm, layer_norm_backward,
                      layer_norm_forward, residual_norm, residual_norm_backward, residual_norm_forward)
+from .block import (Packed8, activation, activation_backward, activation_forward, gclip_activation_backward,  # noqa: E402
+                    gclip_activation_forward, gclip_pack, gclip_residual_rms_backward, gclip_residual_rms_forward,
+                    gclip_rms_workspace, gclip_rmsnorm_backward, gclip_rmsnorm_forward, gclip_unpack, pack8,
+                    residual_rms_norm, residual_rms_norm_backward, residual_rms_norm_forward, rms_norm,
+                    rms_norm_backward, rms_norm_forward, unpack8)
+from .logprob import (TokenLogProbs, gclip_logprob_backward, gclip_logprob_forward,  # noqa: E402
+                      gclip_logprob_workspace, token_log_probs, token_log_probs_backward, token_log_probs_forward)

@@ -1,4 +1,4 @@
-"""ctypes declarations of libgclip's C ABI (include/gclip.h, gclip_layer.h).
+"""ctypes declarations of libgclip's C ABI (include/gclip.h, gclip_layer.h, gclip_block.h, gclip_logprob.h).
 
 Marshalling only: every step of the clipping path runs in the HIP kernels of
 libgclip.so.  Importing this module fails loudly when the library has not
@@ -16,6 +16,10 @@ GCLIP_F32, GCLIP_F16, GCLIP_BF16 = 0, 1, 2
 GCLIP_OK, GCLIP_EINVAL, GCLIP_EDTYPE, GCLIP_ENOMEM, GCLIP_EHIP, GCLIP_ENONFINITE, GCLIP_EDEVICE, GCLIP_ERANGE = range(8)
 GCLIP_NOALLOC_SCRATCH_BYTES = 4 << 20
 GCLIP_PATH_AUTO, GCLIP_PATH_FUSED, GCLIP_PATH_SPLIT = 0, 1, 2
+GCLIP_SCALE_BLOCK = 128
+GCLIP_SCALES_BLOCK, GCLIP_SCALES_ROW = 0, 1
+GCLIP_ACT_SILU, GCLIP_ACT_GELU, GCLIP_ACT_GELU_TANH, GCLIP_ACT_RELU = range(4)
+GCLIP_LOGPROB_MAX_TOP = 32
 
 STATUS_NAMES = {GCLIP_OK: "GCLIP_OK", GCLIP_EINVAL: "GCLIP_EINVAL", GCLIP_EDTYPE: "GCLIP_EDTYPE",
                 GCLIP_ENOMEM: "GCLIP_ENOMEM", GCLIP_EHIP: "GCLIP_EHIP", GCLIP_ENONFINITE: "GCLIP_ENONFINITE",
@@ -90,6 +94,47 @@ class GclipLayerBackward(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_int64)]
 
 
+class GclipPacked8(ctypes.Structure):
+    _fields_ = [("values", ctypes.c_void_p), ("ld", ctypes.c_int64), ("scales", ctypes.c_void_p),
+                ("mode", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class GclipRmsForward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_double), ("x", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("residual", ctypes.c_void_p), ("ldresidual", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("y", ctypes.c_void_p),
+                ("ldy", ctypes.c_int64), ("y8", GclipPacked8), ("kept", GclipPacked8), ("rstd", ctypes.c_void_p)]
+
+
+class GclipRmsBackward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x8", GclipPacked8), ("rstd", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("dresidual", ctypes.c_void_p), ("lddresidual", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
+class GclipActivate(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("gate", ctypes.c_void_p), ("ldgate", ctypes.c_int64),
+                ("up", ctypes.c_void_p), ("ldup", ctypes.c_int64), ("gate8", GclipPacked8), ("up8", GclipPacked8),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64),
+                ("dgate", ctypes.c_void_p), ("lddgate", ctypes.c_int64), ("dup", ctypes.c_void_p),
+                ("lddup", ctypes.c_int64)]
+
+
+class GclipLogprobs(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("size", ctypes.c_int64), ("dtype", ctypes.c_int32), ("top", ctypes.c_int32),
+                ("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("targets", ctypes.c_void_p),
+                ("ignore", ctypes.c_int64), ("stats", ctypes.c_void_p), ("logp", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p), ("top_logp", ctypes.c_void_p), ("top_ids", ctypes.c_void_p),
+                ("dlogp", ctypes.c_void_p), ("dentropy", ctypes.c_void_p), ("dlogits", ctypes.c_void_p),
+                ("lddlogits", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
+
+
 assert ctypes.sizeof(GclipResult) == 64
 assert ctypes.sizeof(GclipAmpState) == 16
 
@@ -133,6 +178,18 @@ def _declare(lib):
         "gclip_residual_backward": ([ctypes.POINTER(GclipLayerBackward), ctypes.POINTER(GclipDropout), vp], i32),
         "gclip_dropout_apply": ([vp, i64, vp, i64, i64, i64, i32, ctypes.POINTER(GclipDropout), vp], i32),
         "gclip_layer_workspace": ([i64, i64], i64),
+        "gclip_rmsnorm_forward": ([ctypes.POINTER(GclipRmsForward), vp], i32),
+        "gclip_rmsnorm_backward": ([ctypes.POINTER(GclipRmsBackward), vp], i32),
+        "gclip_residual_rms_forward": ([ctypes.POINTER(GclipRmsForward), ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_residual_rms_backward": ([ctypes.POINTER(GclipRmsBackward), ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_rms_workspace": ([i64, i64], i64),
+        "gclip_activation_forward": ([ctypes.POINTER(GclipActivate), vp], i32),
+        "gclip_activation_backward": ([ctypes.POINTER(GclipActivate), vp], i32),
+        "gclip_pack": ([vp, i64, ctypes.POINTER(GclipPacked8), i64, i64, i32, vp], i32),
+        "gclip_unpack": ([ctypes.POINTER(GclipPacked8), vp, i64, i64, i64, i32, vp], i32),
+        "gclip_logprob_forward": ([ctypes.POINTER(GclipLogprobs), vp], i32),
+        "gclip_logprob_backward": ([ctypes.POINTER(GclipLogprobs), vp], i32),
+        "gclip_logprob_workspace": ([i64, i64, i32], i64),
         "gclip_status_string": ([i32], ctypes.c_char_p),
         "gclip_last_hip_error": ([], i32),
         "gclip_version": ([], i32),
@@ -162,7 +219,7 @@ def load():
 
 lib = load()
 
-# The C ABI's declared entry points (include/gclip.h, gclip_ref.h and gclip_layer.h), for the export check.
+# The C ABI's declared entry points (include/*.h but gclip_stamps.h), for the export check.
 EXPORTS = ("gclip_list_create", "gclip_list_destroy", "gclip_list_info", "gclip_list_set_path",
            "gclip_list_set_wait", "gclip_norm",
            "gclip_scale", "gclip_clip_", "gclip_result_read", "gclip_plan_query", "gclip_plan_trace", "gclip_status_string",
@@ -171,4 +228,7 @@ EXPORTS = ("gclip_list_create", "gclip_list_destroy", "gclip_list_info", "gclip_
            "gclip_clip_per_tensor_", "gclip_contrib_create", "gclip_contrib_destroy", "gclip_accumulate_norm",
            "gclip_accumulate_clip_", "gclip_set_gather_wait", "gclip_clip_noalloc_", "gclip_ref_read",
            "gclip_ref_copy", "gclip_layernorm_forward", "gclip_layernorm_backward", "gclip_residual_forward",
-           "gclip_residual_backward", "gclip_dropout_apply", "gclip_layer_workspace")
+           "gclip_residual_backward", "gclip_dropout_apply", "gclip_layer_workspace", "gclip_rmsnorm_forward",
+           "gclip_rmsnorm_backward", "gclip_residual_rms_forward", "gclip_residual_rms_backward",
+           "gclip_rms_workspace", "gclip_activation_forward", "gclip_activation_backward", "gclip_pack",
+           "gclip_unpack", "gclip_logprob_forward", "gclip_logprob_backward", "gclip_logprob_workspace")

@@ -22,7 +22,13 @@ STAMPS_LIB = os.path.join(HERE, "_stamps", "libgclip.so")
 SOURCES = ["gclip_api.cpp", "gclip_plan.cpp", "gclip_trace.cpp", "gclip_kernels.hip", "gclip_tensor.hip",
            "gclip_adamw.hip", "gclip_noalloc.hip", "gclip_ref.hip", "gclip_layer_api.cpp", "gclip_layer_any.hip",
            "gclip_layer_forward_f32.hip", "gclip_layer_forward_f16.hip", "gclip_layer_forward_bf16.hip",
-           "gclip_layer_backward_f32.hip", "gclip_layer_backward_f16.hip", "gclip_layer_backward_bf16.hip"]
+           "gclip_layer_backward_f32.hip", "gclip_layer_backward_f16.hip", "gclip_layer_backward_bf16.hip",
+           "gclip_rms_forward8_f32.hip", "gclip_rms_forward8_f16.hip", "gclip_rms_forward8_bf16.hip",
+           "gclip_rms_forward_f32.hip", "gclip_rms_forward_f16.hip", "gclip_rms_forward_bf16.hip",
+           "gclip_rms_backward8_f32.hip", "gclip_rms_backward8_f16.hip", "gclip_rms_backward8_bf16.hip",
+           "gclip_rms_backward_f32.hip", "gclip_rms_backward_f16.hip", "gclip_rms_backward_bf16.hip",
+           "gclip_rms_any.hip", "gclip_activation_f32.hip", "gclip_activation_f16.hip", "gclip_activation_bf16.hip",
+           "gclip_pack8.hip", "gclip_block_api.cpp", "gclip_logprob.hip", "gclip_logprob_api.cpp"]
 ARCH = os.environ.get("GCLIP_OFFLOAD_ARCH", "gfx950")
 
 

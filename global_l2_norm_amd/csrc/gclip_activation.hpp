@@ -1,0 +1,165 @@
+// gclip_activation.hpp -- the (gated) activation and its gradient;
+// instantiated for one storage format in each of gclip_activation_*.hip.
+#pragma once
+
+#include "gclip_block_device.hpp"
+
+namespace gclip {
+
+constexpr int kActThreads = 256;
+
+// e^x: of the 16-bit formats by the hardware's power of two alone, whose
+// error (|x| 2^-24 of the result) is far below the format's step.
+template <int DT>
+__device__ __forceinline__ float exponential(float x) {
+  if constexpr (DT == GCLIP_F32) return expf(x);
+  else return __builtin_amdgcn_exp2f(x * 1.44269504088896f);
+}
+template <int DT>
+__device__ __forceinline__ float reciprocal(float x) {
+  if constexpr (DT == GCLIP_F32) return 1.0f / x;
+  else return __builtin_amdgcn_rcpf(x);
+}
+
+// act(x) and, where wanted, its derivative.  With p = 1 / (1 + e^-x), 1 - p is
+// taken from e^-x p where p is near 1.
+template <int DT, int KIND, bool SLOPE>
+__device__ __forceinline__ float activated(float x, float& slope) {
+  if constexpr (KIND == GCLIP_ACT_RELU) {
+    if (SLOPE) slope = x > 0.0f ? 1.0f : x != x ? x : 0.0f;
+    return x < 0.0f ? 0.0f : x;
+  } else if constexpr (KIND == GCLIP_ACT_SILU) {
+    const float e = exponential<DT>(-x), p = reciprocal<DT>(1.0f + e);
+    if (SLOPE) slope = p * __builtin_fmaf(x, x > 0.0f ? e * p : 1.0f - p, 1.0f);
+    return x * p;
+  } else if constexpr (KIND == GCLIP_ACT_GELU) {
+    const float c = 0.5f * erfcf(x * -0.707106781186547524f);
+    if (SLOPE) slope = __builtin_fmaf(x * 0.398942280401432678f, exponential<DT>(-0.5f * x * x), c);
+    return x * c;
+  } else {
+    // (1 + tanh(u)) / 2 = 1 / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)
+    const float xx = x * x, t = 1.59576912160573071f * x * __builtin_fmaf(xx, 0.044715f, 1.0f);  // 2 u
+    const float e = exponential<DT>(-t), p = reciprocal<DT>(1.0f + e);
+    if (SLOPE) {
+      // beyond 16 the slope is 0 or 1, and the polynomial would leave binary32
+      const float s = fminf(fmaxf(x, -16.0f), 16.0f), du = 1.59576912160573071f * __builtin_fmaf(s * s, 3.0f * 0.044715f, 1.0f);
+      slope = p * __builtin_fmaf(s * du, x > 0.0f ? e * p : 1.0f - p, 1.0f);
+    }
+    return x * p;
+  }
+}
+
+// y = act(gate) up, a unit of 16 bytes a lane; with KEEP the lanes of a block
+// also share their scale and leave gate and up in 8 bits.
+template <int DT, int KIND, bool GATED, bool KEEP, bool STREAMED>
+__global__ __launch_bounds__(kActThreads) void k_activation(ActArgs a, Split split) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint64_t i = workgroup_of_grid() * kActThreads + threadIdx.x;
+  const uint32_t r = row_of(i, split);
+  if (r >= a.rows) return;  // whole blocks of lanes
+  const uint32_t c = (uint32_t)(i - r * split.of) * kU;
+  const bool in = c < a.size;
+  if (!KEEP && !in) return;
+  u32x4 g{0u, 0u, 0u, 0u}, u{0u, 0u, 0u, 0u};
+  if (in) {
+    g = load_unit_at<DT, STREAMED>(a.gate.at + r * a.gate.ld, c, a.size);
+    if (GATED) u = load_unit_at<DT, STREAMED>(a.up.at + r * a.up.ld, c, a.size);
+  }
+  float x[kU], y[kU], b[kU], none;
+  unpack_unit<DT>(g, x);
+  unpack_unit<DT>(u, b);
+#pragma unroll
+  for (uint32_t j = 0; j < kU; ++j) {
+    y[j] = activated<DT, KIND, false>(x[j], none);
+    if (GATED) y[j] *= b[j];
+  }
+  if (in) store_unit<DT, true>(a.y.at + r * a.y.ld, c / kU, a.size, pack_unit<DT>(y));
+  if constexpr (KEEP) {
+    const bool first = threadIdx.x % kBlockLanes<DT> == 0;
+    const float sg = block_scale<DT, kBlockLanes<DT>>(g);
+    if (in) store_eight<DT, true>(a.gate8.at + r * a.gate8.ld, c, unit_eight<DT>(x, 1.0f / sg));
+    if (in && first) store_scale(a.gate8, r, c / kBlock, sg);
+    if constexpr (GATED) {
+      const float su = block_scale<DT, kBlockLanes<DT>>(u);
+      if (in) store_eight<DT, true>(a.up8.at + r * a.up8.ld, c, unit_eight<DT>(b, 1.0f / su));
+      if (in && first) store_scale(a.up8, r, c / kBlock, su);
+    }
+  }
+}
+
+// dgate = dy up act'(gate), dup = dy act(gate), and y again where wanted.
+template <int DT, int KIND, bool GATED, bool EIGHT, bool STREAMED>
+__global__ __launch_bounds__(kActThreads) void k_activation_grad(ActArgs a, Split split) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint64_t i = workgroup_of_grid() * kActThreads + threadIdx.x;
+  const uint32_t r = row_of(i, split);
+  if (r >= a.rows) return;
+  const uint32_t c = (uint32_t)(i - r * split.of) * kU;
+  float x[kU], b[kU], d[kU];
+  const u32x4 dy = load_unit_at<DT, STREAMED>(a.dy.at + r * a.dy.ld, c, a.size);
+  if constexpr (EIGHT) {
+    const Unit8<DT> g = load_eight<DT, STREAMED>(a.gate8.at + r * a.gate8.ld, c);
+    const float sg = load_scale(a.gate8, r, c);
+    if constexpr (GATED) {
+      const Unit8<DT> u = load_eight<DT, STREAMED>(a.up8.at + r * a.up8.ld, c);
+      unit_value<DT>(u, load_scale(a.up8, r, c), b);
+    }
+    unit_value<DT>(g, sg, x);
+  } else {
+    const u32x4 g = load_unit_at<DT, STREAMED>(a.gate.at + r * a.gate.ld, c, a.size);
+    if constexpr (GATED) unpack_unit<DT>(load_unit_at<DT, STREAMED>(a.up.at + r * a.up.ld, c, a.size), b);
+    unpack_unit<DT>(g, x);
+  }
+  unpack_unit<DT>(dy, d);
+  float y[kU], dg[kU], du[kU];
+#pragma unroll
+  for (uint32_t j = 0; j < kU; ++j) {
+    float slope;
+    y[j] = activated<DT, KIND, true>(x[j], slope);
+    if constexpr (GATED) {
+      dg[j] = d[j] * b[j] * slope;
+      du[j] = d[j] * y[j];
+      y[j] *= b[j];
+    } else {
+      dg[j] = d[j] * slope;
+    }
+  }
+  store_unit<DT, true>(a.dgate.at + r * a.dgate.ld, c / kU, a.size, pack_unit<DT>(dg));
+  if constexpr (GATED) store_unit<DT, true>(a.dup.at + r * a.dup.ld, c / kU, a.size, pack_unit<DT>(du));
+  if (a.y.at) store_unit<DT, true>(a.y.at + r * a.y.ld, c / kU, a.size, pack_unit<DT>(y));
+}
+
+template <int DT, int KIND, bool GATED, bool STREAMED>
+hipError_t activation_launch(const ActArgs& a, bool backward, hipStream_t st) {
+  const bool keep = !backward && a.gate8.at, eight = backward && a.gate8.at;
+  // lanes of a row: its units, or whole blocks where lanes share a scale
+  const uint64_t of = keep ? (uint64_t)a.gate8.count * kBlockLanes<DT> : (a.size - 1) / kUnit<DT> + 1;
+  const Split split{of, 1.0 / (double)of};
+  const dim3 grid = grid_of((of * a.rows + kActThreads - 1) / kActThreads), block(kActThreads);
+  if (keep) hipLaunchKernelGGL((k_activation<DT, KIND, GATED, true, STREAMED>), grid, block, 0, st, a, split);
+  else if (!backward) hipLaunchKernelGGL((k_activation<DT, KIND, GATED, false, STREAMED>), grid, block, 0, st, a, split);
+  else if (eight) hipLaunchKernelGGL((k_activation_grad<DT, KIND, GATED, true, STREAMED>), grid, block, 0, st, a, split);
+  else hipLaunchKernelGGL((k_activation_grad<DT, KIND, GATED, false, STREAMED>), grid, block, 0, st, a, split);
+  return hipGetLastError();
+}
+
+template <int DT, int KIND>
+hipError_t activation_kind(const ActArgs& a, bool backward, bool streamed, hipStream_t st) {
+  const bool gated = a.up.at || a.up8.at;
+  if (gated) return streamed ? activation_launch<DT, KIND, true, true>(a, backward, st)
+                             : activation_launch<DT, KIND, true, false>(a, backward, st);
+  return streamed ? activation_launch<DT, KIND, false, true>(a, backward, st)
+                  : activation_launch<DT, KIND, false, false>(a, backward, st);
+}
+
+template <int DT>
+hipError_t activation_of(const ActArgs& a, int32_t kind, bool backward, bool streamed, hipStream_t st) {
+  switch (kind) {
+    case GCLIP_ACT_SILU: return activation_kind<DT, GCLIP_ACT_SILU>(a, backward, streamed, st);
+    case GCLIP_ACT_GELU: return activation_kind<DT, GCLIP_ACT_GELU>(a, backward, streamed, st);
+    case GCLIP_ACT_GELU_TANH: return activation_kind<DT, GCLIP_ACT_GELU_TANH>(a, backward, streamed, st);
+    default: return activation_kind<DT, GCLIP_ACT_RELU>(a, backward, streamed, st);
+  }
+}
+
+}  // namespace gclip

@@ -1,0 +1,526 @@
+// gclip_logprob.hip -- log probabilities of given tokens, with the entropy
+// and the likeliest alternatives, and their gradient.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gclip_layer_device.hpp"
+#include "gclip_logprob.hpp"
+
+namespace gclip {
+namespace {
+
+constexpr int kWaves = kLogpThreads / 64;
+constexpr int kChunk = 4;  // units of a lane at a time
+constexpr uint32_t kCandidates = 1024;
+static_assert(GCLIP_LOGPROB_MAX_TOP * GCLIP_LOGPROB_MAX_TOP <= kCandidates, "the join's candidates");
+constexpr float kLog2e = 1.44269504088896f;
+constexpr float kLowest = -0x1.fffffep+127f;
+constexpr float kNone = -__builtin_huge_valf();
+
+// ---------------------------------------------------------------- a softmax on the way
+// Of the logits so far: the largest, m (-infinity: none that can come), and
+// relative to r = max(m, the lowest finite number) the sums of e^(x - r) and
+// of (x - r) e^(x - r).  Differences are taken before anything is multiplied,
+// so logits of any size, the lowest finite ones too, keep theirs.  A NaN or
+// an infinity in a row makes s a NaN, which stays.
+struct Softmax {
+  float m, s, t;
+};
+__device__ __forceinline__ float reference(float m) { return fmaxf(m, kLowest); }
+// The difference of two references; finite, so that nothing times it is nothing.
+__device__ __forceinline__ float drop_to(float from, float to) { return fmaxf(reference(from) - reference(to), -1e30f); }
+
+template <bool ENTROPY>
+__device__ __forceinline__ void rebase(Softmax& z, float m) {
+  const float delta = drop_to(z.m, m), f = __builtin_amdgcn_exp2f(delta * kLog2e);
+  if (ENTROPY) z.t = f * __builtin_fmaf(delta, z.s, z.t);
+  z.s *= f;
+  z.m = m;
+}
+
+template <bool ENTROPY, int N>
+__device__ __forceinline__ void take(Softmax& z, const float (&v)[N]) {
+  float m = z.m;
+#pragma unroll
+  for (int j = 0; j < N; ++j) m = fmaxf(m, v[j]);
+  rebase<ENTROPY>(z, m);
+  const float r = reference(m);
+  float s = 0.0f, t = 0.0f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const float d = v[j] - r, e = __builtin_amdgcn_exp2f(d * kLog2e);
+    s += e;
+    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, -1e30f), t);
+  }
+  z.s += s;
+  if (ENTROPY) z.t += t;
+}
+
+template <int N>
+__device__ __forceinline__ float lanes_largest(float v) {
+  if constexpr (N >= 2) v = fmaxf(v, permuted<0xB1>(v));
+  if constexpr (N >= 4) v = fmaxf(v, permuted<0x4E>(v));
+  if constexpr (N >= 8) v = fmaxf(v, permuted<0x141>(v));
+  if constexpr (N >= 16) v = fmaxf(v, permuted<0x140>(v));
+  if constexpr (N >= 32) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  if constexpr (N >= 64) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  }
+  return v;
+}
+
+// The workgroup's softmax from its threads', in all of them, in a fixed order.
+template <bool ENTROPY>
+__device__ __forceinline__ Softmax joined(Softmax z, float (*red)[4]) {
+  rebase<ENTROPY>(z, lanes_largest<64>(z.m));
+  z.s = lanes_sum<64>(z.s);
+  if (ENTROPY) z.t = lanes_sum<64>(z.t);
+  if ((threadIdx.x & 63) == 0) {
+    red[threadIdx.x >> 6][0] = z.m;
+    red[threadIdx.x >> 6][1] = z.s;
+    red[threadIdx.x >> 6][2] = z.t;
+  }
+  __syncthreads();
+  float m = red[0][0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, red[i][0]);
+  Softmax all{m, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    Softmax w{red[i][0], red[i][1], red[i][2]};
+    rebase<ENTROPY>(w, m);
+    all.s += w.s;
+    all.t += w.t;
+  }
+  return all;
+}
+
+// What a row's numbers come to: its softmax, its target's logit (column:
+// there is one) and s = log(sum).
+template <bool ENTROPY>
+__device__ __forceinline__ void store_row(const LogpArgs& a, uint32_t r, const Softmax& all, double s, bool column,
+                                          float given) {
+  const bool none = all.s == 0.0f;  // nothing that can come
+  if (a.stats) {
+    a.stats[2ull * r] = none ? kNone : all.m;
+    a.stats[2ull * r + 1] = (float)s;
+  }
+  if (a.logp) a.logp[r] = !column ? __uint_as_float(0x7fc00000u) : none ? kNone : (float)((double)given - (double)all.m - s);
+  if (ENTROPY) a.entropy[r] = none ? 0.0f : (float)(s - (double)all.t / (double)all.s);
+}
+
+// A row that counts for nothing.
+template <bool ENTROPY, bool TOP>
+__device__ __forceinline__ void store_no_row(const LogpArgs& a, uint32_t r) {
+  if (threadIdx.x == 0) {
+    if (a.stats) a.stats[2ull * r] = a.stats[2ull * r + 1] = 0.0f;
+    if (a.logp) a.logp[r] = 0.0f;
+    if (ENTROPY) a.entropy[r] = 0.0f;
+  }
+  if (TOP && threadIdx.x < a.top) {
+    a.top_logp[(uint64_t)r * a.top + threadIdx.x] = kNone;
+    a.top_ids[(uint64_t)r * a.top + threadIdx.x] = -1;
+  }
+}
+
+// ---------------------------------------------------------------- the likeliest
+// A key orders logits, and columns of equal logits from the last to the
+// first; every column has another.  0 is none, and none is all ones.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // both zeros are one
+  return v != v ? 0xffffffffu : b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return k == 0xffffffffu ? __uint_as_float(0x7fc00000u) : __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+__device__ __forceinline__ uint64_t key_of(float v, uint32_t column) {
+  return ((uint64_t)ordered(v) << 32) | (0x7fffffffu - column);
+}
+
+// The k-th largest of a wave's words, the same in all lanes.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t k) {
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | (1u << bit);
+    if ((uint32_t)__popcll(__ballot(v >= c)) >= k) t = c;
+  }
+  return t;
+}
+__device__ __forceinline__ uint64_t kth_largest(uint64_t v, uint32_t k) {
+  const uint32_t high = kth_largest((uint32_t)(v >> 32), k), own = (uint32_t)(v >> 32);
+  uint32_t t = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t c = t | (1u << bit);
+    if ((uint32_t)__popcll(__ballot(own > high || (own == high && (uint32_t)v >= c))) >= k) t = c;
+  }
+  return ((uint64_t)high << 32) | t;
+}
+
+struct Top {
+  uint64_t candidate[kCandidates];
+  uint64_t best[GCLIP_LOGPROB_MAX_TOP];
+  uint64_t largest[kWaves];
+  uint32_t chosen[kLogpThreads];
+  uint32_t threshold[kWaves];
+  uint32_t n, chosen_n;
+};
+
+// best[] from the candidates, n of them at most kCandidates: a candidate's
+// place is the number of larger ones.
+__device__ __forceinline__ void rank_candidates(Top& w, uint32_t n, uint32_t k) {
+  for (uint32_t i = threadIdx.x; i < n; i += kLogpThreads) {
+    const uint64_t own = w.candidate[i];
+    uint32_t place = 0;
+    for (uint32_t j = 0; j < n; ++j) place += w.candidate[j] > own ? 1u : 0u;
+    if (place < k) w.best[place] = own;
+  }
+}
+
+// ---------------------------------------------------------------- reading a segment
+// Unit u of a row: where it passes the row's end its columns there are
+// -infinity.  Loads of units past the end stay inside the row.
+template <int DT, bool NT>
+__device__ __forceinline__ u32x4 logits_raw(uint64_t row, uint32_t u, uint32_t size) {
+  constexpr uint32_t kU = kUnit<DT>;
+  if (size < kU) return load_unit<DT, false>(row, 0, size);
+  const uint64_t c = (uint64_t)u * kU;
+  return load16<DT, NT>(row + (c + kU <= size ? c : size - kU) * kElem<DT>);
+}
+template <int DT>
+__device__ __forceinline__ void logits_settled(u32x4 q, uint32_t u, uint32_t size, float* v) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint64_t c = (uint64_t)u * kU;
+  if (size >= kU && c < size && c + kU > size) q = moved_down<DT>(q, kU - size % kU);
+  float t[kU];
+  unpack_unit<DT>(q, t);
+#pragma unroll
+  for (uint32_t j = 0; j < kU; ++j) v[j] = c + j < size ? t[j] : kNone;
+}
+
+// One pass over a segment of a row (all of it, with many rows), a unit of 16
+// bytes a lane, kChunk of them at a time with the next ones under way.  What a
+// lane has seen as its largest logit then chooses the few lanes that can hold
+// one of the likeliest, and those read theirs again, from the caches: the k-th
+// largest of any 64 lanes' largest is no more than the k-th largest of all.
+// Rows of so many equal logits that the candidates do not fit, and those with
+// NaNs or infinities, are searched k times instead.
+template <int DT, bool ENTROPY, bool TOP, bool STREAMED>
+__global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
+  constexpr uint32_t kU = kUnit<DT>;
+  __shared__ float red[kWaves][4];
+  [[maybe_unused]] __shared__ Top top;
+  const uint64_t wg = workgroup_of_grid();
+  const uint32_t r = (uint32_t)(wg / a.segments), seg = (uint32_t)(wg % a.segments);
+  if (r >= a.rows) return;
+  const uint32_t tid = threadIdx.x;
+  const int64_t target = a.targets ? a.targets[r] : 0;
+  if (a.targets && target == a.ignore) {
+    if (a.segments == 1) store_no_row<ENTROPY, TOP>(a, r);  // else the join does
+    return;
+  }
+  const uint64_t row = a.x.at + r * a.x.ld;
+  const uint32_t first = seg * (a.turns * kLogpThreads) + tid;  // unit
+  const bool column = a.logp && target >= 0 && target < (int64_t)a.size;
+  float given = 0.0f;
+  if (a.segments == 1 && column) given = elem_float<DT>(load_elem<DT>(row + (uint64_t)target * kElem<DT>));
+
+  Softmax z{kNone, 0.0f, 0.0f};
+  u32x4 next[kChunk];
+  const auto fetch = [&](uint32_t turn) {
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) next[k] = logits_raw<DT, STREAMED>(row, first + (turn + k) * kLogpThreads, a.size);
+  };
+  fetch(0);
+  for (uint32_t turn = 0; turn < a.turns; turn += kChunk) {
+    u32x4 q[kChunk];
+    float v[kChunk * kU];
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) q[k] = next[k];
+    if (turn + kChunk < a.turns) fetch(turn + kChunk);
+    // all of the workgroup's units of these turns lie in the row, and in the segment
+    const uint64_t end = ((uint64_t)seg * a.turns * kLogpThreads + (uint64_t)(turn + kChunk) * kLogpThreads) * kU;
+    if (end <= a.size && turn + kChunk <= a.turns) {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        float t[kU];
+        unpack_unit<DT>(q[k], t);
+#pragma unroll
+        for (uint32_t j = 0; j < kU; ++j) v[k * kU + j] = t[j];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kChunk; ++k) {
+        if (turn + k < a.turns) {
+          logits_settled<DT>(q[k], first + (turn + k) * kLogpThreads, a.size, v + k * kU);
+        } else {
+#pragma unroll
+          for (uint32_t j = 0; j < kU; ++j) v[k * kU + j] = kNone;
+        }
+      }
+    }
+    take<ENTROPY>(z, v);
+  }
+
+  const float own = z.m;
+  const Softmax all = joined<ENTROPY>(z, red);
+  const double sum_log = log((double)all.s);
+  if (a.segments == 1) {
+    if (tid == 0) store_row<ENTROPY>(a, r, all, sum_log, column, given);
+  } else if (tid == 0) {
+    float* p = a.parts + wg * 4;
+    p[0] = all.m;
+    p[1] = all.s;
+    p[2] = all.t;
+  }
+  if constexpr (TOP) {
+    const uint32_t mine = ordered(own);
+    const uint32_t kth = kth_largest(mine, a.top);
+    if ((tid & 63) == 0) top.threshold[tid >> 6] = kth;
+    if (tid == 0) top.n = top.chosen_n = 0;
+    if (tid < GCLIP_LOGPROB_MAX_TOP) top.best[tid] = 0;
+    __syncthreads();
+    uint32_t least = top.threshold[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) least = max(least, top.threshold[i]);
+    const bool regular = all.s == all.s;
+    uint32_t n = kCandidates + 1;
+    if (regular) {
+      if (mine >= least) top.chosen[atomicAdd(&top.chosen_n, 1u)] = tid;
+      __syncthreads();
+      const uint32_t items = top.chosen_n * a.turns;
+      bool room = true;
+      for (uint32_t i = tid; room && i < items; i += kLogpThreads) {
+        const uint32_t u = seg * (a.turns * kLogpThreads) + top.chosen[i / a.turns] + i % a.turns * kLogpThreads;
+        const uint64_t c = (uint64_t)u * kU;
+        if (c >= a.size) continue;
+        float v[kU];
+        logits_settled<DT>(logits_raw<DT, false>(row, u, a.size), u, a.size, v);
+#pragma unroll
+        for (uint32_t j = 0; j < kU; ++j) {
+          if (c + j < a.size && ordered(v[j]) >= least) {
+            const uint32_t at = atomicAdd(&top.n, 1u);
+            if (at < kCandidates) top.candidate[at] = key_of(v[j], (uint32_t)c + j);
+            else room = false;
+          }
+        }
+      }
+      __syncthreads();
+      n = top.n;
+      if (n <= kCandidates) rank_candidates(top, n, a.top);
+    }
+    if (n > kCandidates) {
+      uint64_t last = ~0ull;
+      for (uint32_t i = 0; i < a.top; ++i) {
+        uint64_t best = 0;
+        for (uint32_t turn = 0; turn < a.turns; ++turn) {
+          const uint32_t u = first + turn * kLogpThreads;
+          const uint64_t c = (uint64_t)u * kU;
+          if (c >= a.size) break;
+          float v[kU];
+          logits_settled<DT>(logits_raw<DT, false>(row, u, a.size), u, a.size, v);
+#pragma unroll
+          for (uint32_t j = 0; j < kU; ++j) {
+            const uint64_t key = key_of(v[j], (uint32_t)c + j);
+            if (c + j < a.size && key < last && key > best) best = key;
+          }
+        }
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) {
+          const uint64_t other = __shfl_xor((unsigned long long)best, off, 64);
+          if (other > best) best = other;
+        }
+        if ((tid & 63) == 0) top.largest[tid >> 6] = best;
+        __syncthreads();
+        best = top.largest[0];
+#pragma unroll
+        for (int k = 1; k < kWaves; ++k)
+          if (top.largest[k] > best) best = top.largest[k];
+        if (tid == 0) top.best[i] = best;
+        last = best;
+        __syncthreads();  // largest[] may still be read
+      }
+    }
+    __syncthreads();
+    if (tid < a.top) {
+      const uint64_t key = top.best[tid];
+      if (a.segments == 1) {
+        a.top_logp[(uint64_t)r * a.top + tid] = all.s == 0.0f ? kNone : (float)((double)unordered((uint32_t)(key >> 32)) - (double)all.m - sum_log);
+        a.top_ids[(uint64_t)r * a.top + tid] = (int64_t)(0x7fffffffu - (uint32_t)key);
+      } else {
+        a.keys[wg * a.top + tid] = key;
+      }
+    }
+  }
+}
+
+// The join of a row's segments: a lane of the first wave has one, its sums
+// and its largest keys in order.  No more than k segments' first keys reach
+// the k-th largest of them, so at most k k keys are left.
+template <int DT, bool ENTROPY, bool TOP>
+__global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
+  __shared__ float red[kWaves][4];
+  [[maybe_unused]] __shared__ Top top;
+  const uint64_t row_at = workgroup_of_grid();
+  if (row_at >= a.rows) return;
+  const uint32_t r = (uint32_t)row_at, tid = threadIdx.x;
+  const int64_t target = a.targets ? a.targets[r] : 0;
+  if (a.targets && target == a.ignore) {
+    store_no_row<ENTROPY, TOP>(a, r);
+    return;
+  }
+  const bool column = a.logp && target >= 0 && target < (int64_t)a.size;
+  float given = 0.0f;
+  if (column) given = elem_float<DT>(load_elem<DT>(a.x.at + r * a.x.ld + (uint64_t)target * kElem<DT>));
+  Softmax z{kNone, 0.0f, 0.0f};
+  if (tid < a.segments) {
+    const float* p = a.parts + (row_at * a.segments + tid) * 4;
+    z = Softmax{p[0], p[1], p[2]};
+  }
+  const uint64_t* keys = TOP ? a.keys + row_at * a.segments * a.top : nullptr;
+  uint64_t mine = 0;
+  if (TOP && tid < a.segments) mine = keys[(uint64_t)tid * a.top];
+  const Softmax all = joined<ENTROPY>(z, red);
+  const double sum_log = log((double)all.s);
+  if (tid == 0) store_row<ENTROPY>(a, r, all, sum_log, column, given);
+  if constexpr (TOP) {
+    if (tid == 0) top.n = 0;
+    if (tid < GCLIP_LOGPROB_MAX_TOP) top.best[tid] = 0;
+    if (tid < 64) {
+      const uint64_t kth = kth_largest(mine, a.top);
+      if (tid == 0) top.largest[0] = kth;
+    }
+    __syncthreads();
+    const uint64_t least = top.largest[0];
+    const uint32_t all_keys = a.segments * a.top;
+    for (uint32_t i = tid; i < all_keys; i += kLogpThreads) {
+      const uint64_t key = keys[i];
+      if (key != 0 && key >= least) top.candidate[atomicAdd(&top.n, 1u)] = key;
+    }
+    __syncthreads();
+    rank_candidates(top, top.n, a.top);
+    __syncthreads();
+    if (tid < a.top) {
+      const uint64_t key = top.best[tid];
+      a.top_logp[row_at * a.top + tid] = all.s == 0.0f ? kNone : (float)((double)unordered((uint32_t)(key >> 32)) - (double)all.m - sum_log);
+      a.top_ids[row_at * a.top + tid] = (int64_t)(0x7fffffffu - (uint32_t)key);
+    }
+  }
+}
+
+// dx = dlogp (1[t] - p) - dentropy p (log p + entropy), log p = x - m - s: kChunk
+// units a lane of a part of a row.
+template <int DT, bool ENTROPY, bool STREAMED>
+__global__ __launch_bounds__(kLogpThreads) void k_logp_grad(LogpArgs a, uint32_t parts) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint64_t wg = workgroup_of_grid();
+  const uint32_t r = (uint32_t)(wg / parts), part = (uint32_t)(wg % parts);
+  if (r >= a.rows) return;
+  const int64_t target = a.targets[r];
+  const float m = a.stats[2ull * r], s = a.stats[2ull * r + 1], dlogp = a.dlogp[r];
+  const float entropy = ENTROPY ? a.entropy[r] : 0.0f, dent = ENTROPY ? a.dentropy[r] : 0.0f;
+  const bool counts = target != a.ignore, valid = target >= 0 && target < (int64_t)a.size;
+  const uint64_t from = a.x.at + r * a.x.ld, to = a.dx.at + r * a.dx.ld;
+  const uint32_t first = part * (kChunk * kLogpThreads) + threadIdx.x;
+  if (!counts || !valid || m == kNone) {
+    const float fill = counts && m != kNone ? __uint_as_float(0x7fc00000u) : 0.0f;
+    float v[kU];
+#pragma unroll
+    for (uint32_t j = 0; j < kU; ++j) v[j] = fill;
+#pragma unroll
+    for (int k = 0; k < kChunk; ++k) {
+      const uint32_t u = first + k * kLogpThreads;
+      if ((uint64_t)u * kU < a.size) store_unit<DT, true>(to, u, a.size, pack_unit<DT>(v));
+    }
+    return;
+  }
+  u32x4 q[kChunk];
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) q[k] = logits_raw<DT, STREAMED>(from, first + k * kLogpThreads, a.size);
+#pragma unroll
+  for (int k = 0; k < kChunk; ++k) {
+    const uint32_t u = first + k * kLogpThreads;
+    const uint64_t c = (uint64_t)u * kU;
+    if (c >= a.size) break;
+    if (a.size >= kU && c + kU > a.size) q[k] = moved_down<DT>(q[k], kU - a.size % kU);
+    float v[kU];
+    unpack_unit<DT>(q[k], v);
+#pragma unroll
+    for (uint32_t j = 0; j < kU; ++j) {
+      const float d = v[j] - m - s, p = __builtin_amdgcn_exp2f(d * kLog2e);
+      const float f = ENTROPY ? __builtin_fmaf(dent, d + entropy, dlogp) : dlogp;
+      v[j] = p == 0.0f ? 0.0f : -p * f;
+    }
+    if ((uint64_t)target - c < kU) {
+#pragma unroll
+      for (uint32_t j = 0; j < kU; ++j)
+        if ((uint64_t)target - c == j) v[j] += dlogp;
+    }
+    store_unit<DT, true>(to, u, a.size, pack_unit<DT>(v));
+  }
+}
+
+template <int DT, bool ENTROPY, bool TOP>
+hipError_t forward_top(const LogpArgs& a, hipStream_t st) {
+  const dim3 grid = grid_of((uint64_t)a.rows * a.segments), block(kLogpThreads);
+  if (a.streamed) hipLaunchKernelGGL((k_logp<DT, ENTROPY, TOP, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_logp<DT, ENTROPY, TOP, false>), grid, block, 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.segments == 1) return e;
+  hipLaunchKernelGGL((k_logp_join<DT, ENTROPY, TOP>), grid_of(a.rows), block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t forward(const LogpArgs& a, hipStream_t st) {
+  if (a.top) return a.entropy ? forward_top<DT, true, true>(a, st) : forward_top<DT, false, true>(a, st);
+  return a.entropy ? forward_top<DT, true, false>(a, st) : forward_top<DT, false, false>(a, st);
+}
+
+template <int DT>
+hipError_t backward(const LogpArgs& a, hipStream_t st) {
+  const uint32_t units = (a.size - 1) / kUnit<DT> + 1, parts = (units - 1) / (kChunk * kLogpThreads) + 1;
+  const dim3 grid = grid_of((uint64_t)a.rows * parts), block(kLogpThreads);
+  if (a.dentropy) {
+    if (a.streamed) hipLaunchKernelGGL((k_logp_grad<DT, true, true>), grid, block, 0, st, a, parts);
+    else hipLaunchKernelGGL((k_logp_grad<DT, true, false>), grid, block, 0, st, a, parts);
+  } else {
+    if (a.streamed) hipLaunchKernelGGL((k_logp_grad<DT, false, true>), grid, block, 0, st, a, parts);
+    else hipLaunchKernelGGL((k_logp_grad<DT, false, false>), grid, block, 0, st, a, parts);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// With few rows, segments until there are two workgroups for each compute
+// unit, of at least a unit a thread.
+LogpCut logp_cut(uint32_t rows, uint32_t size, int32_t dtype) {
+  const uint32_t units = (size - 1) / (dtype == GCLIP_F32 ? 4u : 8u) + 1, most = (units - 1) / kLogpThreads + 1;
+  const uint32_t wanted = std::max(1u, std::min(kLogpSegments, 512u / std::max(rows, 1u)));
+  const uint32_t turns = (most - 1) / std::min(wanted, most) + 1;
+  return LogpCut{(most - 1) / turns + 1, turns};
+}
+
+hipError_t launch_logprob_forward(const LogpArgs& a, int32_t dtype, hipStream_t st) {
+  switch (dtype) {
+    case GCLIP_F32: return forward<GCLIP_F32>(a, st);
+    case GCLIP_F16: return forward<GCLIP_F16>(a, st);
+    default: return forward<GCLIP_BF16>(a, st);
+  }
+}
+
+hipError_t launch_logprob_backward(const LogpArgs& a, int32_t dtype, hipStream_t st) {
+  switch (dtype) {
+    case GCLIP_F32: return backward<GCLIP_F32>(a, st);
+    case GCLIP_F16: return backward<GCLIP_F16>(a, st);
+    default: return backward<GCLIP_BF16>(a, st);
+  }
+}
+
+}  // namespace gclip

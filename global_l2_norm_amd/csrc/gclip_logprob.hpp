@@ -1,0 +1,42 @@
+// gclip_logprob.hpp -- what the host side of the log probability calls hands
+// to their kernels (include/gclip_logprob.h; internal to libgclip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/gclip_logprob.h"
+#include "gclip_layer.hpp"
+
+namespace gclip {
+
+constexpr uint32_t kLogpThreads = 256;
+// Segments of a row, a workgroup each, where there are few rows: at most a
+// wave's lanes, which the join's first wave holds one each.
+constexpr uint32_t kLogpSegments = 64;
+
+struct LogpArgs {
+  Rows x, dx;
+  const int64_t* targets;
+  int64_t ignore;
+  float *stats, *logp, *entropy, *top_logp;
+  int64_t* top_ids;
+  const float *dlogp, *dentropy;
+  float* parts;    // [rows][segments][4]: largest, sum, weighted sum of a segment
+  uint64_t* keys;  // [rows][segments][top]
+  uint32_t rows, size, top;
+  uint32_t segments, turns;  // of a row; units of a thread in each
+  int32_t streamed;          // see kStreamBytes
+};
+
+// How the rows of a shape are cut.
+struct LogpCut {
+  uint32_t segments, turns;
+};
+LogpCut logp_cut(uint32_t rows, uint32_t size, int32_t dtype);
+
+hipError_t launch_logprob_forward(const LogpArgs& a, int32_t dtype, hipStream_t st);
+hipError_t launch_logprob_backward(const LogpArgs& a, int32_t dtype, hipStream_t st);
+
+}  // namespace gclip

@@ -1,0 +1,257 @@
+// gclip_rms_backward.hpp -- the gradients of the RMS norm and of its residual
+// step for rows that fit into registers, and the join of the weight's
+// gradient; instantiated for one storage format, without or with the normed
+// matrix in 8 bits, in each of gclip_rms_backward_*.hip.
+#pragma once
+
+#include "gclip_block_device.hpp"
+
+namespace gclip {
+
+template <int DT>
+__device__ __forceinline__ void store_rms_weight_grad(const RmsBwdArgs& a, uint32_t c, float t) {
+  if (DT == GCLIP_F32 || a.gdt == GCLIP_F32) {
+    const uint64_t p = a.dweight + c * 4ull;
+    if (a.accumulate) t += elem_float<GCLIP_F32>(load_elem<GCLIP_F32>(p));
+    store_elem<GCLIP_F32>(p, elem_bits<GCLIP_F32>(t));
+  } else {
+    const uint64_t p = a.dweight + c * 2ull;
+    if (a.accumulate) t += elem_float<DT>(load_elem<DT>(p));
+    store_elem<DT>(p, elem_bits<DT>(t));
+  }
+}
+
+// With n = x rstd and g = dy weight:
+//   dx = rstd (g - n sum(g n) / size),  dweight = sum over rows of dy n
+// in one pass: a row's dy and x are read once, into the registers of LANES
+// lanes, where the row's sum and then dx are taken from them; the columns'
+// sums stay in registers over all rows of the workgroup, whose rows meet in
+// shared memory at the end, and each workgroup -- one for each compute unit --
+// leaves one part of them.  While a row is worked on, the loads of the
+// workgroup's next one are under way.  x in 8 bits is half of a 16-bit
+// matrix's bytes, and four operations more for each four elements.
+template <int DT, int LANES, int NV, int SURE, bool RES, bool DROP, bool EIGHT, bool STREAMED>
+__global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_rms_rows_grad(RmsBwdArgs a, DropArgs d) {
+  constexpr uint32_t kBwdThreads = bwd_threads(NV * kUnit<DT>);
+  constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
+  constexpr uint32_t kCols = LANES * NV * kUnit<DT>;
+  constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
+  __shared__ float red[2][kBwdThreads / 64];
+  __shared__ float sums[kMeet > 1 ? kMeet * kCols : 1];
+  const uint32_t lane = threadIdx.x % LANES;
+  uint32_t slot = threadIdx.x / LANES;
+  if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
+  const uint32_t step = DROP ? drop_step(d) : 0u;
+
+  u32x4 ny[NV], nx[EIGHT ? 1 : NV], nh[RES ? NV : 1];
+  Unit8<DT> n8[EIGHT ? NV : 1];
+  float ns[EIGHT ? NV : 1];
+  float nrstd;
+  uint32_t base = blockIdx.x * kRows;
+  const uint32_t last8 = (a.size - 1) / kUnit<DT> * kUnit<DT>;
+  const auto fetch = [&](uint32_t first) {
+    // rows past the end are read as the last one; they count for nothing
+    const uint32_t r = min(first + slot, a.rows - 1);
+    const uint64_t dy = a.dy.at + r * a.dy.ld, x = a.x.at + r * a.x.ld, dh = a.dh.at + r * a.dh.ld;
+    nrstd = a.rstd[r];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      ny[k] = load_columns<DT, LANES, SURE, STREAMED>(dy, lane, k, a.size);
+      if constexpr (EIGHT) {
+        const uint32_t c = k < SURE ? column_of<DT>(lane, LANES, k) : min(column_of<DT>(lane, LANES, k), last8);
+        n8[k] = load_eight<DT, STREAMED>(a.x8.at + r * a.x8.ld, c);
+        ns[k] = load_scale(a.x8, r, c);
+      } else {
+        nx[k] = load_columns<DT, LANES, SURE, STREAMED>(x, lane, k, a.size);
+      }
+      if constexpr (RES)
+        nh[k] = a.dh.at ? load_columns<DT, LANES, SURE, STREAMED>(dh, lane, k, a.size) : u32x4{0u, 0u, 0u, 0u};
+    }
+  };
+  fetch(base);
+  float w[NV][kUnit<DT>], dw[NV][kUnit<DT>];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    weight_columns<DT, LANES, SURE>(a.weight, a.wdt, lane, k, a.size, 1.0f, w[k]);
+#pragma unroll
+    for (uint32_t j = 0; j < kUnit<DT>; ++j) dw[k][j] = 0.0f;
+  }
+  const float count = (float)a.size, inverse = 1.0f / count;
+  const bool full = a.size == kCols;
+  uint32_t turn = 0;
+
+  while (base < a.rows) {
+    const uint32_t r = base + slot;
+    const float rstd = nrstd;
+    float g[NV][kUnit<DT>], n[NV][kUnit<DT>];
+    u32x4 hh[RES ? NV : 1];
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      settle<DT, LANES, SURE>(ny[k], lane, k, a.size, full);
+      if constexpr (EIGHT) {
+        if (k >= SURE && !full) settle_eight<DT>(n8[k], column_of<DT>(lane, LANES, k), a.size);
+        unit_value<DT>(n8[k], ns[k], n[k]);
+      } else {
+        settle<DT, LANES, SURE>(nx[k], lane, k, a.size, full);
+        unpack_unit<DT>(nx[k], n[k]);
+      }
+      // nothing past the row's end or the last row enters the sums, where an
+      // infinite rstd or scale would make it a NaN
+      const float rk = r < a.rows && (k < SURE || column_of<DT>(lane, LANES, k) < a.size) ? rstd : 0.0f;
+      if (r >= a.rows) {
+        ny[k] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) n[k][j] = 0.0f;
+      }
+      unpack_unit<DT>(ny[k], g[k]);
+      if constexpr (RES) {
+        settle<DT, LANES, SURE>(nh[k], lane, k, a.size, full);
+        hh[k] = nh[k];
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+        n[k][j] *= rk;
+        dw[k][j] = __builtin_fmaf(g[k][j], n[k][j], dw[k][j]);
+        g[k][j] *= w[k][j];
+        s = __builtin_fmaf(g[k][j], n[k][j], s);
+      }
+    }
+    const uint32_t next = base + gridDim.x * kRows;
+    if (next < a.rows) fetch(next);
+    // the next row's sum uses the other words
+    const float c2 = rstd * divided(row_sum<LANES>(s, red[turn]), count, inverse);
+    turn ^= 1u;
+    if (r < a.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const uint32_t c = column_of<DT>(lane, LANES, k);
+        float v[kUnit<DT>];
+#pragma unroll
+        for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] = __builtin_fmaf(rstd, g[k][j], -(n[k][j] * c2));
+        if constexpr (RES) {
+          float q[kUnit<DT>];
+          unpack_unit<DT>(hh[k], q);
+#pragma unroll
+          for (uint32_t j = 0; j < kUnit<DT>; ++j) v[j] += q[j];
+        }
+        store_columns<DT, LANES, SURE, !STREAMED>(a.dres.at + r * a.dres.ld, lane, k, a.size, pack_unit<DT>(v));
+        if constexpr (DROP) {
+          drop_unit<DT>(d, step, r, c, v);
+          store_columns<DT, LANES, SURE, !STREAMED>(a.dx.at + r * a.dx.ld, lane, k, a.size, pack_unit<DT>(v));
+        }
+      }
+    }
+    base = next;
+  }
+
+  // this workgroup's part of the columns' sums
+  if (!a.dweight) return;
+  if constexpr (kMeet > 1) {
+    const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+        const float t = across_rows<LANES>(dw[k][j]);
+        if (LANES >= 64 || threadIdx.x % 64 < LANES) sums[row * kCols + column_of<DT>(lane, LANES, k) + j] = t;
+      }
+    }
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < a.size; c += kBwdThreads) {
+      float t = sums[c];
+#pragma unroll
+      for (uint32_t i = 1; i < kMeet; ++i) t += sums[i * kCols + c];
+      if (a.parts == 1) store_rms_weight_grad<DT>(a, c, t);
+      else a.partials[(uint64_t)blockIdx.x * a.size + c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+#pragma unroll
+      for (uint32_t j = 0; j < kUnit<DT>; ++j) {
+        const uint32_t c = column_of<DT>(lane, LANES, k) + j;
+        if (c < a.size) {
+          if (a.parts == 1) store_rms_weight_grad<DT>(a, c, dw[k][j]);
+          else a.partials[(uint64_t)blockIdx.x * a.size + c] = dw[k][j];
+        }
+      }
+    }
+  }
+}
+
+// The sum of the parts: a workgroup takes 64 columns, its sixteen waves share
+// the parts, in a fixed order, all loads of a wave under way at once.
+constexpr uint32_t kRmsJoinThreads = 1024;
+template <int DT>
+__global__ __launch_bounds__(kRmsJoinThreads) void k_rms_join(RmsBwdArgs a) {
+  constexpr uint32_t kWavesOf = kRmsJoinThreads / 64;
+  __shared__ float red[kWavesOf][64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint64_t i = workgroup_of_grid() * 64 + lane;
+  float t = 0.0f;
+  if (i < a.size) {
+#pragma unroll 16
+    for (uint32_t p = wave; p < a.parts; p += kWavesOf) t += a.partials[(uint64_t)p * a.size + i];
+  }
+  red[wave][lane] = t;
+  __syncthreads();
+  if (wave == 0 && i < a.size) {
+#pragma unroll
+    for (uint32_t k = 1; k < kWavesOf; ++k) t += red[k][lane];
+    store_rms_weight_grad<DT>(a, (uint32_t)i, t);
+  }
+}
+
+template <int DT>
+hipError_t rms_join_weight_grad(const RmsBwdArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((k_rms_join<DT>), grid_of(((uint64_t)a.size + 63) / 64), dim3(kRmsJoinThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool EIGHT, int LANES, int NV, int SURE, bool STREAMED>
+hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
+  a.parts = bwd_parts<DT>(a.rows, a.size);
+  const dim3 grid(a.parts), block(bwd_threads(NV * kUnit<DT>));
+  const DropArgs none{};
+  if (!residual)
+    hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, false, false, EIGHT, STREAMED>), grid, block, 0, st, a, none);
+  else if (!drop)
+    hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, true, false, EIGHT, STREAMED>), grid, block, 0, st, a, none);
+  else
+    hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, true, true, EIGHT, STREAMED>), grid, block, 0, st, a, *drop);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.parts == 1 || !a.dweight) return e;
+  return rms_join_weight_grad<DT>(a, st);
+}
+
+template <int DT, bool EIGHT, int I = 0>
+hipError_t rms_backward_of(int shape, const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kBwdShapes<DT>) / sizeof(RowShape))) {
+    if (shape != I) return rms_backward_of<DT, EIGHT, I + 1>(shape, a, residual, drop, st);
+  }
+  constexpr RowShape s = kBwdShapes<DT>[I];
+  constexpr int sure = sure_units(kBwdShapes<DT>, I);
+  return a.streamed ? rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, true>(a, residual, drop, st)
+                    : rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, false>(a, residual, drop, st);
+}
+
+template <int DT, bool EIGHT, int I = 0>
+hipError_t rms_backward_few(int shape, const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (I + 1 < (int)(sizeof(kFewBwdShapes) / sizeof(RowShape))) {
+    if (shape != I) return rms_backward_few<DT, EIGHT, I + 1>(shape, a, residual, drop, st);
+  }
+  constexpr RowShape s = kFewBwdShapes[I];
+  return rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure_units(kFewBwdShapes, I), false>(a, residual, drop, st);
+}
+
+template <int DT, bool EIGHT>
+hipError_t rms_backward_rows(const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
+  if constexpr (DT != GCLIP_F32) {
+    if (few_bwd<DT>(a.rows, a.size))
+      return rms_backward_few<DT, EIGHT>(row_shape_of(kFewBwdShapes, kUnit<DT>, a.size), a, residual, drop, st);
+  }
+  return rms_backward_of<DT, EIGHT>(row_shape_of(kBwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
+}
+
+}  // namespace gclip
