@@ -19,16 +19,19 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgclip.so")
 STAMPS_LIB = os.path.join(HERE, "_stamps", "libgclip.so")
-SOURCES = ["gclip_api.cpp", "gclip_plan.cpp", "gclip_trace.cpp", "gclip_kernels.hip", "gclip_tensor.hip",
-           "gclip_adamw.hip", "gclip_noalloc.hip", "gclip_ref.hip", "gclip_layer_api.cpp", "gclip_layer_any.hip",
-           "gclip_layer_forward_f32.hip", "gclip_layer_forward_f16.hip", "gclip_layer_forward_bf16.hip",
-           "gclip_layer_backward_f32.hip", "gclip_layer_backward_f16.hip", "gclip_layer_backward_bf16.hip",
-           "gclip_rms_forward8_f32.hip", "gclip_rms_forward8_f16.hip", "gclip_rms_forward8_bf16.hip",
-           "gclip_rms_forward_f32.hip", "gclip_rms_forward_f16.hip", "gclip_rms_forward_bf16.hip",
-           "gclip_rms_backward8_f32.hip", "gclip_rms_backward8_f16.hip", "gclip_rms_backward8_bf16.hip",
-           "gclip_rms_backward_f32.hip", "gclip_rms_backward_f16.hip", "gclip_rms_backward_bf16.hip",
-           "gclip_rms_any.hip", "gclip_activation_f32.hip", "gclip_activation_f16.hip", "gclip_activation_bf16.hip",
-           "gclip_pack8.hip", "gclip_block_api.cpp", "gclip_logprob.hip", "gclip_logprob_api.cpp"]
+# the longest compilations first; STAMPED name the macro of the diagnostic build
+STAMPED = ["gclip_kernels.hip"]
+SOURCES = STAMPED + [
+    "gclip_rms_forward8_f32.hip", "gclip_rms_forward8_f16.hip", "gclip_rms_forward8_bf16.hip",
+    "gclip_layer_forward_f32.hip", "gclip_layer_forward_f16.hip", "gclip_layer_forward_bf16.hip",
+    "gclip_layer_backward_f32.hip", "gclip_layer_backward_f16.hip", "gclip_layer_backward_bf16.hip",
+    "gclip_rms_forward_f32.hip", "gclip_rms_forward_f16.hip", "gclip_rms_forward_bf16.hip",
+    "gclip_rms_backward8_f32.hip", "gclip_rms_backward8_f16.hip", "gclip_rms_backward8_bf16.hip",
+    "gclip_rms_backward_f32.hip", "gclip_rms_backward_f16.hip", "gclip_rms_backward_bf16.hip", "gclip_logprob.hip",
+    "gclip_tensor.hip", "gclip_rms_any.hip", "gclip_layer_any.hip", "gclip_activation_f32.hip",
+    "gclip_activation_f16.hip", "gclip_activation_bf16.hip", "gclip_pack8.hip", "gclip_adamw.hip", "gclip_noalloc.hip",
+    "gclip_ref.hip", "gclip_api.cpp", "gclip_plan.cpp", "gclip_trace.cpp", "gclip_layer_api.cpp",
+    "gclip_block_api.cpp", "gclip_logprob_api.cpp"]
 ARCH = os.environ.get("GCLIP_OFFLOAD_ARCH", "gfx950")
 
 
@@ -52,25 +55,20 @@ def _jobs() -> int:
     return max(1, min(n if n > 0 else (os.cpu_count() or 1), 16))
 
 
-def build(verbose: bool = False, defines=(), lib_path: str = LIB) -> str:
-    """Always recompile the library (the sources in parallel); return its
-    path.  `defines` are extra -D flags (tuning sweeps); objects go to a
-    _build folder beside lib_path."""
-    odir = os.path.join(os.path.dirname(lib_path), "_build")
-    os.makedirs(odir, exist_ok=True)
-
-    def compile_one(src):
-        obj = os.path.join(odir, os.path.splitext(src)[0] + ".o")
+def _compile(jobs, verbose):
+    """Compile (source, object, defines) in parallel."""
+    def one(job):
+        src, obj, defines = job
+        os.makedirs(os.path.dirname(obj), exist_ok=True)
         cmd = [hipcc()] + compile_flags() + [f"-D{d}" for d in defines] + ["-x", "hip", "-c",
                                                                              os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         errs = "\n".join(l for l in (r.stderr or "").splitlines() if "packed-fp32-ops" not in l)
-        return src, obj, cmd, r.returncode, errs
+        return src, cmd, r.returncode, errs
 
-    with ThreadPoolExecutor(max_workers=min(_jobs(), len(SOURCES))) as pool:
-        results = list(pool.map(compile_one, SOURCES))
-    objs = []
-    for src, obj, cmd, rc, errs in results:
+    with ThreadPoolExecutor(max_workers=min(_jobs(), len(jobs))) as pool:
+        results = list(pool.map(one, jobs))
+    for src, cmd, rc, errs in results:
         if verbose:
             print(" ".join(cmd), flush=True)
         if rc != 0:
@@ -78,7 +76,9 @@ def build(verbose: bool = False, defines=(), lib_path: str = LIB) -> str:
             raise RuntimeError(f"hipcc failed on {src}")
         if verbose and errs.strip():
             sys.stderr.write(errs + "\n")
-        objs.append(obj)
+
+
+def _link(objs, lib_path, verbose):
     tmp = lib_path + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     if verbose:
@@ -88,8 +88,28 @@ def build(verbose: bool = False, defines=(), lib_path: str = LIB) -> str:
     return lib_path
 
 
+def _object(src, lib_path=LIB):
+    return os.path.join(os.path.dirname(lib_path), "_build", os.path.splitext(src)[0] + ".o")
+
+
+def build(verbose: bool = False, defines=(), lib_path: str = LIB, phase_stamps: bool = False) -> str:
+    """Always recompile the library (the sources in parallel); return its
+    path.  `defines` are extra -D flags (tuning sweeps); objects go to a
+    _build folder beside lib_path.  phase_stamps: the diagnostic build of
+    include/gclip_stamps.h too, which shares the objects of the sources that do
+    not name its macro."""
+    jobs = [(s, _object(s, lib_path), defines) for s in SOURCES]
+    if phase_stamps:
+        jobs = [(s, _object(s, STAMPS_LIB), ("GCLIP_PHASE_STAMPS",)) for s in STAMPED] + jobs
+    _compile(jobs, verbose)
+    _link([_object(s, lib_path) for s in SOURCES], lib_path, verbose)
+    if phase_stamps:
+        _link([_object(s, STAMPS_LIB if s in STAMPED else lib_path) for s in SOURCES], STAMPS_LIB, verbose)
+    return lib_path
+
+
 def build_phase_stamps(verbose: bool = False) -> str:
-    """The diagnostic build of include/gclip_stamps.h."""
+    """The diagnostic build of include/gclip_stamps.h alone."""
     return build(verbose=verbose, defines=("GCLIP_PHASE_STAMPS",), lib_path=STAMPS_LIB)
 
 
