@@ -79,7 +79,8 @@ def gclip_unpack(x, out, ldout, rows, size, dtype, stream):
 if torch is not None:
     from .layers import _CODES, _F32, _raw_stream
     _E4M3 = torch.float8_e4m3fn
-    _DTYPES = {code: dtype for dtype, code in _CODES.items()}
+    # a size in a tuple costs 0.7 us more than one in arguments
+    _empty, _empty_like, _contiguous = torch.empty, torch.empty_like, torch.contiguous_format
 _NONE8 = GclipPacked8()
 
 
@@ -117,17 +118,17 @@ class Packed8:
         self.args = GclipPacked8(values.data_ptr(), ld, scales.data_ptr(), mode, 0)
 
     @classmethod
-    def _new(cls, shape, device, mode):
-        """Memory for one; the device's allocator aligns it."""
+    def _new(cls, x, size, mode):
+        """Memory for x in 8 bits; the device's allocator aligns it."""
         self = cls.__new__(cls)
-        size = shape[-1]
+        lead = x.shape[:-1]
         ld = (size + 7) // 8 * 8
-        self.values = torch.empty((*shape[:-1], ld), dtype=_E4M3, device=device)
-        if ld != size:
-            self.values = self.values[..., :size]
-        count = 1 if mode else (size + GCLIP_SCALE_BLOCK - 1) // GCLIP_SCALE_BLOCK
-        self.scales = torch.empty((*shape[:-1], count), dtype=_F32, device=device)
-        self.args = GclipPacked8(self.values.data_ptr(), ld, self.scales.data_ptr(), mode, 0)
+        if ld == size:
+            self.values = values = _empty_like(x, dtype=_E4M3, memory_format=_contiguous)
+        else:
+            self.values = values = _empty(*lead, ld, dtype=_E4M3, device=x.device)[..., :size]
+        self.scales = scales = _empty(*lead, 1 if mode else (size + 127) // GCLIP_SCALE_BLOCK, dtype=_F32, device=x.device)
+        self.args = GclipPacked8(values.data_ptr(), ld, scales.data_ptr(), mode, 0)
         return self
 
     @property
@@ -204,7 +205,7 @@ def pack8(x, scales="block", *, stream=None):
     device, rows, size, ld, code = _matrix(x, "x")
     if size == 0:
         raise ValueError("x must have at least one column")
-    out = Packed8._new(x.shape, x.device, mode)
+    out = Packed8._new(x, size, mode)
     gclip_pack(x.data_ptr(), ld, out.args, rows, size, code, _raw_stream(device))
     return out
 
@@ -221,7 +222,7 @@ def _unpack8(packed, dtype, out):
     if not isinstance(packed, Packed8):
         raise TypeError(f"packed must be a Packed8, not {type(packed).__name__}")
     if out is None:
-        new = torch.empty(packed.shape, dtype=dtype or torch.bfloat16, device=packed.device)
+        new = _empty(*packed.shape, dtype=dtype or torch.bfloat16, device=packed.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out must have dtype {dtype}, not {out.dtype}")
     else:
@@ -268,21 +269,22 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
     if packed is not None:
         if y is not None:
             raise ValueError("out is for a y that is not packed")
-        y = Packed8._new(x.shape, x.device, _mode(packed))
+        y = Packed8._new(x, size, _mode(packed))
         y8 = y.args
     elif y is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+        y = _empty_like(x, memory_format=_contiguous)
         yp, ldy = y.data_ptr(), size
     else:
         ldy = _like(y, x, "out")
         yp = y.data_ptr()
     kept, k8 = None, _NONE8
     if keep:
-        kept = Packed8._new(x.shape, x.device, GCLIP_SCALES_BLOCK)
+        kept = Packed8._new(x, size, GCLIP_SCALES_BLOCK)
         k8 = kept.args
     rstd = rp = None
     if stats:
-        rstd = torch.empty(x.shape[:-1], dtype=_F32, device=x.device)
+        lead = x.shape[:-1]
+        rstd = _empty(*lead, dtype=_F32, device=x.device) if lead else _empty((), dtype=_F32, device=x.device)
         rp = rstd.data_ptr()
     if residual is None:
         gclip_rmsnorm_forward(GclipRmsForward(rows, size, code, wdt, eps, x.data_ptr(), ld, None, 0, wp, None, 0, yp,
@@ -290,7 +292,7 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
         return None, y, rstd, kept
     ldr = _like(residual, x, "residual")
     if h is None:
-        h = torch.empty_like(x, memory_format=torch.contiguous_format)
+        h = _empty_like(x, memory_format=_contiguous)
         ldh = size
     else:
         ldh = _like(h, x, "out_h")
@@ -353,11 +355,11 @@ def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weig
     if dh is not None:
         hp, lddh = dh.data_ptr(), _like(dh, dy, "dh")
     nbytes = gclip_rms_workspace(rows, size)
-    workspace = torch.empty(nbytes, dtype=torch.uint8, device=dy.device)
+    workspace = _empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
     wgp = None
     if want:
         if dweight is None:
-            dweight = torch.empty(size, dtype=gt, device=dy.device)
+            dweight = _empty(size, dtype=gt, device=dy.device)
         gt = dweight.dtype
         wgp = _vector(dweight, size, dy, "dweight")
     second = not residual or mask is not None  # dx apart from dresidual
@@ -369,20 +371,21 @@ def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weig
     lddx = ldds = 0
     if second:
         if dx is None:
-            dx = torch.empty_like(dy, memory_format=torch.contiguous_format)
+            dx = _empty_like(dy, memory_format=_contiguous)
             lddx = size
         else:
             lddx = _like(dx, dy, "out")
         dxp = dx.data_ptr()
     if residual:
         if dres is None:
-            dres = torch.empty_like(dy, memory_format=torch.contiguous_format)
+            dres = _empty_like(dy, memory_format=_contiguous)
             ldds = size
         else:
             ldds = _like(dres, dy, "out_residual")
         sp = dres.data_ptr()
     args = GclipRmsBackward(rows, size, code, wdt, _CODES[gt], 1 if accumulate else 0, dy.data_ptr(), lddy, hp, lddh, xp,
-                            ldx, x8, rp, wp, sp, ldds, dxp, lddx, wgp, workspace.data_ptr(), nbytes)
+                            ldx, x8, rp, wp, sp, ldds, dxp, lddx, wgp,
+                            workspace.data_ptr() if nbytes else None, nbytes)
     if residual:
         gclip_residual_rms_backward(args, _counted(mask, device) if mask is not None else None, _raw_stream(device))
     else:
@@ -414,15 +417,15 @@ def _activation_forward(gate, up, kind, keep, y):
     device, rows, size, ld, code = _matrix(gate, "gate")
     up_at, ldu = (up.data_ptr(), _like(up, gate, "up")) if up is not None else (None, 0)
     if y is None:
-        y = torch.empty_like(gate, memory_format=torch.contiguous_format)
+        y = _empty_like(gate, memory_format=_contiguous)
         ldy = size
     else:
         ldy = _like(y, gate, "out")
     gate8 = up8 = None
     if keep:
-        gate8 = Packed8._new(gate.shape, gate.device, GCLIP_SCALES_BLOCK)
+        gate8 = Packed8._new(gate, size, GCLIP_SCALES_BLOCK)
         if up is not None:
-            up8 = Packed8._new(gate.shape, gate.device, GCLIP_SCALES_BLOCK)
+            up8 = Packed8._new(gate, size, GCLIP_SCALES_BLOCK)
     if rows == 0 or size == 0:
         return y, gate8, up8
     gclip_activation_forward(GclipActivate(rows, size, code, kind, gate.data_ptr(), ld, up_at, ldu,
@@ -463,14 +466,14 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
             ldu = _like(up, dy, "up")
             up_at = up.data_ptr()
     if dgate is None:
-        dgate = torch.empty_like(dy, memory_format=torch.contiguous_format)
+        dgate = _empty_like(dy, memory_format=_contiguous)
         lddg = size
     else:
         lddg = _like(dgate, dy, "out_gate")
     dup_at, lddu = None, 0
     if up is not None:
         if dup is None:
-            dup = torch.empty_like(dy, memory_format=torch.contiguous_format)
+            dup = _empty_like(dy, memory_format=_contiguous)
             lddu = size
         else:
             lddu = _like(dup, dy, "out_up")
@@ -482,7 +485,7 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
         raise ValueError("out is for recompute")
     if recompute:
         if y is None:
-            y = torch.empty_like(dy, memory_format=torch.contiguous_format)
+            y = _empty_like(dy, memory_format=_contiguous)
             ldy = size
         else:
             ldy = _like(y, dy, "out")

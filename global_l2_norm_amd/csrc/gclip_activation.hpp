@@ -9,16 +9,30 @@ namespace gclip {
 constexpr int kActThreads = 256;
 
 // e^x: of the 16-bit formats by the hardware's power of two alone, whose
-// error (|x| 2^-24 of the result) is far below the format's step.
+// error (|x| 2^-24 of the result) is far below the format's step; in binary32
+// with what the product with log2(e) loses put back, within 3 u.
 template <int DT>
 __device__ __forceinline__ float exponential(float x) {
-  if constexpr (DT == GCLIP_F32) return expf(x);
-  else return __builtin_amdgcn_exp2f(x * 1.44269504088896f);
+  constexpr float kLog2e = 1.44269504088896f;
+  if constexpr (DT == GCLIP_F32) {
+    const float p = x * kLog2e;
+    const float lost = __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, kLog2e, -p));
+    // 0 and infinity are not corrected: an infinite p has lost everything
+    return __builtin_amdgcn_exp2f(p) * (fabsf(p) < 300.0f ? __builtin_fmaf(lost, 0.693147180559945f, 1.0f) : 1.0f);
+  } else {
+    return __builtin_amdgcn_exp2f(x * kLog2e);
+  }
 }
+// 1 / x of x >= 1; in binary32 with a step of Newton's, within 2 u (of an
+// infinite x too).
 template <int DT>
 __device__ __forceinline__ float reciprocal(float x) {
-  if constexpr (DT == GCLIP_F32) return 1.0f / x;
-  else return __builtin_amdgcn_rcpf(x);
+  const float r = __builtin_amdgcn_rcpf(x);
+  if constexpr (DT == GCLIP_F32) {
+    const float d = fminf(x, 0x1.fffffep+127f);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
+  }
+  return r;
 }
 
 // act(x) and, where wanted, its derivative.  With p = 1 / (1 + e^-x), 1 - p is
@@ -33,8 +47,23 @@ __device__ __forceinline__ float activated(float x, float& slope) {
     if (SLOPE) slope = p * __builtin_fmaf(x, x > 0.0f ? e * p : 1.0f - p, 1.0f);
     return x * p;
   } else if constexpr (KIND == GCLIP_ACT_GELU) {
-    const float c = 0.5f * erfcf(x * -0.707106781186547524f);
-    if (SLOPE) slope = __builtin_fmaf(x * 0.398942280401432678f, exponential<DT>(-0.5f * x * x), c);
+    // h = erfc(z) / 2 of z = |x| / sqrt(2) as e^(-z^2) t P(t), t = 1 / (1 + 0.3 z):
+    // P of degree 8 fitted to e^(z^2) erfc(z) / (2 t) for z up to 10, 2.0e-8 off
+    // at most, relative.  The power serves the derivative too.  The library's
+    // erfc took 1.5 times as long as the memory: 2047 x 1367 in binary32 8.9 us.
+    const float e = exponential<DT>(-0.5f * x * x), t = reciprocal<DT>(__builtin_fmaf(fabsf(x), 0.212132034355964f, 1.0f));
+    float h = -0.06476137042f;
+    h = __builtin_fmaf(h, t, 0.24278119206f);
+    h = __builtin_fmaf(h, t, -0.25613820553f);
+    h = __builtin_fmaf(h, t, 0.27385905385f);
+    h = __builtin_fmaf(h, t, -0.04732470214f);
+    h = __builtin_fmaf(h, t, 0.10746274889f);
+    h = __builtin_fmaf(h, t, 0.07416965812f);
+    h = __builtin_fmaf(h, t, 0.08535760641f);
+    h = __builtin_fmaf(h, t, 0.08459400386f);
+    h = e * t * h;
+    const float c = x > 0.0f ? 1.0f - h : h;
+    if (SLOPE) slope = __builtin_fmaf(x * 0.398942280401432678f, e, c);
     return x * c;
   } else {
     // (1 + tanh(u)) / 2 = 1 / (1 + e^-2u), u = sqrt(2 / pi) (x + 0.044715 x^3)

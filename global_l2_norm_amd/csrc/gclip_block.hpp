@@ -39,8 +39,13 @@ struct RmsBwdArgs {
   uint32_t rows, size;
   int32_t wdt, gdt, accumulate;
   uint32_t parts;
+  uint32_t row_groups;  // rows in registers: the workgroups that take rows
   int32_t streamed;
 };
+
+// Rows in registers, and no more than so many: the weight's gradient is taken
+// by workgroups of its own.
+constexpr uint32_t kStripRows = 128;
 
 struct ActArgs {
   Rows gate, up, y, dy, dgate, dup;  // up.at, y.at 0: none

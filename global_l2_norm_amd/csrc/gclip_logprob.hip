@@ -5,14 +5,14 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "gclip_layer_device.hpp"
+#include "gclip_block_device.hpp"
 #include "gclip_logprob.hpp"
 
 namespace gclip {
 namespace {
 
-constexpr int kWaves = kLogpThreads / 64;
 constexpr int kChunk = 4;  // units of a lane at a time
+constexpr uint32_t kGradUnits = 1024;  // rows of fewer units share workgroups backward
 constexpr uint32_t kCandidates = 1024;
 static_assert(GCLIP_LOGPROB_MAX_TOP * GCLIP_LOGPROB_MAX_TOP <= kCandidates, "the join's candidates");
 constexpr float kLog2e = 1.44269504088896f;
@@ -75,30 +75,26 @@ __device__ __forceinline__ float lanes_largest(float v) {
   return v;
 }
 
-// The workgroup's softmax from its threads', in all of them, in a fixed order.
-template <bool ENTROPY>
+// The softmax of the workgroup's WAVES waves from its threads', in all of
+// them, in a fixed order.
+template <int WAVES, bool ENTROPY>
 __device__ __forceinline__ Softmax joined(Softmax z, float (*red)[4]) {
-  rebase<ENTROPY>(z, lanes_largest<64>(z.m));
-  z.s = lanes_sum<64>(z.s);
-  if (ENTROPY) z.t = lanes_sum<64>(z.t);
-  if ((threadIdx.x & 63) == 0) {
-    red[threadIdx.x >> 6][0] = z.m;
-    red[threadIdx.x >> 6][1] = z.s;
-    red[threadIdx.x >> 6][2] = z.t;
-  }
-  __syncthreads();
-  float m = red[0][0];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, red[i][0]);
-  Softmax all{m, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    Softmax w{red[i][0], red[i][1], red[i][2]};
-    rebase<ENTROPY>(w, m);
-    all.s += w.s;
-    all.t += w.t;
+  for (int pass = 0; pass < 2; ++pass) {
+    rebase<ENTROPY>(z, lanes_largest<64>(z.m));
+    z.s = lanes_sum<64>(z.s);
+    if (ENTROPY) z.t = lanes_sum<64>(z.t);
+    if (pass == 1) break;
+    const uint32_t lane = threadIdx.x & 63;
+    if (lane == 0) {
+      red[threadIdx.x >> 6][0] = z.m;
+      red[threadIdx.x >> 6][1] = z.s;
+      red[threadIdx.x >> 6][2] = z.t;
+    }
+    __syncthreads();
+    z = lane < WAVES ? Softmax{red[lane][0], red[lane][1], red[lane][2]} : Softmax{kNone, 0.0f, 0.0f};
   }
-  return all;
+  return z;
 }
 
 // What a row's numbers come to: its softmax, its target's logit (column:
@@ -116,13 +112,15 @@ __device__ __forceinline__ void store_row(const LogpArgs& a, uint32_t r, const S
 }
 
 // A row that counts for nothing.
+template <bool ENTROPY>
+__device__ __forceinline__ void store_nothing(const LogpArgs& a, uint32_t r) {
+  if (a.stats) a.stats[2ull * r] = a.stats[2ull * r + 1] = 0.0f;
+  if (a.logp) a.logp[r] = 0.0f;
+  if (ENTROPY) a.entropy[r] = 0.0f;
+}
 template <bool ENTROPY, bool TOP>
 __device__ __forceinline__ void store_no_row(const LogpArgs& a, uint32_t r) {
-  if (threadIdx.x == 0) {
-    if (a.stats) a.stats[2ull * r] = a.stats[2ull * r + 1] = 0.0f;
-    if (a.logp) a.logp[r] = 0.0f;
-    if (ENTROPY) a.entropy[r] = 0.0f;
-  }
+  if (threadIdx.x == 0) store_nothing<ENTROPY>(a, r);
   if (TOP && threadIdx.x < a.top) {
     a.top_logp[(uint64_t)r * a.top + threadIdx.x] = kNone;
     a.top_ids[(uint64_t)r * a.top + threadIdx.x] = -1;
@@ -143,40 +141,55 @@ __device__ __forceinline__ uint64_t key_of(float v, uint32_t column) {
   return ((uint64_t)ordered(v) << 32) | (0x7fffffffu - column);
 }
 
-// The k-th largest of a wave's words, the same in all lanes.
+// The largest of a wave's words, in all lanes.
+__device__ __forceinline__ uint32_t lanes_most(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
+}
+
+// The k-th largest of a wave's words but for their lowest bits, the same in
+// all lanes: no more than the k-th largest.
+template <int IDLE = 0>
 __device__ __forceinline__ uint32_t kth_largest(uint32_t v, uint32_t k) {
   uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
+#pragma unroll 4
+  for (int bit = 31; bit >= IDLE; --bit) {
     const uint32_t c = t | (1u << bit);
     if ((uint32_t)__popcll(__ballot(v >= c)) >= k) t = c;
   }
   return t;
 }
-__device__ __forceinline__ uint64_t kth_largest(uint64_t v, uint32_t k) {
-  const uint32_t high = kth_largest((uint32_t)(v >> 32), k), own = (uint32_t)(v >> 32);
-  uint32_t t = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t c = t | (1u << bit);
-    if ((uint32_t)__popcll(__ballot(own > high || (own == high && (uint32_t)v >= c))) >= k) t = c;
-  }
-  return ((uint64_t)high << 32) | t;
-}
+// Lowest bits of a converted element that say nothing.
+template <int DT>
+constexpr int kIdleBits = DT == GCLIP_F32 ? 0 : DT == GCLIP_F16 ? 13 : 16;
 
+template <int THREADS>
 struct Top {
   uint64_t candidate[kCandidates];
   uint64_t best[GCLIP_LOGPROB_MAX_TOP];
-  uint64_t largest[kWaves];
-  uint32_t chosen[kLogpThreads];
-  uint32_t threshold[kWaves];
+  uint64_t largest[THREADS / 64];
+  union {
+    uint32_t chosen[THREADS];
+    uint64_t first[64];
+  };
+  uint32_t threshold[2][THREADS / 64];
   uint32_t n, chosen_n;
 };
 
 // best[] from the candidates, n of them at most kCandidates: a candidate's
 // place is the number of larger ones.
-__device__ __forceinline__ void rank_candidates(Top& w, uint32_t n, uint32_t k) {
-  for (uint32_t i = threadIdx.x; i < n; i += kLogpThreads) {
+template <int THREADS>
+__device__ __forceinline__ void rank_candidates(Top<THREADS>& w, uint32_t n, uint32_t k) {
+  for (uint32_t i = threadIdx.x; i < n; i += THREADS) {
     const uint64_t own = w.candidate[i];
     uint32_t place = 0;
+#pragma unroll 8
     for (uint32_t j = 0; j < n; ++j) place += w.candidate[j] > own ? 1u : 0u;
     if (place < k) w.best[place] = own;
   }
@@ -207,14 +220,15 @@ __device__ __forceinline__ void logits_settled(u32x4 q, uint32_t u, uint32_t siz
 // bytes a lane, kChunk of them at a time with the next ones under way.  What a
 // lane has seen as its largest logit then chooses the few lanes that can hold
 // one of the likeliest, and those read theirs again, from the caches: the k-th
-// largest of any 64 lanes' largest is no more than the k-th largest of all.
-// Rows of so many equal logits that the candidates do not fit, and those with
+// largest logit is at least the k-th largest of any wave's lanes' largest, and
+// at least what, in every wave, k / waves of those reach.  Rows of so many equal logits that the candidates do not fit, and those with
 // NaNs or infinities, are searched k times instead.
-template <int DT, bool ENTROPY, bool TOP, bool STREAMED>
-__global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
+template <int DT, int THREADS, bool ENTROPY, bool TOP, bool STREAMED>
+__global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
   constexpr uint32_t kU = kUnit<DT>;
+  constexpr int kWaves = THREADS / 64;
   __shared__ float red[kWaves][4];
-  [[maybe_unused]] __shared__ Top top;
+  [[maybe_unused]] __shared__ Top<THREADS> top;
   const uint64_t wg = workgroup_of_grid();
   const uint32_t r = (uint32_t)(wg / a.segments), seg = (uint32_t)(wg % a.segments);
   if (r >= a.rows) return;
@@ -225,7 +239,7 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
     return;
   }
   const uint64_t row = a.x.at + r * a.x.ld;
-  const uint32_t first = seg * (a.turns * kLogpThreads) + tid;  // unit
+  const uint32_t first = seg * (a.turns * (uint32_t)THREADS) + tid;  // unit
   const bool column = a.logp && target >= 0 && target < (int64_t)a.size;
   float given = 0.0f;
   if (a.segments == 1 && column) given = elem_float<DT>(load_elem<DT>(row + (uint64_t)target * kElem<DT>));
@@ -234,18 +248,18 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
   u32x4 next[kChunk];
   const auto fetch = [&](uint32_t turn) {
 #pragma unroll
-    for (int k = 0; k < kChunk; ++k) next[k] = logits_raw<DT, STREAMED>(row, first + (turn + k) * kLogpThreads, a.size);
+    for (int k = 0; k < kChunk; ++k) next[k] = logits_raw<DT, STREAMED>(row, first + (turn + k) * (uint32_t)THREADS, a.size);
   };
   fetch(0);
   for (uint32_t turn = 0; turn < a.turns; turn += kChunk) {
     u32x4 q[kChunk];
-    float v[kChunk * kU];
 #pragma unroll
     for (int k = 0; k < kChunk; ++k) q[k] = next[k];
     if (turn + kChunk < a.turns) fetch(turn + kChunk);
     // all of the workgroup's units of these turns lie in the row, and in the segment
-    const uint64_t end = ((uint64_t)seg * a.turns * kLogpThreads + (uint64_t)(turn + kChunk) * kLogpThreads) * kU;
+    const uint64_t end = ((uint64_t)seg * a.turns * (uint32_t)THREADS + (uint64_t)(turn + kChunk) * (uint32_t)THREADS) * kU;
     if (end <= a.size && turn + kChunk <= a.turns) {
+      float v[kChunk * kU];
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) {
         float t[kU];
@@ -253,24 +267,24 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
 #pragma unroll
         for (uint32_t j = 0; j < kU; ++j) v[k * kU + j] = t[j];
       }
+      take<ENTROPY>(z, v);
     } else {
 #pragma unroll
       for (int k = 0; k < kChunk; ++k) {
         if (turn + k < a.turns) {
-          logits_settled<DT>(q[k], first + (turn + k) * kLogpThreads, a.size, v + k * kU);
-        } else {
-#pragma unroll
-          for (uint32_t j = 0; j < kU; ++j) v[k * kU + j] = kNone;
+          float t[kU];
+          logits_settled<DT>(q[k], first + (turn + k) * (uint32_t)THREADS, a.size, t);
+          take<ENTROPY>(z, t);
         }
       }
     }
-    take<ENTROPY>(z, v);
   }
 
   const float own = z.m;
-  const Softmax all = joined<ENTROPY>(z, red);
-  const double sum_log = log((double)all.s);
+  const Softmax all = joined<kWaves, ENTROPY>(z, red);
+  double sum_log = 0.0;
   if (a.segments == 1) {
+    sum_log = log((double)all.s);
     if (tid == 0) store_row<ENTROPY>(a, r, all, sum_log, column, given);
   } else if (tid == 0) {
     float* p = a.parts + wg * 4;
@@ -280,23 +294,40 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
   }
   if constexpr (TOP) {
     const uint32_t mine = ordered(own);
-    const uint32_t kth = kth_largest(mine, a.top);
-    if ((tid & 63) == 0) top.threshold[tid >> 6] = kth;
+    const uint32_t share = (a.top + kWaves - 1) / kWaves;
+    const uint32_t kth = kth_largest<kIdleBits<DT>>(mine, a.top), part = kth_largest<kIdleBits<DT>>(mine, share);
+    if ((tid & 63) == 0) {
+      top.threshold[0][tid >> 6] = kth;
+      top.threshold[1][tid >> 6] = part;
+    }
     if (tid == 0) top.n = top.chosen_n = 0;
     if (tid < GCLIP_LOGPROB_MAX_TOP) top.best[tid] = 0;
     __syncthreads();
-    uint32_t least = top.threshold[0];
+    uint32_t least = top.threshold[0][0], every = top.threshold[1][0];
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) least = max(least, top.threshold[i]);
+    for (int i = 1; i < kWaves; ++i) {
+      least = max(least, top.threshold[0][i]);
+      every = min(every, top.threshold[1][i]);
+    }
+    least = max(least, every);
     const bool regular = all.s == all.s;
+    // where fewer than k lanes have anything that can come, all that can, and
+    // of what cannot the first columns, of which at most n can: enough of them
+    const bool scarce = least <= ordered(kNone);
+    if (scarce) least = ordered(kNone) + 1;
     uint32_t n = kCandidates + 1;
     if (regular) {
       if (mine >= least) top.chosen[atomicAdd(&top.chosen_n, 1u)] = tid;
       __syncthreads();
       const uint32_t items = top.chosen_n * a.turns;
       bool room = true;
-      for (uint32_t i = tid; room && i < items; i += kLogpThreads) {
-        const uint32_t u = seg * (a.turns * kLogpThreads) + top.chosen[i / a.turns] + i % a.turns * kLogpThreads;
+      const uint64_t begin = (uint64_t)seg * a.turns * (uint32_t)THREADS * kU + tid;
+      if (scarce && tid < a.top && begin < a.size) {
+        const float v = elem_float<DT>(load_elem<DT>(row + begin * kElem<DT>));
+        if (v == kNone) top.candidate[atomicAdd(&top.n, 1u)] = key_of(v, (uint32_t)begin);
+      }
+      for (uint32_t i = tid; room && i < items; i += (uint32_t)THREADS) {
+        const uint32_t u = seg * (a.turns * (uint32_t)THREADS) + top.chosen[i / a.turns] + i % a.turns * (uint32_t)THREADS;
         const uint64_t c = (uint64_t)u * kU;
         if (c >= a.size) continue;
         float v[kU];
@@ -319,7 +350,7 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
       for (uint32_t i = 0; i < a.top; ++i) {
         uint64_t best = 0;
         for (uint32_t turn = 0; turn < a.turns; ++turn) {
-          const uint32_t u = first + turn * kLogpThreads;
+          const uint32_t u = first + turn * (uint32_t)THREADS;
           const uint64_t c = (uint64_t)u * kU;
           if (c >= a.size) break;
           float v[kU];
@@ -359,13 +390,154 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp(LogpArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- short rows
+// A row lies in the registers of LANES lanes, NV units each, is read once, and
+// its largest and its sums are taken from there.  The likeliest: those logits
+// that reach the k-th largest of the lanes' largest, found and ordered within
+// the wave; rows with NaNs or infinities, and those whose candidates do not
+// fit, are searched k times.
+constexpr uint32_t kRowCandidates = 128;
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+//
+// The likeliest of rows of up to kScattered columns: a lane holds every 64th
+// column, so that every lane has some to choose from.
+constexpr uint32_t kScattered = 512;
+template <int DT, int LANES, int NV, bool ENTROPY, bool TOP, bool SCATTERED>
+__global__ __launch_bounds__(kLogpThreads) void k_logp_rows(LogpArgs a) {
+  constexpr uint32_t kU = kUnit<DT>;
+  static_assert(!SCATTERED || (LANES == 64 && NV * kU == kScattered / 64), "columns of a lane");
+  [[maybe_unused]] __shared__ uint64_t lists[kLogpThreads / 64][kRowCandidates];
+  const uint64_t at = workgroup_of_grid() * (kLogpThreads / LANES) + threadIdx.x / LANES;
+  if (LANES == 64 && at >= a.rows) return;
+  const uint32_t r = (uint32_t)(at < a.rows ? at : a.rows - 1), lane = threadIdx.x % LANES;
+  const int64_t target = a.targets ? a.targets[r] : 0;
+  const bool ignored = a.targets && target == a.ignore, column = a.logp && target >= 0 && target < (int64_t)a.size;
+  const uint64_t row = a.x.at + r * a.x.ld;
+  float given = 0.0f;
+  if (column && !ignored && lane == 0) given = elem_float<DT>(load_elem<DT>(row + (uint64_t)target * kElem<DT>));
+  u32x4 q[NV];
+  float v[NV * kU];
+  const auto column_at = [&](uint32_t j) { return SCATTERED ? lane + j * 64u : (lane + j / kU * LANES) * kU + j % kU; };
+  if constexpr (SCATTERED) {
+#pragma unroll
+    for (uint32_t j = 0; j < NV * kU; ++j)
+      v[j] = elem_float<DT>(load_elem<DT>(row + (uint64_t)min(column_at(j), a.size - 1) * kElem<DT>));
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) q[k] = logits_raw<DT, false>(row, lane + k * LANES, a.size);
+  }
+  if (LANES == 64 && ignored) {
+    if (lane == 0) store_nothing<ENTROPY>(a, r);
+    if (TOP && lane < a.top) {
+      a.top_logp[(uint64_t)r * a.top + lane] = kNone;
+      a.top_ids[(uint64_t)r * a.top + lane] = -1;
+    }
+    return;
+  }
+  float m = kNone;
+  if constexpr (SCATTERED) {
+#pragma unroll
+    for (uint32_t j = 0; j < NV * kU; ++j) v[j] = column_at(j) < a.size ? v[j] : kNone;
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) logits_settled<DT>(q[k], lane + k * LANES, a.size, v + k * kU);
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < NV * kU; ++j) m = fmaxf(m, v[j]);
+  const float own = m;
+  m = lanes_largest<LANES>(m);
+  const float ref = reference(m);
+  float s = 0.0f, t = 0.0f;
+#pragma unroll
+  for (uint32_t j = 0; j < NV * kU; ++j) {
+    const float d = v[j] - ref, e = __builtin_amdgcn_exp2f(d * kLog2e);
+    s += e;
+    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, -1e30f), t);
+  }
+  s = lanes_sum<LANES>(s);
+  if (ENTROPY) t = lanes_sum<LANES>(t);
+  const bool none = s == 0.0f;
+  const float sum_log = logf(s);
+  if (lane == 0 && at < a.rows) {
+    if (ignored) {
+      store_nothing<ENTROPY>(a, r);
+    } else {
+      if (a.stats) {
+        a.stats[2ull * r] = none ? kNone : m;
+        a.stats[2ull * r + 1] = sum_log;
+      }
+      if (a.logp) a.logp[r] = !column ? __uint_as_float(0x7fc00000u) : none ? kNone : given - ref - sum_log;
+      if (ENTROPY) a.entropy[r] = none ? 0.0f : sum_log - t / s;
+    }
+  }
+  if constexpr (TOP) {
+    static_assert(LANES == 64, "the likeliest are a wave's");
+    uint64_t* list = lists[threadIdx.x >> 6];
+    uint32_t least = kth_largest<kIdleBits<DT>>(ordered(own), a.top), n = 0;
+    const bool scarce = least <= ordered(kNone);  // as in k_logp
+    if (scarce) least = ordered(kNone) + 1;
+    const auto put = [&](bool mine, uint64_t key) {
+      const uint64_t who = __ballot(mine);
+      if (!who) return;
+      const uint32_t place = n + __builtin_amdgcn_mbcnt_hi((uint32_t)(who >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)who, 0u));
+      if (mine && place < kRowCandidates) list[place] = key;
+      n += (uint32_t)__popcll(who);
+    };
+    if (s == s) {
+      if (scarce) {
+        const bool first = lane < a.top;
+        const float x = first ? elem_float<DT>(load_elem<DT>(row + (uint64_t)lane * kElem<DT>)) : 0.0f;
+        put(first && x == kNone, key_of(x, lane));
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < NV * kU; ++j)
+        put(ordered(v[j]) >= least && column_at(j) < a.size, key_of(v[j], column_at(j)));
+    } else {
+      n = kRowCandidates + 1;
+    }
+    const auto store = [&](uint32_t place, uint64_t key) {
+      a.top_logp[(uint64_t)r * a.top + place] = none ? kNone : unordered((uint32_t)(key >> 32)) - ref - sum_log;
+      a.top_ids[(uint64_t)r * a.top + place] = (int64_t)(0x7fffffffu - (uint32_t)key);
+    };
+    if (n <= kRowCandidates) {
+      wave_sync();
+      for (uint32_t i = lane; i < n; i += 64) {
+        const uint64_t key = list[i];
+        uint32_t place = 0;
+#pragma unroll 8
+        for (uint32_t j = 0; j < n; ++j) place += list[j] > key ? 1u : 0u;
+        if (place < a.top) store(place, key);
+      }
+    } else {
+      uint64_t last = ~0ull;
+      for (uint32_t i = 0; i < a.top; ++i) {
+        uint64_t best = 0;
+#pragma unroll
+        for (uint32_t j = 0; j < NV * kU; ++j) {
+          const uint64_t key = column_at(j) < a.size ? key_of(v[j], column_at(j)) : 0;
+          if (key < last && key > best) best = key;
+        }
+        const uint32_t high = lanes_most((uint32_t)(best >> 32));
+        const uint32_t low = lanes_most((uint32_t)(best >> 32) == high ? (uint32_t)best : 0u);
+        last = ((uint64_t)high << 32) | low;
+        if (lane == 0) store(i, last);
+      }
+    }
+  }
+}
+
 // The join of a row's segments: a lane of the first wave has one, its sums
 // and its largest keys in order.  No more than k segments' first keys reach
 // the k-th largest of them, so at most k k keys are left.
 template <int DT, bool ENTROPY, bool TOP>
 __global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
+  constexpr int kWaves = kLogpThreads / 64;
   __shared__ float red[kWaves][4];
-  [[maybe_unused]] __shared__ Top top;
+  [[maybe_unused]] __shared__ Top<kLogpThreads> top;
   const uint64_t row_at = workgroup_of_grid();
   if (row_at >= a.rows) return;
   const uint32_t r = (uint32_t)row_at, tid = threadIdx.x;
@@ -382,26 +554,39 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
     const float* p = a.parts + (row_at * a.segments + tid) * 4;
     z = Softmax{p[0], p[1], p[2]};
   }
+  // every key is under way while the sums are joined
+  constexpr int kKeys = GCLIP_LOGPROB_MAX_TOP * kLogpSegments / kLogpThreads;
   const uint64_t* keys = TOP ? a.keys + row_at * a.segments * a.top : nullptr;
-  uint64_t mine = 0;
-  if (TOP && tid < a.segments) mine = keys[(uint64_t)tid * a.top];
-  const Softmax all = joined<ENTROPY>(z, red);
+  uint64_t own[TOP ? kKeys : 1], mine = 0;
+  if constexpr (TOP) {
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const uint32_t at = tid + i * kLogpThreads;
+      own[i] = at < a.segments * a.top ? keys[at] : 0;
+    }
+    if (tid < a.segments) mine = keys[(uint64_t)tid * a.top];
+  }
+  const Softmax all = joined<kWaves, ENTROPY>(z, red);
   const double sum_log = log((double)all.s);
   if (tid == 0) store_row<ENTROPY>(a, r, all, sum_log, column, given);
   if constexpr (TOP) {
     if (tid == 0) top.n = 0;
     if (tid < GCLIP_LOGPROB_MAX_TOP) top.best[tid] = 0;
-    if (tid < 64) {
-      const uint64_t kth = kth_largest(mine, a.top);
-      if (tid == 0) top.largest[0] = kth;
+    // the k-th largest of the first keys, 0 where there are fewer
+    if (tid < 64) top.first[tid] = mine;
+    if (tid == 0) top.largest[0] = 0;
+    __syncthreads();
+    if (tid < a.segments) {
+      uint32_t place = 0;
+#pragma unroll 16
+      for (uint32_t j = 0; j < kLogpSegments; ++j) place += top.first[j] > mine ? 1u : 0u;
+      if (place == a.top - 1) top.largest[0] = mine;
     }
     __syncthreads();
     const uint64_t least = top.largest[0];
-    const uint32_t all_keys = a.segments * a.top;
-    for (uint32_t i = tid; i < all_keys; i += kLogpThreads) {
-      const uint64_t key = keys[i];
-      if (key != 0 && key >= least) top.candidate[atomicAdd(&top.n, 1u)] = key;
-    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (own[i] != 0 && own[i] >= least) top.candidate[atomicAdd(&top.n, 1u)] = own[i];
     __syncthreads();
     rank_candidates(top, top.n, a.top);
     __syncthreads();
@@ -465,14 +650,74 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_grad(LogpArgs a, uint32_t
   }
 }
 
+// The same of short rows, a unit a lane over all of them.
+template <int DT, bool ENTROPY>
+__global__ __launch_bounds__(kLogpThreads) void k_logp_grad_rows(LogpArgs a, Split split) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint64_t i = workgroup_of_grid() * kLogpThreads + threadIdx.x;
+  const uint32_t r = row_of(i, split);
+  if (r >= a.rows) return;
+  const uint32_t u = (uint32_t)(i - r * split.of), c = u * kU;
+  const int64_t target = a.targets[r];
+  const float m = a.stats[2ull * r], s = a.stats[2ull * r + 1], dlogp = a.dlogp[r];
+  const float entropy = ENTROPY ? a.entropy[r] : 0.0f, dent = ENTROPY ? a.dentropy[r] : 0.0f;
+  const bool counts = target != a.ignore && m != kNone, valid = target >= 0 && target < (int64_t)a.size;
+  u32x4 q = logits_raw<DT, false>(a.x.at + r * a.x.ld, u, a.size);
+  if (a.size >= kU && c + kU > a.size) q = moved_down<DT>(q, kU - a.size % kU);
+  float v[kU];
+  unpack_unit<DT>(q, v);
+#pragma unroll
+  for (uint32_t j = 0; j < kU; ++j) {
+    const float d = v[j] - m - s, p = __builtin_amdgcn_exp2f(d * kLog2e);
+    const float f = ENTROPY ? __builtin_fmaf(dent, d + entropy, dlogp) : dlogp;
+    float g = p == 0.0f ? 0.0f : -p * f;
+    if ((uint64_t)target == (uint64_t)c + j) g += dlogp;
+    v[j] = !counts ? 0.0f : valid ? g : __uint_as_float(0x7fc00000u);
+  }
+  store_unit<DT, true>(a.dx.at + r * a.dx.ld, u, a.size, pack_unit<DT>(v));
+}
+
+template <int DT, bool ENTROPY, bool TOP, int LANES, int NV, bool SCATTERED = false>
+hipError_t forward_short(const LogpArgs& a, hipStream_t st) {
+  constexpr uint32_t kRows = kLogpThreads / LANES;
+  hipLaunchKernelGGL((k_logp_rows<DT, LANES, NV, ENTROPY, TOP, SCATTERED>), grid_of(((uint64_t)a.rows + kRows - 1) / kRows),
+                     dim3(kLogpThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+template <int DT, bool ENTROPY, bool TOP>
+hipError_t forward_short(const LogpArgs& a, hipStream_t st) {
+  const uint32_t units = (a.size - 1) / kUnit<DT> + 1;
+  if constexpr (!TOP) {
+    if (units <= 1) return forward_short<DT, ENTROPY, TOP, 1, 1>(a, st);
+    if (units <= 2) return forward_short<DT, ENTROPY, TOP, 2, 1>(a, st);
+    if (units <= 4) return forward_short<DT, ENTROPY, TOP, 4, 1>(a, st);
+    if (units <= 8) return forward_short<DT, ENTROPY, TOP, 8, 1>(a, st);
+    if (units <= 16) return forward_short<DT, ENTROPY, TOP, 16, 1>(a, st);
+    if (units <= 32) return forward_short<DT, ENTROPY, TOP, 32, 1>(a, st);
+  } else if (a.size <= kScattered) {
+    return forward_short<DT, ENTROPY, TOP, 64, kScattered / 64 / kUnit<DT>, true>(a, st);
+  }
+  if (units <= 64) return forward_short<DT, ENTROPY, TOP, 64, 1>(a, st);
+  if (units <= 128) return forward_short<DT, ENTROPY, TOP, 64, 2>(a, st);
+  if (DT != GCLIP_F32 || units <= 256) return forward_short<DT, ENTROPY, TOP, 64, 4>(a, st);
+  return forward_short<DT, ENTROPY, TOP, 64, DT == GCLIP_F32 ? 8 : 4>(a, st);
+}
+
 template <int DT, bool ENTROPY, bool TOP>
 hipError_t forward_top(const LogpArgs& a, hipStream_t st) {
-  const dim3 grid = grid_of((uint64_t)a.rows * a.segments), block(kLogpThreads);
-  if (a.streamed) hipLaunchKernelGGL((k_logp<DT, ENTROPY, TOP, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_logp<DT, ENTROPY, TOP, false>), grid, block, 0, st, a);
+  if (a.segments == 0) return forward_short<DT, ENTROPY, TOP>(a, st);
+  const dim3 grid = grid_of((uint64_t)a.rows * a.segments), block(a.threads);
+  if (a.threads == kLogpWide) hipLaunchKernelGGL((k_logp<DT, kLogpWide, ENTROPY, TOP, false>), grid, block, 0, st, a);
+  else if (a.threads == kLogpNarrow && a.streamed)
+    hipLaunchKernelGGL((k_logp<DT, kLogpNarrow, ENTROPY, TOP, true>), grid, block, 0, st, a);
+  else if (a.threads == kLogpNarrow)
+    hipLaunchKernelGGL((k_logp<DT, kLogpNarrow, ENTROPY, TOP, false>), grid, block, 0, st, a);
+  else if (a.streamed) hipLaunchKernelGGL((k_logp<DT, kLogpThreads, ENTROPY, TOP, true>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_logp<DT, kLogpThreads, ENTROPY, TOP, false>), grid, block, 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.segments == 1) return e;
-  hipLaunchKernelGGL((k_logp_join<DT, ENTROPY, TOP>), grid_of(a.rows), block, 0, st, a);
+  hipLaunchKernelGGL((k_logp_join<DT, ENTROPY, TOP>), grid_of(a.rows), dim3(kLogpThreads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -485,6 +730,13 @@ hipError_t forward(const LogpArgs& a, hipStream_t st) {
 template <int DT>
 hipError_t backward(const LogpArgs& a, hipStream_t st) {
   const uint32_t units = (a.size - 1) / kUnit<DT> + 1, parts = (units - 1) / (kChunk * kLogpThreads) + 1;
+  if (units < kGradUnits) {
+    const Split split{units, 1.0 / (double)units};
+    const dim3 grid = grid_of(((uint64_t)a.rows * units + kLogpThreads - 1) / kLogpThreads), block(kLogpThreads);
+    if (a.dentropy) hipLaunchKernelGGL((k_logp_grad_rows<DT, true>), grid, block, 0, st, a, split);
+    else hipLaunchKernelGGL((k_logp_grad_rows<DT, false>), grid, block, 0, st, a, split);
+    return hipGetLastError();
+  }
   const dim3 grid = grid_of((uint64_t)a.rows * parts), block(kLogpThreads);
   if (a.dentropy) {
     if (a.streamed) hipLaunchKernelGGL((k_logp_grad<DT, true, true>), grid, block, 0, st, a, parts);
@@ -498,13 +750,16 @@ hipError_t backward(const LogpArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// With few rows, segments until there are two workgroups for each compute
-// unit, of at least a unit a thread.
 LogpCut logp_cut(uint32_t rows, uint32_t size, int32_t dtype) {
+  if (size <= kShortRow) return LogpCut{0, 0, 0};
   const uint32_t units = (size - 1) / (dtype == GCLIP_F32 ? 4u : 8u) + 1, most = (units - 1) / kLogpThreads + 1;
-  const uint32_t wanted = std::max(1u, std::min(kLogpSegments, 512u / std::max(rows, 1u)));
-  const uint32_t turns = (most - 1) / std::min(wanted, most) + 1;
-  return LogpCut{(most - 1) / turns + 1, turns};
+  if (rows >= kLogpManyRows && units <= kLogpNarrow * kLogpNarrowTurns)
+    return LogpCut{1, (units - 1) / kLogpNarrow + 1, kLogpNarrow};
+  if (rows > kLogpFewRows) return LogpCut{1, most, kLogpThreads};
+  if (units <= kLogpWide * kLogpTurns) return LogpCut{1, (units - 1) / kLogpWide + 1, kLogpWide};
+  const uint32_t wanted = std::min(kLogpSegments, 4 * kLogpFewRows / std::max(rows, 1u));
+  const uint32_t turns = (most - 1) / wanted + 1;
+  return LogpCut{(most - 1) / turns + 1, turns, kLogpThreads};
 }
 
 hipError_t launch_logprob_forward(const LogpArgs& a, int32_t dtype, hipStream_t st) {

@@ -11,10 +11,13 @@
 
 namespace gclip {
 
-constexpr uint32_t kLogpThreads = 256;
-// Segments of a row, a workgroup each, where there are few rows: at most a
-// wave's lanes, which the join's first wave holds one each.
-constexpr uint32_t kLogpSegments = 64;
+constexpr uint32_t kLogpThreads = 256, kLogpNarrow = 64;
+// Many rows: a wave each, while its lanes take few enough units.
+constexpr uint32_t kLogpManyRows = 1536, kLogpNarrowTurns = 64;
+// Few rows: workgroups of more threads, one a row, which take up to kLogpTurns
+// units each; longer rows in segments, a workgroup each: at most a wave's
+// lanes, which the join's first wave holds one each.
+constexpr uint32_t kLogpFewRows = 256, kLogpWide = 1024, kLogpTurns = 8, kLogpSegments = 64;
 
 struct LogpArgs {
   Rows x, dx;
@@ -27,12 +30,16 @@ struct LogpArgs {
   uint64_t* keys;  // [rows][segments][top]
   uint32_t rows, size, top;
   uint32_t segments, turns;  // of a row; units of a thread in each
+  uint32_t threads;          // of a workgroup
   int32_t streamed;          // see kStreamBytes
 };
 
-// How the rows of a shape are cut.
+// Rows of up to so many columns lie in a wave's registers.
+constexpr uint32_t kShortRow = 2048;
+
+// How the rows of a shape are cut; no segments: short rows.
 struct LogpCut {
-  uint32_t segments, turns;
+  uint32_t segments, turns, threads;
 };
 LogpCut logp_cut(uint32_t rows, uint32_t size, int32_t dtype);
 

@@ -64,6 +64,7 @@ gclip_status gclip_logprob_forward(const gclip_logprobs* a, void* stream) {
   k.top = (uint32_t)a->top;
   k.segments = cut.segments;
   k.turns = cut.turns;
+  k.threads = cut.threads;
   k.streamed = streams(a->rows, a->size, format_bytes(a->dtype));
   return launched(launch_logprob_forward(k, a->dtype, static_cast<hipStream_t>(stream)));
 }

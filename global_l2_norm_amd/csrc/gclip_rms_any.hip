@@ -179,42 +179,100 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_row_means(RmsBwdArgs a) {
   }
 }
 
-// A workgroup takes a strip of 64 groups of columns and part blockIdx.z of the
-// rows, its waves in turn.
-template <int DT, bool RES, bool DROP>
+// Unit u's place in a row: a unit that passes the row's end is read as its last
+// 16 bytes, and settled afterwards.
+template <int DT>
+__device__ __forceinline__ u32x4 load_clamped(uint64_t row, uint32_t c, uint32_t size) {
+  return load16<DT, false>(row + (uint64_t)min(c, size - kUnit<DT>) * kElem<DT>);
+}
+template <int DT>
+__device__ __forceinline__ void settle_unit(u32x4& q, uint32_t c, uint32_t size) {
+  if (c + kUnit<DT> > size) q = c < size ? moved_down<DT>(q, kUnit<DT> - size % kUnit<DT>) : u32x4{0u, 0u, 0u, 0u};
+}
+
+// A workgroup takes a strip of 64 units of columns and part blockIdx.z of the
+// rows, its waves in turn; a row's loads are under way while the one before is
+// worked on.
+template <int DT, bool RES, bool DROP, bool EIGHT>
 __global__ __launch_bounds__(kLongThreads) void k_rms_grad_long(RmsBwdArgs a, DropArgs d) {
-  __shared__ float red[kLongWaves][64 * kGroup + 1];
+  constexpr uint32_t kU = kUnit<DT>;
+  __shared__ float red[kLongWaves][64 * kU + 1];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint64_t strip = workgroup_of_grid() * (64 * kGroup);
+  const uint64_t strip = workgroup_of_grid() * (64 * kU);
   if (strip >= a.size) return;
-  const uint32_t g = (uint32_t)(strip / kGroup) + lane;
+  const uint32_t c = (uint32_t)strip + lane * kU, c8 = min(c, (a.size - 1) / kU * kU);
   const uint32_t step = DROP ? drop_step(d) : 0u;
-  float w[8], dw[8] = {};
-  weight_group<DT>(a.weight, a.wdt, g, a.size, 1.0f, w);
-  for (uint32_t r = blockIdx.z * kLongWaves + wave; r < a.rows; r += gridDim.z * kLongWaves) {
-    float y[8], n[8], h[8] = {};
-    unpack<DT>(load_group8<DT, false>(a.dy.at + r * a.dy.ld, g, a.size), y);
-    normed_input<DT>(a, r, g, n);
-    if (RES && a.dh.at) unpack<DT>(load_group8<DT, false>(a.dh.at + r * a.dh.ld, g, a.size), h);
-    const float rstd = a.rstd[r], c2 = a.sums[r];
+  const uint32_t stride = gridDim.z * kLongWaves;
+  float w[kU], dw[kU] = {};
+  if (a.weight == 0) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      n[k] *= rstd;
-      dw[k] = __builtin_fmaf(y[k], n[k], dw[k]);
-      n[k] = rstd * (y[k] * w[k] - n[k] * c2);
-      if constexpr (RES) n[k] += h[k];
+    for (uint32_t j = 0; j < kU; ++j) w[j] = 1.0f;
+  } else if (DT != GCLIP_F32 && a.wdt == GCLIP_F32) {
+    float t[8];
+    weight_group<DT>(a.weight, a.wdt, c / kGroup, a.size, 1.0f, t);
+#pragma unroll
+    for (uint32_t j = 0; j < kU; ++j) w[j] = t[j];
+  } else {
+    u32x4 q = load_clamped<DT>(a.weight, c, a.size);
+    settle_unit<DT>(q, c, a.size);
+    unpack_unit<DT>(q, w);
+  }
+  u32x4 ny, nx{0u, 0u, 0u, 0u}, nh{0u, 0u, 0u, 0u};
+  Unit8<DT> n8{};
+  float ns = 0.0f, nrstd = 0.0f, nc2 = 0.0f;
+  const auto fetch = [&](uint32_t r) {
+    ny = load_clamped<DT>(a.dy.at + r * a.dy.ld, c, a.size);
+    if constexpr (EIGHT) {
+      n8 = load_eight<DT, false>(a.x8.at + r * a.x8.ld, c8);
+      ns = load_scale(a.x8, r, c8);
+    } else {
+      nx = load_clamped<DT>(a.x.at + r * a.x.ld, c, a.size);
     }
-    store_group8<DT, true>(a.dres.at + r * a.dres.ld, g, a.size, pack<DT>(n));
-    if constexpr (DROP) {
-      drop_group(d, step, r, g, n);
-      store_group8<DT, true>(a.dx.at + r * a.dx.ld, g, a.size, pack<DT>(n));
+    if (RES && a.dh.at) nh = load_clamped<DT>(a.dh.at + r * a.dh.ld, c, a.size);
+    nrstd = a.rstd[r];
+    nc2 = a.sums[r];
+  };
+  uint32_t r = blockIdx.z * kLongWaves + wave;
+  if (r < a.rows) fetch(r);
+  while (r < a.rows) {
+    float y[kU], n[kU], h[kU];
+    const float rstd = nrstd, c2 = nc2;
+    settle_unit<DT>(ny, c, a.size);
+    unpack_unit<DT>(ny, y);
+    if constexpr (EIGHT) {
+      settle_eight<DT>(n8, c, a.size);
+      unit_value<DT>(n8, ns, n);
+    } else {
+      settle_unit<DT>(nx, c, a.size);
+      unpack_unit<DT>(nx, n);
     }
+    if constexpr (RES) {
+      settle_unit<DT>(nh, c, a.size);
+      unpack_unit<DT>(nh, h);
+    }
+    const uint32_t next = r + stride;
+    if (next < a.rows) fetch(next);
+#pragma unroll
+    for (uint32_t j = 0; j < kU; ++j) {
+      n[j] *= rstd;
+      dw[j] = __builtin_fmaf(y[j], n[j], dw[j]);
+      n[j] = rstd * (y[j] * w[j] - n[j] * c2);
+      if constexpr (RES) n[j] += h[j];
+    }
+    if (c < a.size) {
+      store_unit<DT, true>(a.dres.at + r * a.dres.ld, c / kU, a.size, pack_unit<DT>(n));
+      if constexpr (DROP) {
+        drop_unit<DT>(d, step, r, c, n);
+        store_unit<DT, true>(a.dx.at + r * a.dx.ld, c / kU, a.size, pack_unit<DT>(n));
+      }
+    }
+    r = next;
   }
   if (!a.dweight) return;
 #pragma unroll
-  for (uint32_t j = 0; j < 8; ++j) red[wave][lane * kGroup + j] = dw[j];
+  for (uint32_t j = 0; j < kU; ++j) red[wave][lane * kU + j] = dw[j];
   __syncthreads();
-  for (uint32_t i = threadIdx.x; i < 64 * kGroup; i += kLongThreads) {
+  for (uint32_t i = threadIdx.x; i < 64 * kU; i += kLongThreads) {
     const uint64_t col = strip + i;
     float t = red[0][i];
 #pragma unroll
@@ -346,6 +404,13 @@ hipError_t forward_any(const RmsFwdArgs& a, bool residual, const DropArgs* drop,
   return hipGetLastError();
 }
 
+template <int DT, bool EIGHT>
+void launch_long(const RmsBwdArgs& a, bool residual, const DropArgs* drop, dim3 strips, dim3 block, hipStream_t st) {
+  if (!residual) hipLaunchKernelGGL((k_rms_grad_long<DT, false, false, EIGHT>), strips, block, 0, st, a, DropArgs{});
+  else if (!drop) hipLaunchKernelGGL((k_rms_grad_long<DT, true, false, EIGHT>), strips, block, 0, st, a, DropArgs{});
+  else hipLaunchKernelGGL((k_rms_grad_long<DT, true, true, EIGHT>), strips, block, 0, st, a, *drop);
+}
+
 template <int DT>
 hipError_t backward_any(const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
   if (a.rows > 0 && a.size < kRegistersMin) {
@@ -354,13 +419,12 @@ hipError_t backward_any(const RmsBwdArgs& a, bool residual, const DropArgs* drop
     else if (!drop) hipLaunchKernelGGL((k_rms_grad_short<DT, true, false>), grid, block, 0, st, a, DropArgs{});
     else hipLaunchKernelGGL((k_rms_grad_short<DT, true, true>), grid, block, 0, st, a, *drop);
   } else if (a.rows > 0) {
-    const dim3 block(kLongThreads), strips = grid_of((a.size - 1) / (64 * kGroup) + 1, a.parts);
+    const dim3 block(kLongThreads), strips = grid_of((a.size - 1) / (64 * kUnit<DT>) + 1, a.parts);
     hipLaunchKernelGGL((k_rms_row_means<DT>), dim3(std::min<uint32_t>(a.rows, 1u << 20)), block, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (!residual) hipLaunchKernelGGL((k_rms_grad_long<DT, false, false>), strips, block, 0, st, a, DropArgs{});
-    else if (!drop) hipLaunchKernelGGL((k_rms_grad_long<DT, true, false>), strips, block, 0, st, a, DropArgs{});
-    else hipLaunchKernelGGL((k_rms_grad_long<DT, true, true>), strips, block, 0, st, a, *drop);
+    if (a.x8.at) launch_long<DT, true>(a, residual, drop, strips, block, st);
+    else launch_long<DT, false>(a, residual, drop, strips, block, st);
   }
   const hipError_t e = hipGetLastError();
   return e != hipSuccess || !a.dweight ? e : rms_join_weight_grad<DT>(a, st);

@@ -21,6 +21,61 @@ __device__ __forceinline__ void store_rms_weight_grad(const RmsBwdArgs& a, uint3
   }
 }
 
+// The weight's gradient of few rows: it takes neither the rows' sums nor their
+// results, so workgroups of their own, in the same launch, take a strip of 64
+// units of columns each down all rows, from the caches, and no parts are left
+// to join.
+template <int DT, bool EIGHT, uint32_t WAVES>
+__device__ __forceinline__ void strip_weight_grad(const RmsBwdArgs& a, uint32_t strip, float* meet) {
+  constexpr uint32_t kU = kUnit<DT>;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t unit = strip * 64 + lane, c = unit * kU, c8 = min(c, (a.size - 1) / kU * kU);
+  constexpr int kAtOnce = 4;  // rows of a wave under way
+  float dw[kU] = {};
+  for (uint32_t first = wave; first < a.rows; first += kAtOnce * WAVES) {
+    u32x4 ny[kAtOnce], nx[kAtOnce];
+    Unit8<DT> n8[kAtOnce];
+    float ns[kAtOnce], rstd[kAtOnce];
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      const uint32_t r = min(first + i * WAVES, a.rows - 1);
+      ny[i] = load_columns<DT, 1, 0, false>(a.dy.at + r * a.dy.ld, unit, 0, a.size);
+      if constexpr (EIGHT) {
+        n8[i] = load_eight<DT, false>(a.x8.at + r * a.x8.ld, c8);
+        ns[i] = load_scale(a.x8, r, c8);
+      } else {
+        nx[i] = load_columns<DT, 1, 0, false>(a.x.at + r * a.x.ld, unit, 0, a.size);
+      }
+      rstd[i] = a.rstd[r];
+    }
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i) {
+      if (first + i * WAVES >= a.rows) break;
+      float y[kU], n[kU];
+      settle<DT, 1, 0>(ny[i], unit, 0, a.size);
+      unpack_unit<DT>(ny[i], y);
+      if constexpr (EIGHT) {
+        unit_value<DT>(n8[i], ns[i], n);  // past the row's end y is 0, and nothing is stored
+      } else {
+        settle<DT, 1, 0>(nx[i], unit, 0, a.size);
+        unpack_unit<DT>(nx[i], n);
+      }
+#pragma unroll
+      for (uint32_t j = 0; j < kU; ++j) dw[j] = __builtin_fmaf(y[j], n[j] * rstd[i], dw[j]);
+    }
+  }
+#pragma unroll
+  for (uint32_t j = 0; j < kU; ++j) meet[wave * (64 * kU) + lane * kU + j] = dw[j];
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < 64 * kU; i += WAVES * 64) {
+    float t = meet[i];
+#pragma unroll
+    for (uint32_t k = 1; k < WAVES; ++k) t += meet[k * (64 * kU) + i];
+    const uint32_t column = strip * 64 * kU + i;
+    if (column < a.size) store_rms_weight_grad<DT>(a, column, t);
+  }
+}
+
 // With n = x rstd and g = dy weight:
 //   dx = rstd (g - n sum(g n) / size),  dweight = sum over rows of dy n
 // in one pass: a row's dy and x are read once, into the registers of LANES
@@ -37,7 +92,13 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_rms_rows_grad(R
   constexpr uint32_t kCols = LANES * NV * kUnit<DT>;
   constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
   __shared__ float red[2][kBwdThreads / 64];
-  __shared__ float sums[kMeet > 1 ? kMeet * kCols : 1];
+  constexpr uint32_t kStripFloats = kBwdThreads / 64 * 64 * kUnit<DT>;  // see strip_weight_grad()
+  constexpr uint32_t kSums = kMeet > 1 ? kMeet * kCols : 1;
+  __shared__ float sums[kSums > kStripFloats ? kSums : kStripFloats];
+  if (blockIdx.x >= a.row_groups) {
+    strip_weight_grad<DT, EIGHT, kBwdThreads / 64>(a, blockIdx.x - a.row_groups, sums);
+    return;
+  }
   const uint32_t lane = threadIdx.x % LANES;
   uint32_t slot = threadIdx.x / LANES;
   if constexpr (LANES >= 64) slot = __builtin_amdgcn_readfirstlane(slot);
@@ -117,7 +178,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_rms_rows_grad(R
         s = __builtin_fmaf(g[k][j], n[k][j], s);
       }
     }
-    const uint32_t next = base + gridDim.x * kRows;
+    const uint32_t next = base + a.row_groups * kRows;
     if (next < a.rows) fetch(next);
     // the next row's sum uses the other words
     const float c2 = rstd * divided(row_sum<LANES>(s, red[turn]), count, inverse);
@@ -146,7 +207,7 @@ __global__ __launch_bounds__(bwd_threads(NV * kUnit<DT>)) void k_rms_rows_grad(R
   }
 
   // this workgroup's part of the columns' sums
-  if (!a.dweight) return;
+  if (!a.dweight || a.row_groups < gridDim.x) return;
   if constexpr (kMeet > 1) {
     const uint32_t row = LANES < 64 ? threadIdx.x / 64 : slot;
 #pragma unroll
@@ -211,8 +272,9 @@ hipError_t rms_join_weight_grad(const RmsBwdArgs& a, hipStream_t st) {
 
 template <int DT, bool EIGHT, int LANES, int NV, int SURE, bool STREAMED>
 hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
-  a.parts = bwd_parts<DT>(a.rows, a.size);
-  const dim3 grid(a.parts), block(bwd_threads(NV * kUnit<DT>));
+  a.parts = a.row_groups = bwd_parts<DT>(a.rows, a.size);
+  const bool strips = a.dweight && a.parts > 1 && a.rows <= kStripRows;
+  const dim3 grid(a.parts + (strips ? (a.size - 1) / (64 * kUnit<DT>) + 1 : 0)), block(bwd_threads(NV * kUnit<DT>));
   const DropArgs none{};
   if (!residual)
     hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, false, false, EIGHT, STREAMED>), grid, block, 0, st, a, none);
@@ -221,7 +283,7 @@ hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop,
   else
     hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, true, true, EIGHT, STREAMED>), grid, block, 0, st, a, *drop);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.parts == 1 || !a.dweight) return e;
+  if (e != hipSuccess || a.parts == 1 || strips || !a.dweight) return e;
   return rms_join_weight_grad<DT>(a, st);
 }
 

@@ -97,7 +97,7 @@ def act_tolerances(kind, x):
     by one more.  The derivative's two terms have those of p, of 1 - p and of
     two or three products.  erfc is taken to be good to 16 u, and its
     argument's rounding (1.5 u of x / sqrt 2) moves it by up to x^2 + 1 times
-    that; the density has (x^2 + 4) u.  Where e^-x passes 2^126 (and leaves
+    that; the density e^(-x^2 / 2) has (x^2 + 4) u.  Where e^-x passes 2^126 (and leaves
     binary32 at 2^128) p may be 0, which is up to 2^-126 off: `less` of a p.
     The tail of erfc and the density below 2^-126 may be 0 as well."""
     a = np.abs(x)

@@ -113,8 +113,9 @@ def test_residual_forward_refuses(over):
 @pytest.mark.parametrize("over,code", EXTENTS + [
     (dict(grad_dtype=BF16), EDTYPE), (dict(weight_dtype=BF16), EDTYPE), (dict(dy=None), EINVAL),
     (dict(dx=None), EINVAL), (dict(lddx=3), EINVAL), (dict(rstd=None), EINVAL), (dict(dweight=0x5001), EINVAL),
-    (dict(workspace=None), EINVAL), (dict(workspace=0x100008), EINVAL), (dict(workspace_bytes=63), EINVAL),
-    (dict(workspace_bytes=-1), EINVAL), (dict(dweight=0x1000), EINVAL), (dict(dx=0x100000), EINVAL),
+    (dict(rows=4096, workspace=None), EINVAL), (dict(rows=4096, workspace=0x100008), EINVAL),
+    (dict(rows=4096, workspace_bytes=63), EINVAL), (dict(workspace_bytes=-1), EINVAL), (dict(dweight=0x1000), EINVAL),
+    (dict(rows=4096, dy=0x1000000, x=0x2000000, dx=0x100000, workspace_bytes=1 << 24), EINVAL),
     (dict(dh=0x40000, lddh=16), EINVAL), (dict(dresidual=0x50000), EINVAL), (dict(x=None), EINVAL),
     (dict(x8=packed(0x70000, 16, 0x8000)), EINVAL),                   # x and x8
     (dict(x=None, x8=packed(0x30000, 16, 0x8000)), EINVAL),           # x8 under dx
@@ -232,7 +233,10 @@ def test_workspaces():
     for rows in (0, 1, 17, 4096, MOST):
         for size in (1, 7, 768, 16384, 1 << 22, MOST):
             n = L.gclip_rms_workspace(rows, size)
-            assert n == 0 if rows == 0 else 4 * size <= n <= max(4 * size, 32 << 20) + 4 * rows
+            if rows == 0 or (rows <= 128 and 8 <= size <= 8192):  # few rows in registers leave no parts
+                assert n == 0
+            else:
+                assert 4 * size <= n <= max(4 * size, 32 << 20) + 4 * rows
     for bad in ((-1, 8, 0), (8, 0, 0), (8, 8, -1), (8, 8, 9), (8, 64, 33)):
         assert L.gclip_logprob_workspace(*bad) == 0
     for rows in (0, 1, 8, 511, 512, 513, 8192, MOST):

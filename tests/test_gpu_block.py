@@ -35,7 +35,7 @@ def bits(*ts):
         if t is None:
             continue
         flat += [t.values, t.scales] if isinstance(t, G().Packed8) else [t]
-    return b"".join(t.detach().contiguous().view(torch.uint8).cpu().numpy().tobytes() for t in flat)
+    return b"".join(t.detach().contiguous().reshape(-1).view(torch.uint8).cpu().numpy().tobytes() for t in flat)
 
 
 # ---------------------------------------------------------------- 8 bits
@@ -481,6 +481,25 @@ def test_no_rows_and_no_columns():
     assert g.unpack8(g.pack8(x)).shape == (0, 24)
     e = torch.ones(4, 0, device="cuda")
     assert g.activation_forward(e, e)[0].shape == (4, 0) and g.activation_backward(e, e, e)[0].shape == (4, 0)
+
+
+def test_single_rows_without_other_dimensions():
+    import torch
+    g, x, w = G(), torch.randn(300, device="cuda"), torch.ones(300, device="cuda")
+    m = x[None]
+    for args in ({}, {"packed": "row", "keep": True}, {"packed": "block"}):
+        a, b = g.rms_norm_forward(x, w, **args), g.rms_norm_forward(m, w, **args)
+        assert bits(*a) == bits(*b) and a[1].shape == () and a[0].shape == (300,)
+    y, rstd, kept = g.rms_norm_forward(x, w, keep=True)
+    assert bits(*g.rms_norm_backward(x, kept, rstd, w)) == bits(*g.rms_norm_backward(m, g.pack8(m), rstd[None], w))
+    assert bits(*g.activation_forward(x, w, keep=True)) == bits(*g.activation_forward(m, w[None], keep=True))
+    assert bits(g.unpack8(g.pack8(x))) == bits(g.unpack8(g.pack8(m)))
+    t = torch.tensor(7, device="cuda")
+    a, b = (g.token_log_probs_forward(v, s, entropy=True, top=3) for v, s in ((x, t), (m, t[None])))
+    assert bits(*a) == bits(*b) and a.logp.shape == () and a.top_ids.shape == (3,)
+    v = x.clone().requires_grad_()
+    g.token_log_probs(g.rms_norm(g.activation(v, checkpoint=True), w, checkpoint=True), t).logp.backward()
+    assert torch.isfinite(v.grad).all()
 
 
 # ---------------------------------------------------------------- as they are used
