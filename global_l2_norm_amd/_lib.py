@@ -6,6 +6,7 @@ been built -- there is no fallback.
 """
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # GCLIP_LIBRARY may name another build of the same library to load instead:
@@ -135,6 +136,18 @@ class GclipLogprobs(ctypes.Structure):
                 ("lddlogits", ctypes.c_int64), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
+# A small call takes a few microseconds, a third of it once for filling a
+# structure field by field: the same bytes from one call of struct.
+PACK_PACKED8 = struct.Struct("PqPii")
+PACK_RMS_FORWARD = struct.Struct("qqiidPqPqPPqPq" + "PqPii" * 2 + "P")
+PACK_RMS_BACKWARD = struct.Struct("qqiiiiPqPqPq" + "PqPii" + "PPPqPqPPq")
+PACK_ACTIVATE = struct.Struct("qqiiPqPq" + "PqPii" * 2 + "PqPqPqPq")
+PACK_LOGPROBS = struct.Struct("qqiiPqPqPPPPPPPPqPq")
+for _packed, _structure in ((PACK_PACKED8, GclipPacked8), (PACK_RMS_FORWARD, GclipRmsForward),
+                            (PACK_RMS_BACKWARD, GclipRmsBackward), (PACK_ACTIVATE, GclipActivate),
+                            (PACK_LOGPROBS, GclipLogprobs)):
+    assert _packed.size == ctypes.sizeof(_structure), _structure
+
 assert ctypes.sizeof(GclipResult) == 64
 assert ctypes.sizeof(GclipAmpState) == 16
 
@@ -178,17 +191,18 @@ def _declare(lib):
         "gclip_residual_backward": ([ctypes.POINTER(GclipLayerBackward), ctypes.POINTER(GclipDropout), vp], i32),
         "gclip_dropout_apply": ([vp, i64, vp, i64, i64, i64, i32, ctypes.POINTER(GclipDropout), vp], i32),
         "gclip_layer_workspace": ([i64, i64], i64),
-        "gclip_rmsnorm_forward": ([ctypes.POINTER(GclipRmsForward), vp], i32),
-        "gclip_rmsnorm_backward": ([ctypes.POINTER(GclipRmsBackward), vp], i32),
-        "gclip_residual_rms_forward": ([ctypes.POINTER(GclipRmsForward), ctypes.POINTER(GclipDropout), vp], i32),
-        "gclip_residual_rms_backward": ([ctypes.POINTER(GclipRmsBackward), ctypes.POINTER(GclipDropout), vp], i32),
+        # a structure by reference, or its bytes
+        "gclip_rmsnorm_forward": ([vp, vp], i32),
+        "gclip_rmsnorm_backward": ([vp, vp], i32),
+        "gclip_residual_rms_forward": ([vp, ctypes.POINTER(GclipDropout), vp], i32),
+        "gclip_residual_rms_backward": ([vp, ctypes.POINTER(GclipDropout), vp], i32),
         "gclip_rms_workspace": ([i64, i64], i64),
-        "gclip_activation_forward": ([ctypes.POINTER(GclipActivate), vp], i32),
-        "gclip_activation_backward": ([ctypes.POINTER(GclipActivate), vp], i32),
-        "gclip_pack": ([vp, i64, ctypes.POINTER(GclipPacked8), i64, i64, i32, vp], i32),
-        "gclip_unpack": ([ctypes.POINTER(GclipPacked8), vp, i64, i64, i64, i32, vp], i32),
-        "gclip_logprob_forward": ([ctypes.POINTER(GclipLogprobs), vp], i32),
-        "gclip_logprob_backward": ([ctypes.POINTER(GclipLogprobs), vp], i32),
+        "gclip_activation_forward": ([vp, vp], i32),
+        "gclip_activation_backward": ([vp, vp], i32),
+        "gclip_pack": ([vp, i64, vp, i64, i64, i32, vp], i32),
+        "gclip_unpack": ([vp, vp, i64, i64, i64, i32, vp], i32),
+        "gclip_logprob_forward": ([vp, vp], i32),
+        "gclip_logprob_backward": ([vp, vp], i32),
         "gclip_logprob_workspace": ([i64, i64, i32], i64),
         "gclip_status_string": ([i32], ctypes.c_char_p),
         "gclip_last_hip_error": ([], i32),

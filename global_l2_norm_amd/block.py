@@ -27,31 +27,37 @@ except ImportError:  # the functions named like the C ABI do without it
 
 from . import _check, _lib
 from ._lib import (GCLIP_ACT_GELU, GCLIP_ACT_GELU_TANH, GCLIP_ACT_RELU, GCLIP_ACT_SILU, GCLIP_F32, GCLIP_SCALE_BLOCK,
-                   GCLIP_SCALES_BLOCK, GCLIP_SCALES_ROW, GclipActivate, GclipPacked8, GclipRmsBackward,
-                   GclipRmsForward)
+                   GCLIP_SCALES_BLOCK, GCLIP_SCALES_ROW, GclipPacked8)
 from .layers import _counted, _like, _matrix, _there, _vector, _wrote
 
 _byref = ctypes.byref
+_pack8, _pack_activate = _lib.PACK_PACKED8.pack, _lib.PACK_ACTIVATE.pack
+_pack_forward, _pack_backward = _lib.PACK_RMS_FORWARD.pack, _lib.PACK_RMS_BACKWARD.pack
 ACTIVATIONS = {"silu": GCLIP_ACT_SILU, "gelu": GCLIP_ACT_GELU, "gelu_tanh": GCLIP_ACT_GELU_TANH, "relu": GCLIP_ACT_RELU}
 _MODES = {"block": GCLIP_SCALES_BLOCK, "row": GCLIP_SCALES_ROW}
 
 
 # ---------------------------------------------------------------- C ABI names
+def _at(args):
+    """A structure's address; its bytes are an address to ctypes as they are."""
+    return args if type(args) is bytes else _byref(args)
+
+
 def gclip_rmsnorm_forward(args, stream):
-    _check(_lib.lib.gclip_rmsnorm_forward(_byref(args), stream), "gclip_rmsnorm_forward")
+    _check(_lib.lib.gclip_rmsnorm_forward(_at(args), stream), "gclip_rmsnorm_forward")
 
 
 def gclip_rmsnorm_backward(args, stream):
-    _check(_lib.lib.gclip_rmsnorm_backward(_byref(args), stream), "gclip_rmsnorm_backward")
+    _check(_lib.lib.gclip_rmsnorm_backward(_at(args), stream), "gclip_rmsnorm_backward")
 
 
 def gclip_residual_rms_forward(args, drop, stream):
-    _check(_lib.lib.gclip_residual_rms_forward(_byref(args), _byref(drop) if drop is not None else None, stream),
+    _check(_lib.lib.gclip_residual_rms_forward(_at(args), _byref(drop) if drop is not None else None, stream),
            "gclip_residual_rms_forward")
 
 
 def gclip_residual_rms_backward(args, drop, stream):
-    _check(_lib.lib.gclip_residual_rms_backward(_byref(args), _byref(drop) if drop is not None else None, stream),
+    _check(_lib.lib.gclip_residual_rms_backward(_at(args), _byref(drop) if drop is not None else None, stream),
            "gclip_residual_rms_backward")
 
 
@@ -60,19 +66,19 @@ def gclip_rms_workspace(rows, size):
 
 
 def gclip_activation_forward(args, stream):
-    _check(_lib.lib.gclip_activation_forward(_byref(args), stream), "gclip_activation_forward")
+    _check(_lib.lib.gclip_activation_forward(_at(args), stream), "gclip_activation_forward")
 
 
 def gclip_activation_backward(args, stream):
-    _check(_lib.lib.gclip_activation_backward(_byref(args), stream), "gclip_activation_backward")
+    _check(_lib.lib.gclip_activation_backward(_at(args), stream), "gclip_activation_backward")
 
 
 def gclip_pack(x, ldx, out, rows, size, dtype, stream):
-    _check(_lib.lib.gclip_pack(x, ldx, _byref(out), rows, size, dtype, stream), "gclip_pack")
+    _check(_lib.lib.gclip_pack(x, ldx, _at(out), rows, size, dtype, stream), "gclip_pack")
 
 
 def gclip_unpack(x, out, ldout, rows, size, dtype, stream):
-    _check(_lib.lib.gclip_unpack(_byref(x), out, ldout, rows, size, dtype, stream), "gclip_unpack")
+    _check(_lib.lib.gclip_unpack(_at(x), out, ldout, rows, size, dtype, stream), "gclip_unpack")
 
 
 # ---------------------------------------------------------------- matrices in 8 bits
@@ -81,7 +87,7 @@ if torch is not None:
     _E4M3 = torch.float8_e4m3fn
     # a size in a tuple costs 0.7 us more than one in arguments
     _empty, _empty_like, _contiguous = torch.empty, torch.empty_like, torch.contiguous_format
-_NONE8 = GclipPacked8()
+_NONE8 = (0, 0, 0, 0, 0)
 
 
 class Packed8:
@@ -96,7 +102,7 @@ class Packed8:
     ``pack8``, and the forward passes' ``keep`` and ``packed``, make them.
     """
 
-    __slots__ = ("values", "scales", "args")
+    __slots__ = ("held", "size", "scales", "fields")
 
     def __init__(self, values, scales):
         if values.dtype != _E4M3 or scales.dtype != _F32:
@@ -113,9 +119,8 @@ class Packed8:
             raise ValueError(f"{count} scales a row for {size} columns: one, or one for each {GCLIP_SCALE_BLOCK}")
         if scales.get_device() != values.get_device():
             raise ValueError("values and scales must be on one device")
-        ld = _row_bytes(values)
-        self.values, self.scales = values, scales
-        self.args = GclipPacked8(values.data_ptr(), ld, scales.data_ptr(), mode, 0)
+        self.held, self.size, self.scales = values, size, scales
+        self.fields = values.data_ptr(), _row_bytes(values), scales.data_ptr(), mode, 0
 
     @classmethod
     def _new(cls, x, size, mode):
@@ -124,23 +129,38 @@ class Packed8:
         lead = x.shape[:-1]
         ld = (size + 7) // 8 * 8
         if ld == size:
-            self.values = values = _empty_like(x, dtype=_E4M3, memory_format=_contiguous)
+            held = _empty_like(x, dtype=_E4M3, memory_format=_contiguous)
         else:
-            self.values = values = _empty(*lead, ld, dtype=_E4M3, device=x.device)[..., :size]
-        self.scales = scales = _empty(*lead, 1 if mode else (size + 127) // GCLIP_SCALE_BLOCK, dtype=_F32, device=x.device)
-        self.args = GclipPacked8(values.data_ptr(), ld, scales.data_ptr(), mode, 0)
+            held = _empty(*lead, ld, dtype=_E4M3, device=x.device)
+        scales = _empty(*lead, 1 if mode else (size + 127) // GCLIP_SCALE_BLOCK, dtype=_F32, device=x.device)
+        self.held, self.size, self.scales = held, size, scales
+        self.fields = held.data_ptr(), ld, scales.data_ptr(), mode, 0
         return self
 
     @property
+    def values(self):
+        held, size = self.held, self.size
+        return held if held.shape[-1] == size else held[..., :size]
+
+    def __reduce__(self):
+        return Packed8, (self.values, self.scales)
+
+    @property
+    def args(self):
+        """The C ABI's structure."""
+        return GclipPacked8(*self.fields)
+
+    @property
     def shape(self):
-        return self.values.shape
+        shape = self.held.shape
+        return shape if shape[-1] == self.size else torch.Size((*shape[:-1], self.size))
 
     @property
     def device(self):
-        return self.values.device
+        return self.held.device
 
     def record_stream(self, stream):
-        self.values.record_stream(stream)
+        self.held.record_stream(stream)
         self.scales.record_stream(stream)
 
     def dequantize(self):
@@ -175,11 +195,12 @@ def _packed(p, x, name):
     """A Packed8 of x's shape and device."""
     if not isinstance(p, Packed8):
         raise TypeError(f"{name} must be a Packed8 or a tensor, not {type(p).__name__}")
-    if p.shape != x.shape or p.values.get_device() != x.get_device():
+    if p.shape != x.shape or p.held.get_device() != x.get_device():
         raise ValueError(f"{name} must have shape {tuple(x.shape)} on {x.device}")
-    if p.values.data_ptr() != (p.args.values or 0) or p.scales.data_ptr() != (p.args.scales or 0):
+    fields = p.fields
+    if p.held.data_ptr() != fields[0] or p.scales.data_ptr() != fields[2]:
         raise ValueError(f"{name} has another storage than when it was made")
-    return p.args
+    return fields
 
 
 def _mode(name):
@@ -206,7 +227,7 @@ def pack8(x, scales="block", *, stream=None):
     if size == 0:
         raise ValueError("x must have at least one column")
     out = Packed8._new(x, size, mode)
-    gclip_pack(x.data_ptr(), ld, out.args, rows, size, code, _raw_stream(device))
+    gclip_pack(x.data_ptr(), ld, _pack8(*out.fields), rows, size, code, _raw_stream(device))
     return out
 
 
@@ -228,7 +249,7 @@ def _unpack8(packed, dtype, out):
     else:
         new = out
     device, rows, size, ld, code = _matrix(new, "out")
-    gclip_unpack(_packed(packed, new, "packed"), new.data_ptr(), ld, rows, size, code, _raw_stream(device))
+    gclip_unpack(_pack8(*_packed(packed, new, "packed")), new.data_ptr(), ld, rows, size, code, _raw_stream(device))
     _wrote(out)
     return new
 
@@ -262,15 +283,15 @@ def residual_rms_norm_forward(x, residual, weight=None, eps=1e-6, mask=None, *, 
 
 def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
     device, rows, size, ld, code = _matrix(x, "x")
-    wp, wdt = None, GCLIP_F32
+    wp, wdt = 0, GCLIP_F32
     if weight is not None:
         wp, wdt = _vector(weight, size, x, "weight"), _CODES[weight.dtype]
-    yp, ldy, y8 = None, 0, _NONE8
+    yp, ldy, y8 = 0, 0, _NONE8
     if packed is not None:
         if y is not None:
             raise ValueError("out is for a y that is not packed")
         y = Packed8._new(x, size, _mode(packed))
-        y8 = y.args
+        y8 = y.fields
     elif y is None:
         y = _empty_like(x, memory_format=_contiguous)
         yp, ldy = y.data_ptr(), size
@@ -280,15 +301,15 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
     kept, k8 = None, _NONE8
     if keep:
         kept = Packed8._new(x, size, GCLIP_SCALES_BLOCK)
-        k8 = kept.args
-    rstd = rp = None
+        k8 = kept.fields
+    rstd, rp = None, 0
     if stats:
         lead = x.shape[:-1]
         rstd = _empty(*lead, dtype=_F32, device=x.device) if lead else _empty((), dtype=_F32, device=x.device)
         rp = rstd.data_ptr()
     if residual is None:
-        gclip_rmsnorm_forward(GclipRmsForward(rows, size, code, wdt, eps, x.data_ptr(), ld, None, 0, wp, None, 0, yp,
-                                              ldy, y8, k8, rp), _raw_stream(device))
+        gclip_rmsnorm_forward(_pack_forward(rows, size, code, wdt, eps, x.data_ptr(), ld, 0, 0, wp, 0, 0, yp, ldy, *y8,
+                                            *k8, rp), _raw_stream(device))
         return None, y, rstd, kept
     ldr = _like(residual, x, "residual")
     if h is None:
@@ -296,8 +317,8 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
         ldh = size
     else:
         ldh = _like(h, x, "out_h")
-    gclip_residual_rms_forward(GclipRmsForward(rows, size, code, wdt, eps, x.data_ptr(), ld, residual.data_ptr(), ldr,
-                                               wp, h.data_ptr(), ldh, yp, ldy, y8, k8, rp),
+    gclip_residual_rms_forward(_pack_forward(rows, size, code, wdt, eps, x.data_ptr(), ld, residual.data_ptr(), ldr, wp,
+                                             h.data_ptr(), ldh, yp, ldy, *y8, *k8, rp),
                                _counted(mask, device) if mask is not None and mask.drops else None,
                                _raw_stream(device))
     return h, y, rstd, kept
@@ -335,7 +356,7 @@ def residual_rms_norm_backward(dy, dh, h, rstd, weight=None, mask=None, *, dweig
 
 def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weight_grad, dx, dres):
     device, rows, size, lddy, code = _matrix(dy, "dy")
-    wp, wdt, gt = None, GCLIP_F32, _F32
+    wp, wdt, gt = 0, GCLIP_F32, _F32
     if weight is not None:
         wp, gt = _vector(weight, size, dy, "weight"), weight.dtype
         wdt = _CODES[gt]
@@ -345,18 +366,18 @@ def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weig
     if rstd.dtype != _F32:
         raise TypeError(f"rstd must be float32, not {rstd.dtype}")
     rp = _vector(rstd, rows, dy, "rstd")
-    xp, ldx, x8 = None, 0, _NONE8
+    xp, ldx, x8 = 0, 0, _NONE8
     if isinstance(x, Packed8):
         x8 = _packed(x, dy, "x")
     else:
         ldx = _like(x, dy, "x")
         xp = x.data_ptr()
-    hp, lddh = None, 0
+    hp, lddh = 0, 0
     if dh is not None:
         hp, lddh = dh.data_ptr(), _like(dh, dy, "dh")
     nbytes = gclip_rms_workspace(rows, size)
     workspace = _empty(nbytes, dtype=torch.uint8, device=dy.device) if nbytes else None
-    wgp = None
+    wgp = 0
     if want:
         if dweight is None:
             dweight = _empty(size, dtype=gt, device=dy.device)
@@ -367,8 +388,7 @@ def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weig
         if dx is not None and dres is not None and dx is not dres:
             raise ValueError("without dropout dx is dresidual: give one buffer")
         dres = dres if dres is not None else dx
-    dxp = sp = None
-    lddx = ldds = 0
+    dxp = sp = lddx = ldds = 0
     if second:
         if dx is None:
             dx = _empty_like(dy, memory_format=_contiguous)
@@ -383,9 +403,8 @@ def _backward(dy, dh, x, rstd, weight, mask, residual, dweight, accumulate, weig
         else:
             ldds = _like(dres, dy, "out_residual")
         sp = dres.data_ptr()
-    args = GclipRmsBackward(rows, size, code, wdt, _CODES[gt], 1 if accumulate else 0, dy.data_ptr(), lddy, hp, lddh, xp,
-                            ldx, x8, rp, wp, sp, ldds, dxp, lddx, wgp,
-                            workspace.data_ptr() if nbytes else None, nbytes)
+    args = _pack_backward(rows, size, code, wdt, _CODES[gt], 1 if accumulate else 0, dy.data_ptr(), lddy, hp, lddh, xp,
+                          ldx, *x8, rp, wp, sp, ldds, dxp, lddx, wgp, workspace.data_ptr() if nbytes else 0, nbytes)
     if residual:
         gclip_residual_rms_backward(args, _counted(mask, device) if mask is not None else None, _raw_stream(device))
     else:
@@ -415,7 +434,7 @@ def _kind(name):
 def _activation_forward(gate, up, kind, keep, y):
     kind = _kind(kind)
     device, rows, size, ld, code = _matrix(gate, "gate")
-    up_at, ldu = (up.data_ptr(), _like(up, gate, "up")) if up is not None else (None, 0)
+    up_at, ldu = (up.data_ptr(), _like(up, gate, "up")) if up is not None else (0, 0)
     if y is None:
         y = _empty_like(gate, memory_format=_contiguous)
         ldy = size
@@ -428,9 +447,10 @@ def _activation_forward(gate, up, kind, keep, y):
             up8 = Packed8._new(gate, size, GCLIP_SCALES_BLOCK)
     if rows == 0 or size == 0:
         return y, gate8, up8
-    gclip_activation_forward(GclipActivate(rows, size, code, kind, gate.data_ptr(), ld, up_at, ldu,
-                                           gate8.args if keep else _NONE8, up8.args if up8 is not None else _NONE8,
-                                           y.data_ptr(), ldy, None, 0, None, 0, None, 0), _raw_stream(device))
+    gclip_activation_forward(_pack_activate(rows, size, code, kind, gate.data_ptr(), ld, up_at, ldu,
+                                            *(gate8.fields if keep else _NONE8),
+                                            *(up8.fields if up8 is not None else _NONE8), y.data_ptr(), ldy, 0, 0, 0, 0,
+                                            0, 0), _raw_stream(device))
     return y, gate8, up8
 
 
@@ -452,8 +472,7 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
     eight = isinstance(gate, Packed8)
     if up is not None and isinstance(up, Packed8) != eight:
         raise TypeError("gate and up must both be tensors, or both in 8 bits")
-    gp = up_at = None
-    ldg = ldu = 0
+    gp = up_at = ldg = ldu = 0
     g8 = u8 = _NONE8
     if eight:
         g8 = _packed(gate, dy, "gate")
@@ -470,7 +489,7 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
         lddg = size
     else:
         lddg = _like(dgate, dy, "out_gate")
-    dup_at, lddu = None, 0
+    dup_at = lddu = 0
     if up is not None:
         if dup is None:
             dup = _empty_like(dy, memory_format=_contiguous)
@@ -480,7 +499,7 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
         dup_at = dup.data_ptr()
     elif dup is not None:
         raise ValueError("out_up is for a gated activation")
-    yp, ldy = None, 0
+    yp = ldy = 0
     if y is not None and not recompute:
         raise ValueError("out is for recompute")
     if recompute:
@@ -491,8 +510,8 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
             ldy = _like(y, dy, "out")
         yp = y.data_ptr()
     if rows and size:
-        gclip_activation_backward(GclipActivate(rows, size, code, kind, gp, ldg, up_at, ldu, g8, u8, yp, ldy,
-                                                dy.data_ptr(), lddy, dgate.data_ptr(), lddg, dup_at, lddu),
+        gclip_activation_backward(_pack_activate(rows, size, code, kind, gp, ldg, up_at, ldu, *g8, *u8, yp, ldy,
+                                                 dy.data_ptr(), lddy, dgate.data_ptr(), lddg, dup_at, lddu),
                                   _raw_stream(device))
     return dgate, dup, y
 
@@ -503,14 +522,21 @@ if torch is not None:
 
     from .layers import _matrix_of, _tracked, dropout_backward
 
+    def _of_held(held, scales, size):
+        """A Packed8 from the memory that holds its rows whole, which is what
+        autograd saves: a hook that moves a saved tensor keeps its values and
+        not its layout."""
+        return Packed8(held if held.shape[-1] == size else held[..., :size], scales)
+
     def _save(ctx, kept, x, *more):
         """x or its 8-bit form, for the backward pass."""
         ctx.packed = kept is not None
-        ctx.save_for_backward(*((kept.values, kept.scales) if kept is not None else (x, None)), *more)
+        ctx.size = x.shape[-1]
+        ctx.save_for_backward(*((kept.held, kept.scales) if kept is not None else (x, None)), *more)
 
     def _saved(ctx):
         a, b, *more = ctx.saved_tensors
-        return Packed8(a, b) if ctx.packed else a, *more
+        return _of_held(a, b, ctx.size) if ctx.packed else a, *more
 
     class _RmsNorm(torch.autograd.Function):
         @staticmethod
@@ -558,9 +584,9 @@ if torch is not None:
         @staticmethod
         def forward(ctx, gate, up, kind, checkpoint):
             y, gate8, up8 = activation_forward(gate, up, kind, keep=checkpoint)
-            ctx.kind, ctx.packed, ctx.gated = kind, checkpoint, up is not None
+            ctx.kind, ctx.packed, ctx.gated, ctx.size = kind, checkpoint, up is not None, gate.shape[-1]
             if checkpoint:
-                ctx.save_for_backward(gate8.values, gate8.scales, *((up8.values, up8.scales) if up is not None else ()))
+                ctx.save_for_backward(gate8.held, gate8.scales, *((up8.held, up8.scales) if up is not None else ()))
             else:
                 ctx.save_for_backward(gate, *((up,) if up is not None else ()))
             return y
@@ -570,7 +596,7 @@ if torch is not None:
         def backward(ctx, dy):
             saved = ctx.saved_tensors
             if ctx.packed:
-                saved = [Packed8(*saved[i:i + 2]) for i in range(0, len(saved), 2)]
+                saved = [_of_held(*saved[i:i + 2], ctx.size) for i in range(0, len(saved), 2)]
             dgate, dup, _ = activation_backward(_matrix_of(dy), saved[0], saved[1] if ctx.gated else None, ctx.kind)
             return dgate, dup, None, None
 

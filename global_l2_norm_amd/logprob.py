@@ -6,7 +6,6 @@ backward pass starts from, and what a server answers with.
 ``token_log_probs`` is the same under autograd, in its backward mode.
 Matrices, streams, captures and refusals are those of ``layers``.
 """
-import ctypes
 from typing import NamedTuple
 
 try:
@@ -15,19 +14,20 @@ except ImportError:  # the functions named like the C ABI do without it
     torch = None
 
 from . import _check, _lib
-from ._lib import GCLIP_LOGPROB_MAX_TOP, GclipLogprobs
+from ._lib import GCLIP_LOGPROB_MAX_TOP
+from .block import _at
 from .layers import _like, _matrix, _there, _vector, _wrote
 
-_byref = ctypes.byref
+_pack = _lib.PACK_LOGPROBS.pack
 
 
 # ---------------------------------------------------------------- C ABI names
 def gclip_logprob_forward(args, stream):
-    _check(_lib.lib.gclip_logprob_forward(_byref(args), stream), "gclip_logprob_forward")
+    _check(_lib.lib.gclip_logprob_forward(_at(args), stream), "gclip_logprob_forward")
 
 
 def gclip_logprob_backward(args, stream):
-    _check(_lib.lib.gclip_logprob_backward(_byref(args), stream), "gclip_logprob_backward")
+    _check(_lib.lib.gclip_logprob_backward(_at(args), stream), "gclip_logprob_backward")
 
 
 def gclip_logprob_workspace(rows, size, top):
@@ -88,7 +88,7 @@ def _forward(logits, targets, entropy, top, ignore, stats):
     if not 0 <= top <= min(GCLIP_LOGPROB_MAX_TOP, size):
         raise ValueError(f"top must be at most {GCLIP_LOGPROB_MAX_TOP} and the {size} tokens, not {top}")
     lead = logits.shape[:-1]
-    tp = _targets(targets, rows, logits) if targets is not None else None
+    tp = _targets(targets, rows, logits) if targets is not None else 0
     on = logits.device
     row = lead or ((),)  # a size in a tuple costs 0.7 us more than one in arguments
     logp = _empty(*row, dtype=_F32, device=on) if targets is not None else None
@@ -99,10 +99,9 @@ def _forward(logits, targets, entropy, top, ignore, stats):
         top_logp, top_ids = _empty(*lead, top, dtype=_F32, device=on), _empty(*lead, top, dtype=_I64, device=on)
     nbytes = gclip_logprob_workspace(rows, size, top)
     workspace = _empty(nbytes, dtype=torch.uint8, device=on) if nbytes else None
-    at = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
-    gclip_logprob_forward(GclipLogprobs(rows, size, code, top, logits.data_ptr(), ld, tp, ignore, at(stats), at(logp),
-                                        at(h), at(top_logp), at(top_ids), None, None, None, 0, at(workspace), nbytes),
-                          _raw_stream(device))
+    at = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
+    gclip_logprob_forward(_pack(rows, size, code, top, logits.data_ptr(), ld, tp, ignore, at(stats), at(logp), at(h),
+                                at(top_logp), at(top_ids), 0, 0, 0, 0, at(workspace), nbytes), _raw_stream(device))
     return TokenLogProbs(logp, h, stats, top_logp, top_ids)
 
 
@@ -121,7 +120,7 @@ def _backward(dlogp, dentropy, logits, targets, stats, entropy, ignore, out):
     device, rows, size, ld, code = _matrix(logits, "logits")
     tp, sp = _targets(targets, rows, logits), _numbers(stats, 2 * rows, logits, "stats")
     dp = _numbers(dlogp, rows, logits, "dlogp")
-    ep = hp = None
+    ep = hp = 0
     if dentropy is not None:
         if entropy is None:
             raise ValueError("dentropy needs the entropy of the forward pass")
@@ -131,8 +130,8 @@ def _backward(dlogp, dentropy, logits, targets, stats, entropy, ignore, out):
         ldo = size
     else:
         ldo = _like(out, logits, "out")
-    gclip_logprob_backward(GclipLogprobs(rows, size, code, 0, logits.data_ptr(), ld, tp, ignore, sp, None, hp, None,
-                                         None, dp, ep, out.data_ptr(), ldo, None, 0), _raw_stream(device))
+    gclip_logprob_backward(_pack(rows, size, code, 0, logits.data_ptr(), ld, tp, ignore, sp, 0, hp, 0, 0, dp, ep,
+                                 out.data_ptr(), ldo, 0, 0), _raw_stream(device))
     return out
 
 
@@ -166,6 +165,7 @@ if torch is not None:
 def token_log_probs(logits, targets, *, entropy=False, top=0, ignore_index=-100):
     """A ``TokenLogProbs`` whose logp and entropy have gradients; the others
     have none."""
+    targets = targets.contiguous()
     if not _tracked(logits):
         return token_log_probs_forward(logits, targets, entropy=entropy, top=top, ignore_index=ignore_index)
     return TokenLogProbs(*_TokenLogProbs.apply(logits, targets, entropy, top, ignore_index))

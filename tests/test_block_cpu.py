@@ -71,6 +71,17 @@ BAD8 = [packed(0x70000, 16, None), packed(0x70004, 16, 0x8000), packed(0x70000, 
         packed(None, 16, 0x8000)]
 
 
+class _ByReference:
+    """The calls with a structure by reference."""
+
+    def __getattr__(self, name):
+        f = getattr(_lib.lib, name)
+        return lambda *a: f(*(ctypes.byref(x) if isinstance(x, ctypes.Structure) else x for x in a))
+
+
+L = _ByReference()
+
+
 @pytest.mark.parametrize("over,code", EXTENTS + [
     (dict(weight_dtype=F16), EDTYPE), (dict(dtype=BF16, weight_dtype=F16), EDTYPE), (dict(x=None), EINVAL),
     (dict(x=0x10002), EINVAL), (dict(ldx=-16), EINVAL), (dict(ldx=1 << 60), EINVAL), (dict(weight=0x1001), EINVAL),
@@ -322,6 +333,36 @@ def test_packed_matrices_check_their_layout():
             G.Packed8(values, scales)
     with pytest.raises(ValueError):
         G.pack8(one(4, 8), "column")
+
+
+def test_structures_as_bytes():
+    """The bytes that the tensors' functions pass are the structure's."""
+    a = fwd(y=None, y8=packed(0x70000, 32, 0x8000, ROW), kept=packed(0x90000, 16, 0x9000), **RES_F)
+    assert bytes(a) == _lib.PACK_RMS_FORWARD.pack(4, 16, F32, F32, 1e-5, 0x10000, 16, 0x30000, 16, 0x1000, 0x40000, 16, 0, 16,
+                                                  0x70000, 32, 0x8000, ROW, 0, 0x90000, 16, 0x9000, BLOCK, 0, 0x4000)
+    a = bwd(dtype=BF16, grad_dtype=BF16, accumulate=1, x=None, ldx=3, x8=packed(0x70000, 32, 0x8000), **RES_B)
+    assert bytes(a) == _lib.PACK_RMS_BACKWARD.pack(4, 16, BF16, F32, BF16, 1, 0x10000, 16, 0x40000, 16, 0, 3, 0x70000, 32, 0x8000,
+                                                   BLOCK, 0, 0x4000, 0x1000, 0x50000, 16, 0x30000, 16, 0x5000, 0x100000, 1 << 20)
+    a = act(**{**ACT_B, "kind": 2}, gate8=packed(1, 2, 3), up8=packed(4, 5, 6))
+    assert bytes(a) == _lib.PACK_ACTIVATE.pack(4, 16, F32, 2, 0x10000, 16, 0x20000, 16, 1, 2, 3, 0, 0, 4, 5, 6, 0, 0, 0, 16, 0x40000,
+                                               16, 0x50000, 16, 0x60000, 16)
+    a = logp(top=3, top_logp=1, top_ids=2, dlogp=3, dentropy=4, dlogits=5, lddlogits=6)
+    assert bytes(a) == _lib.PACK_LOGPROBS.pack(4, 16, F32, 3, 0x10000, 16, 0x1000, -100, 0x2000, 0x3000, 0x4000, 1, 2, 3, 4, 5, 6,
+                                               0x100000, 1 << 20)
+    assert _lib.lib.gclip_rmsnorm_forward(bytes(fwd(size=0)), None) == EINVAL
+
+
+def test_packed_matrices_are_copied():
+    import copy
+
+    import torch
+
+    import global_l2_norm_amd as G
+    held = torch.arange(4 * 136, dtype=torch.uint8).view(4, 136).view(torch.float8_e4m3fn)
+    p = G.Packed8(held[:, :131], torch.rand(4, 2))
+    for q in (copy.copy(p), copy.deepcopy(p)):
+        assert torch.equal(q.values.view(torch.uint8), p.values.view(torch.uint8)) and torch.equal(q.scales, p.scales)
+        assert q.args.ld == 136 and q.args.values == q.values.data_ptr()
 
 
 def test_forward_mode_derivatives_and_traces_are_refused():

@@ -666,6 +666,30 @@ def test_under_autograd(dtype):
         first.sum().backward()
 
 
+def test_saved_tensors_may_be_moved():
+    """Hooks that move what autograd saves (to the host and back, or into
+    memory of another layout) keep the gradients' bits."""
+    import torch
+    g = G()
+    for size in (200, 203):
+        x = torch.randn(6, 2 * size, device="cuda", dtype=torch.bfloat16)
+        w = torch.ones(size, device="cuda")
+
+        def step(hooks):
+            v = x.clone().requires_grad_()
+            with hooks:
+                h, y = g.residual_rms_norm(v[:, :size], v[:, size:], w, checkpoint=True)
+                z = g.activation(y, h, checkpoint=True)
+                z = g.rms_norm(z, w, checkpoint=True)
+                p = g.token_log_probs(z, torch.zeros(6, dtype=torch.int64, device="cuda"), entropy=True)
+            (p.logp.sum() + p.entropy.sum()).backward()
+            return bits(v.grad)
+        import contextlib
+        want = step(contextlib.nullcontext())
+        assert step(torch.autograd.graph.save_on_cpu()) == want
+        assert step(torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(memory_format=torch.contiguous_format), lambda t: t)) == want
+
+
 def test_written_buffers_count_their_versions_up():
     import torch
     g = G()
