@@ -137,3 +137,55 @@ def test_served_tokens_products_of_8_bit_operands(rows):
     want = a @ b.T
     tol = (width + 4) * lu.U * (np.abs(a) @ np.abs(b).T)
     lu.within(lu.values(out), want, bu.stored(want, "bf16", tol), "product")
+
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "gated_lm.py")
+    spec = importlib.util.spec_from_file_location("gated_lm", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("bf16,checkpoint,entropy", [(False, False, 0.0), (True, True, 0.01), (False, True, 0.0)])
+def test_the_example_runs(bf16, checkpoint, entropy):
+    import torch
+    losses, norms = _example().train(3, dtype=torch.bfloat16 if bf16 else torch.float32, checkpoint=checkpoint, entropy=entropy)
+    assert len(losses) == len(norms) == 3 and np.isfinite(losses).all() and np.isfinite(norms).all() and min(norms) > 0
+
+
+def test_the_examples_gradients():
+    """Against the model written in binary64 torch operations.  Each of the
+    about 25 steps from the embeddings to the loss and back is off by at most
+    (K + 10) u of its result's norm, with K <= 512 terms a sum, 25 522 2^-24 =
+    8e-4 in all, and errors grow from step to step by what the blocks pass on
+    of them, for which a factor of 10 stands."""
+    import torch
+    e = _example()
+    model = e.Model(seed=3)
+    generator = torch.Generator().manual_seed(4)
+    tokens, targets = e.batch(torch.randperm(257, generator=generator), 4, 16, generator)
+    model.loss(tokens, targets, entropy=0.05).backward()
+
+    p = [t.detach().double().cpu().requires_grad_() for t in model.params]
+    emb, norms, rest = p[0], p[1:5], p[5:]
+    rms = lambda h, w: h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * w  # noqa: E731
+    x = emb[tokens.cpu().reshape(-1)]
+    h = torch.zeros_like(x)
+    for i in range(3):
+        h = h + x
+        both = rms(h, norms[i]) @ rest[2 * i]
+        gate, up = both[:, :512], both[:, 512:]
+        x = (gate * torch.sigmoid(gate) * up) @ rest[2 * i + 1]
+    z = torch.log_softmax(rms(h + x, norms[3]) @ emb.t(), 1)
+    t = targets.cpu().reshape(-1)
+    counted = t != -100
+    logp = z.gather(1, t.clamp(min=0)[:, None])[:, 0]
+    entropy = -(z.exp() * z).sum(1)
+    loss = -((logp + 0.05 * entropy) * counted).sum() / counted.sum()
+    loss.backward()
+    for i, (a, b) in enumerate(zip(model.params, p)):
+        off = (a.grad.double().cpu() - b.grad).norm() / b.grad.norm()
+        assert off <= 8e-3, (i, float(off))
