@@ -172,6 +172,13 @@ def test_rms_every_number_of_rows(rows, size, dtype):
     run_rms(rows, size, dtype, "f32", "plain" if rows % 2 else "padded", seed=1)
 
 
+@pytest.mark.parametrize("rows,size", [(100, 768), (128, 130), (128, 4097), (129, 4097), (127, 8193), (129, 40), (2, 8193)])
+def test_rms_weight_gradients_of_few_rows(rows, size):
+    """As many rows as one launch serves, and one more."""
+    for dtype, wt in (("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")):
+        run_rms(rows, size, dtype, wt, "shifted" if rows % 2 else "plain", seed=4, forms=("row",))
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("shape", [8, 16, 32, 64, 128, 192, 256, 384, 512, 768, 1024, 1536, 2048, 4096, 6144, 8192, 12288])
 def test_rms_shapes_of_many_rows(shape, dtype):

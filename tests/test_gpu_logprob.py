@@ -111,6 +111,43 @@ def test_every_number_of_rows(rows, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,size", [(1536, 2049), (1600, 2500), (1535, 2500), (1537, 8449), (1536, 16384), (1536, 16385)])
+def test_many_rows_by_a_wave_each(rows, size, dtype):
+    """As many as have a wave each and one fewer; rows at a lane's last turn
+    and one column past it."""
+    x, rng = logits(rows, size, 8)
+    targets = rng.integers(0, size, rows)
+    targets[::7] = -100
+    x[3, size // 3:] = -np.inf
+    x[4, :] = -np.inf
+    x[5, :-1] = -np.inf
+    targets[3], targets[4], targets[5] = 0, 1, size - 1
+    layout = ("plain", "padded", "shifted")[size % 3]
+    check(x, targets, 20, dtype, f"{rows} x {size} {dtype} top", layout, gradient=False)
+    check(x, targets, 0, dtype, f"{rows} x {size} {dtype}", layout, entropy=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_rows_by_a_wave_each_streamed(dtype):
+    x, rng = logits(4500 if dtype == "f32" else 9001, 8449, 9)
+    check(x, rng.integers(0, 8449, len(x)), 3, dtype, f"streamed by waves {dtype}", gradient=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [1, 4, 5, 16, 17, 31, 33, 64, 65, 127, 129, 250, 256, 257, 500, 513, 1000, 1025])
+def test_many_short_rows(size, dtype):
+    """8192 rows and more, where a row has fewer lanes."""
+    for rows in (8192, 8201):
+        x, rng = logits(rows, size, 10)
+        targets = rng.integers(0, size, rows)
+        targets[::11] = -100
+        x[2, size // 2:] = -np.inf
+        x[rows - 1, :] = -np.inf
+        check(x, targets, 0, dtype, f"{rows} x {size} {dtype}", "padded" if rows % 2 else "plain")
+        check(x, targets, min(3, size), dtype, f"{rows} x {size} {dtype} top", entropy=False, gradient=False)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_streamed(dtype):
     x, rng = logits(2100, 20011 if dtype == "f32" else 40011, 2)
     check(x, rng.integers(0, x.shape[1], len(x)), 3, dtype, f"streamed {dtype}")
