@@ -24,7 +24,8 @@ __device__ __forceinline__ void store_rms_weight_grad(const RmsBwdArgs& a, uint3
 // The weight's gradient of few rows: it takes neither the rows' sums nor their
 // results, so workgroups of their own, in the same launch, take a strip of 64
 // units of columns each down all rows, from the caches, and no parts are left
-// to join.
+// to join.  Where the results go in place over what the strips read, the
+// strips have a launch of their own, before the rows'.
 template <int DT, bool EIGHT, uint32_t WAVES>
 __device__ __forceinline__ void strip_weight_grad(const RmsBwdArgs& a, uint32_t strip, float* meet) {
   constexpr uint32_t kU = kUnit<DT>;
@@ -270,11 +271,10 @@ hipError_t rms_join_weight_grad(const RmsBwdArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Rows' workgroups (a.row_groups of them) and strips'.
 template <int DT, bool EIGHT, int LANES, int NV, int SURE, bool STREAMED>
-hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
-  a.parts = a.row_groups = bwd_parts<DT>(a.rows, a.size);
-  const bool strips = a.dweight && a.parts > 1 && a.rows <= kStripRows;
-  const dim3 grid(a.parts + (strips ? (a.size - 1) / (64 * kUnit<DT>) + 1 : 0)), block(bwd_threads(NV * kUnit<DT>));
+hipError_t rms_backward_launch(const RmsBwdArgs& a, uint32_t strips, bool residual, const DropArgs* drop, hipStream_t st) {
+  const dim3 grid(a.row_groups + strips), block(bwd_threads(NV * kUnit<DT>));
   const DropArgs none{};
   if (!residual)
     hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, false, false, EIGHT, STREAMED>), grid, block, 0, st, a, none);
@@ -282,8 +282,28 @@ hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop,
     hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, true, false, EIGHT, STREAMED>), grid, block, 0, st, a, none);
   else
     hipLaunchKernelGGL((k_rms_rows_grad<DT, LANES, NV, SURE, true, true, EIGHT, STREAMED>), grid, block, 0, st, a, *drop);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.parts == 1 || strips || !a.dweight) return e;
+  return hipGetLastError();
+}
+
+template <int DT, bool EIGHT, int LANES, int NV, int SURE, bool STREAMED>
+hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop, hipStream_t st) {
+  a.parts = a.row_groups = bwd_parts<DT>(a.rows, a.size);
+  if (a.dweight && a.parts > 1 && a.rows <= kStripRows) {
+    uint32_t strips = (a.size - 1) / (64 * kUnit<DT>) + 1;
+    const auto over = [&](uint64_t out) { return out != 0 && (out == a.dy.at || out == a.x.at); };
+    if (over(a.dres.at) || over(a.dx.at)) {
+      RmsBwdArgs weight_alone = a;
+      weight_alone.row_groups = 0;
+      const hipError_t e =
+          rms_backward_launch<DT, EIGHT, LANES, NV, SURE, STREAMED>(weight_alone, strips, residual, drop, st);
+      if (e != hipSuccess) return e;
+      a.dweight = 0;
+      strips = 0;
+    }
+    return rms_backward_launch<DT, EIGHT, LANES, NV, SURE, STREAMED>(a, strips, residual, drop, st);
+  }
+  const hipError_t e = rms_backward_launch<DT, EIGHT, LANES, NV, SURE, STREAMED>(a, 0, residual, drop, st);
+  if (e != hipSuccess || a.parts == 1 || !a.dweight) return e;
   return rms_join_weight_grad<DT>(a, st);
 }
 

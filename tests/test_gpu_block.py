@@ -302,6 +302,33 @@ def test_rms_in_place_and_between_guards(size, dtype):
     assert (guard == 7.0).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,size", [(9, 768), (128, 768), (100, 8200), (128, 2047), (129, 2047), (128, 16384), (70, 20000)])
+def test_rms_gradients_in_place_of_few_rows(rows, size, dtype):
+    """The weight's gradient reads dy and x of all rows, which the rows' own
+    results may be written over."""
+    import torch
+    g, rng = G(), np.random.default_rng([rows, size])
+    v = [rng.standard_normal((rows, size)) for _ in range(3)]
+    fresh = lambda: [lu.matrix(t, dtype, "padded") for t in v]  # noqa: E731
+    x, dy, dh = fresh()
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal(size)).float().cuda()
+    m = mask()
+    _, rstd, kept = g.rms_norm_forward(x, w, EPS, keep=True)
+    for held in (x, kept):
+        plain, step = g.rms_norm_backward(dy, held, rstd, w), g.residual_rms_norm_backward(dy, dh, held, rstd, w, m)
+        for _ in range(3):
+            x1, dy1, dh1 = fresh()
+            x2 = x1 if held is x else held
+            assert bits(*g.rms_norm_backward(dy1, x2, rstd, w, out=dy1)) == bits(*plain)
+            x1, dy1, dh1 = fresh()
+            x2 = x1 if held is x else held
+            assert bits(*g.residual_rms_norm_backward(dy1, dh1, x2, rstd, w, m, out=x1, out_residual=dy1)) == bits(*step)
+    for _ in range(3):
+        x1, dy1, _ = fresh()
+        assert bits(*g.rms_norm_backward(dy1, x1, rstd, w, out=x1)) == bits(*g.rms_norm_backward(dy, x, rstd, w))
+
+
 @pytest.mark.parametrize("size", [5, 64, 129, 1000, 2048, 20001])
 def test_values_in_8_bits_between_guards(size):
     """The C ABI's rows of values in a wider buffer: bytes outside of a row's
