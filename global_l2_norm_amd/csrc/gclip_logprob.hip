@@ -616,7 +616,8 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_grad(LogpArgs a, Split sp
   const int64_t target = a.targets[r];
   const float m = a.stats[2ull * r], s = a.stats[2ull * r + 1], dlogp = a.dlogp[r];
   const float entropy = ENTROPY ? a.entropy[r] : 0.0f, dent = ENTROPY ? a.dentropy[r] : 0.0f;
-  const bool counts = target != a.ignore && m != kNone, valid = target >= 0 && target < (int64_t)a.size;
+  // s of -infinity: nothing that can come; m alone is that in a row of NaNs too
+  const bool counts = target != a.ignore && s != kNone, valid = target >= 0 && target < (int64_t)a.size;
   if (a.size >= kU && c + kU > a.size) q = moved_down<DT>(q, kU - a.size % kU);
   float v[kU];
   unpack_unit<DT>(q, v);

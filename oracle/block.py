@@ -134,6 +134,6 @@ def log_probs_gradient(x, target, dlogp, dentropy, m, s, entropy, ignore=-100):
     valid = (target >= 0) & (target < x.shape[1])
     d[np.flatnonzero(valid), target[valid]] += dlogp[valid]
     d[~valid] = np.nan
-    d[np.isneginf(m)] = 0.0
+    d[np.isneginf(s)] = 0.0
     d[target == ignore] = 0.0
     return d

@@ -203,6 +203,29 @@ def test_nans_and_infinities_stay_in_their_rows(size, rows):
         assert bits(q.logp[[0]]) == bits(r.logp[[0]])
 
 
+@pytest.mark.parametrize("rows", [3, 600])
+@pytest.mark.parametrize("size", [1, 6, 2048, 3000, 70000])
+def test_rows_of_nans_and_nothing_that_can_come(size, rows):
+    """A NaN is in the gradient though no number is the row's largest."""
+    import torch
+    if rows * size > 10 ** 7:
+        rows = 100
+    for dtype in DTYPES:
+        x, rng = logits(rows, size, 11)
+        x[0] = np.nan
+        x[1] = -np.inf
+        x[1, -1] = np.nan
+        t, tt = lu.matrix(x, dtype), torch.zeros(rows, dtype=torch.int64, device="cuda")
+        q = G().token_log_probs_forward(t, tt, entropy=True, top=1)
+        one = torch.ones(rows, device="cuda")
+        for de in (None, one):
+            d = G().token_log_probs_backward(one, de, t, tt, q.stats, q.entropy if de is not None else None)
+            assert torch.isnan(d[:2]).all() and torch.isfinite(d[2:]).all()
+        for got in (q.logp, q.entropy, q.stats[:, 1], q.top_logp[:, 0]):
+            assert torch.isnan(got[:2]).all() and torch.isfinite(got[2:]).all()
+        assert q.top_ids[:2, 0].tolist() == [0, size - 1]
+
+
 @pytest.mark.parametrize("size", [40, 2048, 5000, 131072])
 def test_equal_logits_take_the_lowest_columns(size):
     """Rows of one value, of two, of halves of a step, in falling and rising
