@@ -34,18 +34,39 @@ struct RmsBwdArgs {
   Eight x8;                  // x8.at: in the place of x
   const float* rstd;
   uint64_t weight, dweight;
-  float* partials;  // [parts][size]: sums of dy * n
+  float* partials;  // [parts][part_columns(size)]: sums of dy * n
   float* sums;      // [rows], long rows: their means of dy * weight * n
   uint32_t rows, size;
   int32_t wdt, gdt, accumulate;
   uint32_t parts;
-  uint32_t row_groups;  // rows in registers: the workgroups that take rows
+  uint32_t row_groups, strips;  // rows in registers: workgroups that take rows, and before them the weight's gradient
   int32_t streamed;
 };
 
-// Rows in registers, and no more than so many: the weight's gradient is taken
-// by workgroups of its own.
-constexpr uint32_t kStripRows = 128;
+// A part's columns lie at whole units of 16 bytes.
+__host__ __device__ constexpr uint64_t part_columns(uint32_t size) { return ((uint64_t)size + 3) / 4 * 4; }
+
+// Few rows in registers: the weight's gradient is taken by workgroups of its
+// own, and leaves no parts.  Residual gradients with dropout, so and by parts:
+// 256 x 2048 in bfloat16 5.9 and 9.3 us, 512 x 2048 8.3 and 10.8, 1021 x 2048
+// 13.4 and 11.3; in binary32 256 x 8192 13.2 and 16.3, 512 x 4096 13.7 and
+// 13.9, 512 x 8192 20.5 and 19.4.
+constexpr uint32_t kStripRows = 256, kStripMoreRows = 512, kStripMoreMax = 4096;
+inline bool weight_by_strips(uint32_t rows, uint32_t size) {
+  return rows <= kStripRows || (rows <= kStripMoreRows && size <= kStripMoreMax);
+}
+
+// Gradients of rows in registers: the shapes of the layer norm's, and of
+// longer rows than those a workgroup of 1024 lanes.
+constexpr uint32_t kRmsBwdMax = 16384, kRmsBwdLanes = 1024;
+template <int DT>
+constexpr RowShape kRmsLongShapes[] = {{kRmsBwdLanes, 2}};
+template <>
+inline constexpr RowShape kRmsLongShapes<GCLIP_F32>[] = {{kRmsBwdLanes, 3}, {kRmsBwdLanes, 4}};
+template <int DT>
+inline uint32_t rms_bwd_parts(uint32_t rows, uint32_t size) {
+  return size <= kBwdMax ? bwd_parts<DT>(rows, size) : rows < kBwdParts ? rows : kBwdParts;
+}
 
 struct ActArgs {
   Rows gate, up, y, dy, dgate, dup;  // up.at, y.at 0: none

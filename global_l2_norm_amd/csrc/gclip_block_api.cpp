@@ -26,12 +26,12 @@ bool dropout_of(const gclip_dropout* d, DropArgs* out, bool* any) {
   return true;
 }
 
-int64_t part_floats(int64_t rows, int64_t size) { return (int64_t)rms_parts(rows, size) * size; }
+int64_t part_floats(int64_t rows, int64_t size) { return (int64_t)rms_parts(rows, size) * (int64_t)part_columns((uint32_t)size); }
 // The long rows' means follow the partial sums.  Few rows in registers leave
 // none.
 int64_t workspace_bytes(int64_t rows, int64_t size) {
-  if (in_registers((uint32_t)size, kBwdMax) && rows <= kStripRows) return 0;
-  return 4 * (part_floats(rows, size) + (size > kBwdMax ? rows : 0));
+  if (in_registers((uint32_t)size, kRmsBwdMax) && weight_by_strips((uint32_t)rows, (uint32_t)size)) return 0;
+  return 4 * (part_floats(rows, size) + (size > kRmsBwdMax ? rows : 0));
 }
 
 gclip_status forward(const gclip_rms_forward* a, bool residual, const gclip_dropout* drop, void* stream) {
@@ -98,7 +98,7 @@ gclip_status backward(const gclip_rms_backward* a, bool residual, const gclip_dr
                      address_of(a->weight), address_of(a->dweight), static_cast<float*>(a->workspace),
                      static_cast<float*>(a->workspace) + part_floats(a->rows, a->size), (uint32_t)a->rows,
                      (uint32_t)a->size, a->weight_dtype, a->grad_dtype, a->accumulate ? 1 : 0,
-                     rms_parts(a->rows, a->size), 0, streams(a->rows, a->size, moved)};
+                     rms_parts(a->rows, a->size), 0, 0, streams(a->rows, a->size, moved)};
   return launched(launch_rms_backward(k, a->dtype, residual, two ? &d : nullptr, static_cast<hipStream_t>(stream)));
 }
 

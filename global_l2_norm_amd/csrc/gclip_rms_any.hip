@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_grad_long(RmsBwdArgs a, Dr
     float t = red[0][i];
 #pragma unroll
     for (int k = 1; k < kLongWaves; ++k) t += red[k][i];
-    if (col < a.size) a.partials[(uint64_t)blockIdx.z * a.size + col] = t;
+    if (col < a.size) a.partials[blockIdx.z * part_columns(a.size) + col] = t;
   }
 }
 
@@ -384,7 +384,7 @@ __global__ __launch_bounds__(kShortThreads) void k_rms_grad_short(RmsBwdArgs a, 
     float t = red[0][threadIdx.x];
 #pragma unroll
     for (int i = 1; i < kShortThreads / 64; ++i) t += red[i][threadIdx.x];
-    a.partials[(uint64_t)blockIdx.x * a.size + threadIdx.x] = t;
+    a.partials[blockIdx.x * part_columns(a.size) + threadIdx.x] = t;
   }
 }
 
@@ -439,7 +439,7 @@ hipError_t forward(const RmsFwdArgs& a, bool residual, const DropArgs* drop, hip
 
 template <int DT>
 hipError_t backward(const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  if (a.rows == 0 || !in_registers(a.size, kBwdMax)) return backward_any<DT>(a, residual, drop, st);
+  if (a.rows == 0 || !in_registers(a.size, kRmsBwdMax)) return backward_any<DT>(a, residual, drop, st);
   return a.x8.at ? rms_backward_rows<DT, true>(a, residual, drop, st) : rms_backward_rows<DT, false>(a, residual, drop, st);
 }
 
@@ -451,7 +451,7 @@ hipError_t backward(const RmsBwdArgs& a, bool residual, const DropArgs* drop, hi
 uint32_t rms_parts(int64_t rows, int64_t size) {
   if (rows == 0) return 0;
   const uint32_t n = (uint32_t)rows, c = (uint32_t)size;
-  if (in_registers(c, kBwdMax)) return std::max(bwd_parts<GCLIP_F32>(n, c), bwd_parts<GCLIP_BF16>(n, c));
+  if (in_registers(c, kRmsBwdMax)) return std::max(rms_bwd_parts<GCLIP_F32>(n, c), rms_bwd_parts<GCLIP_BF16>(n, c));
   if (c < kRegistersMin) return std::min<uint32_t>((n - 1) / (4 * kShortThreads) + 1, kBwdParts);
   const uint32_t strips = (c - 1) / 512 + 1;
   return std::min<uint32_t>({std::max<uint32_t>(kLongStrips / strips, 1), (n - 1) / (2 * kLongWaves) + 1, kBwdParts});

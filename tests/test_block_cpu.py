@@ -241,10 +241,11 @@ def test_calls_without_rows_do_nothing():
 
 def test_workspaces():
     assert L.gclip_rms_workspace(-1, 8) == 0 and L.gclip_rms_workspace(8, 0) == 0
-    for rows in (0, 1, 17, 4096, MOST):
+    assert L.gclip_rms_workspace(512, 4096) == 0 < L.gclip_rms_workspace(513, 4096) and L.gclip_rms_workspace(512, 4097) > 0
+    for rows in (0, 1, 17, 256, 4096, MOST):
         for size in (1, 7, 768, 16384, 1 << 22, MOST):
             n = L.gclip_rms_workspace(rows, size)
-            if rows == 0 or (rows <= 128 and 8 <= size <= 8192):  # few rows in registers leave no parts
+            if rows == 0 or (rows <= 256 and 8 <= size <= 16384):  # few rows in registers leave no parts
                 assert n == 0
             else:
                 assert 4 * size <= n <= max(4 * size, 32 << 20) + 4 * rows

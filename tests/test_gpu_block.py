@@ -172,7 +172,9 @@ def test_rms_every_number_of_rows(rows, size, dtype):
     run_rms(rows, size, dtype, "f32", "plain" if rows % 2 else "padded", seed=1)
 
 
-@pytest.mark.parametrize("rows,size", [(100, 768), (128, 130), (128, 4097), (129, 4097), (127, 8193), (129, 40), (2, 8193)])
+@pytest.mark.parametrize("rows,size", [(100, 768), (128, 130), (128, 4097), (129, 4097), (127, 8193), (129, 40), (2, 8193),
+                                       (256, 16384), (257, 16384), (512, 4096), (513, 4096), (512, 4097), (300, 12289),
+                                       (256, 8193), (600, 8200)])
 def test_rms_weight_gradients_of_few_rows(rows, size):
     """As many rows as one launch serves, and one more."""
     for dtype, wt in (("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")):
@@ -190,7 +192,8 @@ def test_rms_shapes_of_many_rows(shape, dtype):
 
 
 @pytest.mark.parametrize("rows,size,dtype", [(13000, 1537, "f32"), (300001, 64, "bf16"), (2300, 8192, "f32"),
-                                             (9001, 2048, "f16"), (40000, 768, "bf16")])
+                                             (9001, 2048, "f16"), (40000, 768, "bf16"),
+                                             (1200, 16383, "bf16"), (1000, 12000, "f32")])
 def test_rms_streamed(rows, size, dtype):
     run_rms(rows, size, dtype, "f32", seed=3, forms=(None, "row"))
 
@@ -303,7 +306,8 @@ def test_rms_in_place_and_between_guards(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,size", [(9, 768), (128, 768), (100, 8200), (128, 2047), (129, 2047), (128, 16384), (70, 20000)])
+@pytest.mark.parametrize("rows,size", [(9, 768), (128, 768), (100, 8200), (128, 2047), (129, 2047), (128, 16384), (70, 20000),
+                                       (256, 2048), (512, 4095), (257, 8200), (256, 12289)])
 def test_rms_gradients_in_place_of_few_rows(rows, size, dtype):
     """The weight's gradient reads dy and x of all rows, which the rows' own
     results may be written over."""
