@@ -56,16 +56,23 @@ inline bool weight_by_strips(uint32_t rows, uint32_t size) {
   return rows <= kStripRows || (rows <= kStripMoreRows && size <= kStripMoreMax);
 }
 
-// Gradients of rows in registers: the shapes of the layer norm's, and of
-// longer rows than those a workgroup of 1024 lanes.
+// Gradients of rows in registers: the shapes of the layer norm's for shorter
+// rows, and for longer ones 1024 lanes, a workgroup, each.  By them and by
+// the other shapes: 2048 x 8192 norms with a checkpoint in bfloat16 21.0 and
+// 22.6 us, in binary32 30.3 and 33.7, 4000 x 4100 30.4 and 34.3; but 4000 x
+// 4100 residual gradients with dropout in bfloat16, which leave half of the
+// lanes idle, 47.3 and 39.4.  2048 x 16384 in bfloat16 44.9 us in one pass,
+// 64.6 in two; with residual and dropout 78 and 87, in binary32 147 and 167.
 constexpr uint32_t kRmsBwdMax = 16384, kRmsBwdLanes = 1024;
 template <int DT>
-constexpr RowShape kRmsLongShapes[] = {{kRmsBwdLanes, 2}};
+constexpr uint32_t kRmsShortMax = DT == GCLIP_F32 ? 4096 : 6144;
+template <int DT>
+constexpr RowShape kRmsLongShapes[] = {{kRmsBwdLanes, 1}, {kRmsBwdLanes, 2}};
 template <>
-inline constexpr RowShape kRmsLongShapes<GCLIP_F32>[] = {{kRmsBwdLanes, 3}, {kRmsBwdLanes, 4}};
+inline constexpr RowShape kRmsLongShapes<GCLIP_F32>[] = {{kRmsBwdLanes, 2}, {kRmsBwdLanes, 3}, {kRmsBwdLanes, 4}};
 template <int DT>
 inline uint32_t rms_bwd_parts(uint32_t rows, uint32_t size) {
-  return size <= kBwdMax ? bwd_parts<DT>(rows, size) : rows < kBwdParts ? rows : kBwdParts;
+  return size <= kRmsShortMax<DT> ? bwd_parts<DT>(rows, size) : rows < kBwdParts ? rows : kBwdParts;
 }
 
 struct ActArgs {

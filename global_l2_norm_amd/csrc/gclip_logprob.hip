@@ -715,7 +715,7 @@ LogpCut logp_cut(uint32_t rows, uint32_t size, int32_t dtype) {
   if (rows >= kLogpManyRows && units <= kLogpNarrow * kLogpNarrowTurns)
     return LogpCut{1, (units - 1) / kLogpNarrow + 1, kLogpNarrow};
   if (rows > kLogpFewRows) return LogpCut{1, most, kLogpThreads};
-  if (units <= kLogpWide * kLogpTurns) return LogpCut{1, (units - 1) / kLogpWide + 1, kLogpWide};
+  if (units <= kLogpWide * std::max(kLogpTurns, rows / kLogpRowsATurn)) return LogpCut{1, (units - 1) / kLogpWide + 1, kLogpWide};
   const uint32_t wanted = std::min(kLogpSegments, 4 * kLogpFewRows / std::max(rows, 1u));
   const uint32_t turns = (most - 1) / wanted + 1;
   return LogpCut{(most - 1) / turns + 1, turns, kLogpThreads};

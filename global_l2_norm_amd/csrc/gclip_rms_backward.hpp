@@ -105,9 +105,10 @@ __global__ __launch_bounds__(rms_bwd_threads<LANES>(NV * kUnit<DT>)) void k_rms_
   constexpr uint32_t kRows = kBwdThreads / LANES;  // of a workgroup at a time
   constexpr uint32_t kCols = LANES * NV * kUnit<DT>;
   constexpr uint32_t kMeet = LANES < 64 ? kBwdThreads / 64 : kRows;  // sums of a column that meet
-  // a workgroup a row: its registers do not hold the weight (nor in binary32
-  // dh under way) besides
-  constexpr bool kLate = LANES == (int)kRmsBwdLanes && DT == GCLIP_F32, kAside = LANES == (int)kRmsBwdLanes;
+  // More than eight columns for each of 1024 lanes: their registers do not hold
+  // the weight and the columns' sums besides, which lie in shared memory, nor
+  // in binary32 the next row's dh.
+  constexpr bool kAside = LANES == (int)kRmsBwdLanes && NV * kUnit<DT> > 8, kLate = kAside && DT == GCLIP_F32;
   constexpr int kFours = NV * (int)kUnit<DT> / 4;
   __shared__ f32x4 aside[kAside ? 2 : 1][kAside ? kFours * LANES : 1];
   __shared__ float red[2][kBwdThreads / 64];
@@ -372,10 +373,10 @@ hipError_t rms_backward_shape(RmsBwdArgs a, bool residual, const DropArgs* drop,
 
 template <int DT, bool EIGHT, int I = 0>
 hipError_t rms_backward_of(int shape, const RmsBwdArgs& a, bool residual, const DropArgs* drop, hipStream_t st) {
-  if constexpr (I + 1 < (int)(sizeof(kBwdShapes<DT>) / sizeof(RowShape))) {
+  constexpr RowShape s = kBwdShapes<DT>[I];
+  if constexpr (s.lanes * s.units * kUnit<DT> < kRmsShortMax<DT>) {
     if (shape != I) return rms_backward_of<DT, EIGHT, I + 1>(shape, a, residual, drop, st);
   }
-  constexpr RowShape s = kBwdShapes<DT>[I];
   constexpr int sure = sure_units(kBwdShapes<DT>, I);
   return a.streamed ? rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, true>(a, residual, drop, st)
                     : rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, false>(a, residual, drop, st);
@@ -396,7 +397,7 @@ hipError_t rms_backward_long(int shape, const RmsBwdArgs& a, bool residual, cons
     if (shape != I) return rms_backward_long<DT, EIGHT, I + 1>(shape, a, residual, drop, st);
   }
   constexpr RowShape s = kRmsLongShapes<DT>[I];
-  constexpr int sure = I > 0 ? sure_units(kRmsLongShapes<DT>, I) : kBwdMax / kUnit<DT> / s.lanes;
+  constexpr int sure = I > 0 ? sure_units(kRmsLongShapes<DT>, I) : kRmsShortMax<DT> / kUnit<DT> / s.lanes;
   return a.streamed ? rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, true>(a, residual, drop, st)
                     : rms_backward_shape<DT, EIGHT, s.lanes, s.units, sure, false>(a, residual, drop, st);
 }
@@ -407,7 +408,7 @@ hipError_t rms_backward_rows(const RmsBwdArgs& a, bool residual, const DropArgs*
     if (few_bwd<DT>(a.rows, a.size))
       return rms_backward_few<DT, EIGHT>(row_shape_of(kFewBwdShapes, kUnit<DT>, a.size), a, residual, drop, st);
   }
-  if (a.size > kBwdMax)
+  if (a.size > kRmsShortMax<DT>)
     return rms_backward_long<DT, EIGHT>(row_shape_of(kRmsLongShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
   return rms_backward_of<DT, EIGHT>(row_shape_of(kBwdShapes<DT>, kUnit<DT>, a.size), a, residual, drop, st);
 }

@@ -128,6 +128,22 @@ def test_many_rows_by_a_wave_each(rows, size, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,size", [(63, 65536), (64, 65537), (96, 90001), (128, 131072), (128, 131080), (255, 50304),
+                                       (256, 131072), (257, 40000), (200, 200001)])
+def test_few_long_rows(rows, size, dtype):
+    """A workgroup a row, of more turns with more rows, and in segments."""
+    x, rng = logits(rows, size, 12)
+    targets = rng.integers(0, size, rows)
+    targets[::9] = -100
+    x[1, 5:] = -np.inf
+    x[2, :] = -np.inf
+    targets[1], targets[2] = 3, 0
+    layout = "plain" if rows % 2 else "padded"
+    check(x, targets, 20, dtype, f"{rows} x {size} {dtype} top", layout, gradient=False)
+    check(x, targets, 0, dtype, f"{rows} x {size} {dtype}", layout, entropy=False, gradient=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_rows_by_a_wave_each_streamed(dtype):
     x, rng = logits(4500 if dtype == "f32" else 9001, 8449, 9)
     check(x, rng.integers(0, 8449, len(x)), 3, dtype, f"streamed by waves {dtype}", gradient=False)
