@@ -49,8 +49,8 @@ __device__ __forceinline__ float activated(float x, float& slope) {
   } else if constexpr (KIND == GCLIP_ACT_GELU) {
     // h = erfc(z) / 2 of z = |x| / sqrt(2) as e^(-z^2) t P(t), t = 1 / (1 + 0.3 z):
     // P of degree 8 fitted to e^(z^2) erfc(z) / (2 t) for z up to 10, 2.0e-8 off
-    // at most, relative.  The power serves the derivative too.  The library's
-    // erfc took 1.5 times as long as the memory: 2047 x 1367 in binary32 8.9 us.
+    // at most, relative.  The power serves the derivative too.  2047 x 1367 in
+    // binary32, kept, 7.4 us, and 8.6 with the library's erfc and exponential.
     const float e = exponential<DT>(-0.5f * x * x), t = reciprocal<DT>(__builtin_fmaf(fabsf(x), 0.212132034355964f, 1.0f));
     float h = -0.06476137042f;
     h = __builtin_fmaf(h, t, 0.24278119206f);
@@ -79,7 +79,8 @@ __device__ __forceinline__ float activated(float x, float& slope) {
 }
 
 // y = act(gate) up, a unit of 16 bytes a lane; with KEEP the lanes of a block
-// also share their scale and leave gate and up in 8 bits.
+// also share their scale and leave gate and up in 8 bits.  Bound by memory:
+// 16384 x 5504 bfloat16 silu, gated and kept, 117 us, 727 MB at 6.2 TB/s.
 template <int DT, int KIND, bool GATED, bool KEEP, bool STREAMED>
 __global__ __launch_bounds__(kActThreads) void k_activation(ActArgs a, Split split) {
   constexpr uint32_t kU = kUnit<DT>;
@@ -117,6 +118,8 @@ __global__ __launch_bounds__(kActThreads) void k_activation(ActArgs a, Split spl
 }
 
 // dgate = dy up act'(gate), dup = dy act(gate), and y again where wanted.
+// Bound by memory: 16384 x 5504 in bfloat16 from 8 bits, y too, 145 us, 907 MB
+// at 6.3 TB/s.
 template <int DT, int KIND, bool GATED, bool EIGHT, bool STREAMED>
 __global__ __launch_bounds__(kActThreads) void k_activation_grad(ActArgs a, Split split) {
   constexpr uint32_t kU = kUnit<DT>;

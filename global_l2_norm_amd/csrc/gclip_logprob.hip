@@ -220,8 +220,14 @@ __device__ __forceinline__ void logits_settled(u32x4 q, uint32_t u, uint32_t siz
 // lane has seen as its largest logit then chooses the few lanes that can hold
 // one of the likeliest, and those read theirs again, from the caches: the k-th
 // largest logit is at least the k-th largest of any wave's lanes' largest, and
-// at least what, in every wave, k / waves of those reach.  Rows of so many equal logits that the candidates do not fit, and those with
-// NaNs or infinities, are searched k times instead.
+// at least what, in every wave, k / waves of those reach.  Rows of so many equal
+// logits that the candidates do not fit, and those with NaNs or infinities, are
+// searched k times instead.
+//
+// Long rows of 16-bit logits are bound by the exponentials: 4096 x 50304 with
+// entropies 69.6 us, 412 MB at 5.9 TB/s with the vector units full; 8192 x 8449
+// in binary32 by memory, 49.4 us, 277 MB at 5.6 TB/s.  Few rows by latency: 8 x
+// 131072 in segments 8.0 us with 20 alternatives and 5.8 for the join.
 template <int DT, int THREADS, bool ENTROPY, bool TOP, bool STREAMED>
 __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
   constexpr uint32_t kU = kUnit<DT>;
@@ -394,14 +400,15 @@ __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
 // its largest and its sums are taken from there.  The likeliest: those logits
 // that reach the k-th largest of the lanes' largest, found and ordered within
 // the wave; rows with NaNs or infinities, and those whose candidates do not
-// fit, are searched k times.
+// fit, are searched k times.  Bound by the vector units: 59629 x 382 in
+// bfloat16 14.4 us, 45 MB; 28860 x 186 with 20 alternatives 23.8 us, which
+// were 137 by k_logp's way.
 constexpr uint32_t kRowCandidates = 128;
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
 
-//
 // Many rows have fewer lanes each, for what each row costs whatever its
 // length: 59629 x 382 bfloat16 15.2 us by 16 lanes and 23.0 by 64.
 constexpr uint32_t kManyShort = 8192;
@@ -605,6 +612,8 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
 // of 16 bytes a lane over all rows, whose numbers come from the caches.  A
 // workgroup for four units a thread of one row loses what its last one does
 // not fill: 7544 x 11328 bfloat16 68 us (63), 8192 x 8449 binary32 97 (91).
+// Bound by memory: 8192 x 8449 binary32 with entropies 92.8 us, 554 MB at 6.0
+// TB/s; 4096 x 50304 bfloat16 133 us, 824 MB at 6.2.
 template <int DT, bool ENTROPY, bool STREAMED>
 __global__ __launch_bounds__(kLogpThreads) void k_logp_grad(LogpArgs a, Split split) {
   constexpr uint32_t kU = kUnit<DT>;

@@ -8,7 +8,9 @@ namespace {
 
 constexpr int kPackThreads = 256;
 
-// A scale a block: its lanes hold a unit each and share it.
+// A scale a block: its lanes hold a unit each and share it.  Bound by memory:
+// 16384 x 2048 in bfloat16 18.1 us, 102 MB at 5.6 TB/s (a copy of 100 MB: 5.6);
+// out of 8 bits 15.8 us, 6.5 TB/s.
 template <int DT, bool STREAMED>
 __global__ __launch_bounds__(kPackThreads) void k_pack8(Rows x, Eight out, uint32_t rows, uint32_t size, Split split) {
   constexpr uint32_t kU = kUnit<DT>;

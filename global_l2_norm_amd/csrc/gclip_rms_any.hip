@@ -66,7 +66,8 @@ __device__ __forceinline__ void store_eight_block(const Eight& e, uint64_t r, ui
 // Two passes over a row, h and the squares, then y, which finds the row in the
 // caches; y in 8 bits with a scale a row takes one more between them.  A
 // thread reads there only the groups that it wrote itself.  The sums are
-// binary64, so no finite row overflows them.  Bound by the passes' latency.
+// binary64, so no finite row overflows them.  Bound by the passes' latency:
+// 1000 x 40000 residual steps in bfloat16 77 us, 320 MB at 4.2 TB/s.
 template <int DT, bool RES, bool DROP>
 __global__ __launch_bounds__(kLongThreads) void k_rms_long(RmsFwdArgs a, DropArgs d) {
   __shared__ double red[kLongWaves];
@@ -136,7 +137,9 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(RmsFwdArgs a, DropArg
 // registers and more.  The first leaves a row's mean; the second takes strips
 // of columns down many rows, whose sums stay in registers, and reads the
 // matrices again, mostly from the cache before memory.  Workgroups of the
-// second: kLongStrips, two for each compute unit.
+// second: kLongStrips, two for each compute unit.  1000 x 40000 residual
+// gradients in bfloat16 41.9 and 48.4 us, and 4.8 for the join: 400 MB at 4.2
+// TB/s, of which 320 would do.
 constexpr uint32_t kLongStrips = 512;
 
 // The eight values of group g of what was normed, zeros past the row's end.

@@ -31,7 +31,8 @@
  *     column gives NaN for logp, and a gradient of NaN.
  *   - Sums are binary32, of at most 32 terms in a lane and then of those,
  *     relative to the largest logit so far; a row's results are taken from
- *     them in binary64 and rounded once.
+ *     them in binary64 and rounded once, those of rows of up to 2048 logits in
+ *     binary32.
  */
 #ifndef GCLIP_LOGPROB_H
 #define GCLIP_LOGPROB_H

@@ -258,6 +258,24 @@ def test_workspaces():
                 assert 0 <= n <= 512 * 64 * (8 * top + 16) and (n == 0 or rows <= 256)
 
 
+def test_the_profile_summary_is_of_the_present_kernels():
+    """profiles/block__trace_pmc.txt names the code it was taken on, without
+    its comments."""
+    import hashlib
+    import os
+    import re
+
+    import bench
+    csrc = os.path.join(bench.ROOT, "global_l2_norm_amd", "csrc")
+    h = hashlib.sha256()
+    for f in sorted(os.listdir(csrc)):
+        if re.match("gclip_(block|rms|activation|pack8|operand|logprob)", f):
+            with open(os.path.join(csrc, f), encoding="utf-8") as src:
+                h.update(bench._code_only(src.read()).encode())
+    with open(os.path.join(bench.PROFILES, "block__trace_pmc.txt")) as f:
+        assert re.search(r"^kernel_source_sha256_16: (\w+)$", f.read(), re.M)[1] == h.hexdigest()[:16]
+
+
 def test_overlaps_of_8_bit_rows_against_every_byte():
     """unpack between values and a matrix: refused when any byte is shared,
     those behind a row's end up to a multiple of eight among the values', or

@@ -189,3 +189,25 @@ def test_the_examples_gradients():
     for i, (a, b) in enumerate(zip(model.params, p)):
         off = (a.grad.double().cpu() - b.grad).norm() / b.grad.norm()
         assert off <= 8e-3, (i, float(off))
+
+
+def test_the_readme_runs():
+    """README.md's example of these operators."""
+    import os
+    import re
+
+    import torch
+
+    import global_l2_norm_amd as g
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        block, = (b for b in re.findall(r"```python\n(.*?)```", f.read(), re.S) if "residual_rms_norm" in b)
+    torch.manual_seed(3)
+    make = lambda *n: torch.randn(*n, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    env = dict(G=g, x=make(20, 64).requires_grad_(), residual=make(20, 64), weight=make(64), w_gate=make(96, 64),
+               w_up=make(96, 64), logits=make(20, 1000).requires_grad_(), targets=torch.arange(20, device="cuda"),
+               mask=g.DropoutMask(0.1, 1))
+    exec(block, env)
+    (env["loss"] + env["r"].entropy.sum() + env["z"].float().sum()).backward()
+    assert torch.isfinite(env["x"].grad).all() and torch.isfinite(env["logits"].grad).all()
+    assert torch.equal(env["logits"].gather(1, env["best"].top_ids), env["logits"].topk(20, dim=1).values)
+    assert env["y8"].values.dtype == torch.float8_e4m3fn and env["y8"].scales.shape == (20, 1)
