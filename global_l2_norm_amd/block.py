@@ -308,8 +308,8 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
         rstd = _empty(*lead, dtype=_F32, device=x.device) if lead else _empty((), dtype=_F32, device=x.device)
         rp = rstd.data_ptr()
     if residual is None:
-        gclip_rmsnorm_forward(_pack_forward(rows, size, code, wdt, eps, x.data_ptr(), ld, 0, 0, wp, 0, 0, yp, ldy, *y8,
-                                            *k8, rp), _raw_stream(device))
+        gclip_rmsnorm_forward(_pack_forward(rows, size, code, wdt, float(eps), x.data_ptr(), ld, 0, 0, wp, 0, 0, yp, ldy,
+                                            *y8, *k8, rp), _raw_stream(device))
         return None, y, rstd, kept
     ldr = _like(residual, x, "residual")
     if h is None:
@@ -317,8 +317,8 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
         ldh = size
     else:
         ldh = _like(h, x, "out_h")
-    gclip_residual_rms_forward(_pack_forward(rows, size, code, wdt, eps, x.data_ptr(), ld, residual.data_ptr(), ldr, wp,
-                                             h.data_ptr(), ldh, yp, ldy, *y8, *k8, rp),
+    gclip_residual_rms_forward(_pack_forward(rows, size, code, wdt, float(eps), x.data_ptr(), ld, residual.data_ptr(), ldr,
+                                             wp, h.data_ptr(), ldh, yp, ldy, *y8, *k8, rp),
                                _counted(mask, device) if mask is not None and mask.drops else None,
                                _raw_stream(device))
     return h, y, rstd, kept

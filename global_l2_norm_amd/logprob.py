@@ -6,6 +6,7 @@ backward pass starts from, and what a server answers with.
 ``token_log_probs`` is the same under autograd, in its backward mode.
 Matrices, streams, captures and refusals are those of ``layers``.
 """
+from operator import index
 from typing import NamedTuple
 
 try:
@@ -62,6 +63,13 @@ def _targets(t, rows, x):
     return t.data_ptr()
 
 
+def _ignored(i):
+    i = index(i)
+    if not -1 << 63 <= i < 1 << 63:
+        raise ValueError(f"ignore_index must be an int64, not {i}")
+    return i
+
+
 def _numbers(t, rows, x, name):
     if t.dtype != _F32:
         raise TypeError(f"{name} must be float32, not {t.dtype}")
@@ -100,8 +108,8 @@ def _forward(logits, targets, entropy, top, ignore, stats):
     nbytes = gclip_logprob_workspace(rows, size, top)
     workspace = _empty(nbytes, dtype=torch.uint8, device=on) if nbytes else None
     at = lambda t: t.data_ptr() if t is not None else 0  # noqa: E731
-    gclip_logprob_forward(_pack(rows, size, code, top, logits.data_ptr(), ld, tp, ignore, at(stats), at(logp), at(h),
-                                at(top_logp), at(top_ids), 0, 0, 0, 0, at(workspace), nbytes), _raw_stream(device))
+    gclip_logprob_forward(_pack(rows, size, code, top, logits.data_ptr(), ld, tp, _ignored(ignore), at(stats), at(logp),
+                                at(h), at(top_logp), at(top_ids), 0, 0, 0, 0, at(workspace), nbytes), _raw_stream(device))
     return TokenLogProbs(logp, h, stats, top_logp, top_ids)
 
 
@@ -130,8 +138,8 @@ def _backward(dlogp, dentropy, logits, targets, stats, entropy, ignore, out):
         ldo = size
     else:
         ldo = _like(out, logits, "out")
-    gclip_logprob_backward(_pack(rows, size, code, 0, logits.data_ptr(), ld, tp, ignore, sp, 0, hp, 0, 0, dp, ep,
-                                 out.data_ptr(), ldo, 0, 0), _raw_stream(device))
+    gclip_logprob_backward(_pack(rows, size, code, 0, logits.data_ptr(), ld, tp, _ignored(ignore), sp, 0, hp, 0, 0, dp,
+                                 ep, out.data_ptr(), ldo, 0, 0), _raw_stream(device))
     return out
 
 

@@ -313,6 +313,21 @@ def test_refusals():
     assert g.token_log_probs_backward(one[:0], one[:0], x[:0], t[:0], none.stats, none.entropy).shape == (0, 50)
 
 
+def test_numbers_that_are_none_are_refused():
+    import torch
+    g, x, t = G(), torch.zeros(4, 8, device="cuda"), torch.zeros(4, dtype=torch.int64, device="cuda")
+    for bad, error in ((1.0, TypeError), ("1", TypeError), (1 << 63, ValueError), (-(1 << 63) - 1, ValueError)):
+        with pytest.raises(error):
+            g.token_log_probs_forward(x, t, ignore_index=bad)
+    r = g.token_log_probs_forward(x, t, ignore_index=-(1 << 63))
+    for bad, error in ((1.0, TypeError), (1 << 63, ValueError)):
+        with pytest.raises(error):
+            g.token_log_probs_backward(r.logp, None, x, t, r.stats, ignore_index=bad)
+    for bad, error in ((None, TypeError), ("x", ValueError), (0, g.GclipError)):
+        with pytest.raises(error):
+            g.rms_norm_forward(x, eps=bad)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_in_place_and_between_guards(dtype):
     import torch
