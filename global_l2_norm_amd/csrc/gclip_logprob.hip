@@ -181,6 +181,16 @@ struct Top {
   uint32_t n, chosen_n;
 };
 
+// One more candidate, if there is room for it; n counts it either way.  The
+// only store to candidate[]: others of the workgroup may have filled it.
+template <int THREADS>
+__device__ __forceinline__ bool offer(Top<THREADS>& w, uint64_t key) {
+  const uint32_t at = atomicAdd(&w.n, 1u);
+  if (at >= kCandidates) return false;
+  w.candidate[at] = key;
+  return true;
+}
+
 // best[] from the candidates, n of them at most kCandidates: a candidate's
 // place is the number of larger ones.
 template <int THREADS>
@@ -329,7 +339,7 @@ __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
       const uint64_t begin = (uint64_t)seg * a.turns * (uint32_t)THREADS * kU + tid;
       if (scarce && tid < a.top && begin < a.size) {
         const float v = elem_float<DT>(load_elem<DT>(row + begin * kElem<DT>));
-        if (v == kNone) top.candidate[atomicAdd(&top.n, 1u)] = key_of(v, (uint32_t)begin);
+        if (v == kNone) room = offer(top, key_of(v, (uint32_t)begin));
       }
       for (uint32_t i = tid; room && i < items; i += (uint32_t)THREADS) {
         const uint32_t u = seg * (a.turns * (uint32_t)THREADS) + top.chosen[i / a.turns] + i % a.turns * (uint32_t)THREADS;
@@ -339,11 +349,7 @@ __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
         logits_settled<DT>(logits_raw<DT, false>(row, u, a.size), u, a.size, v);
 #pragma unroll
         for (uint32_t j = 0; j < kU; ++j) {
-          if (c + j < a.size && ordered(v[j]) >= least) {
-            const uint32_t at = atomicAdd(&top.n, 1u);
-            if (at < kCandidates) top.candidate[at] = key_of(v[j], (uint32_t)c + j);
-            else room = false;
-          }
+          if (c + j < a.size && ordered(v[j]) >= least) room &= offer(top, key_of(v[j], (uint32_t)c + j));
         }
       }
       __syncthreads();
@@ -596,7 +602,7 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
     const uint64_t least = top.largest[0];
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
-      if (own[i] != 0 && own[i] >= least) top.candidate[atomicAdd(&top.n, 1u)] = own[i];
+      if (own[i] != 0 && own[i] >= least) offer(top, own[i]);  // all have room
     __syncthreads();
     rank_candidates(top, top.n, a.top);
     __syncthreads();

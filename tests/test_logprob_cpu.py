@@ -1,0 +1,38 @@
+"""Log probabilities without a GPU: how the sources store a candidate, and that
+the inputs of tests/test_gpu_logprob_edges.py reach the ways that they are
+for."""
+import os
+import re
+
+import numpy as np
+import pytest
+
+from tests import logprob_util as lp
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "global_l2_norm_amd", "csrc")
+
+
+def test_every_store_of_a_candidate_is_bounded():
+    """More of a row's logits than there is room for may reach the threshold,
+    in whatever order the waves come."""
+    with open(os.path.join(CSRC, "gclip_logprob.hip"), encoding="utf-8") as f:
+        code = f.read()
+    stores = [m.start() for m in re.finditer(r"candidate\[[^;]*\]\s*=[^=]", code)]
+    assert len(stores) == 1
+    assert re.search(r"if \(at >= kCandidates\) return false;\s*\S*$", code[:stores[0]])
+    assert f"kCandidates = {lp.CANDIDATES};" in code
+
+
+@pytest.mark.parametrize("rows,size,dtype", [c[:3] for c in lp.CROWDED])
+def test_crowded_rows_pass_the_room_from_other_waves(rows, size, dtype):
+    """Rows of which little can come in few lanes, and much in those."""
+    segments, turns, threads = lp.cut(rows, size, dtype)
+    assert (segments, threads) == next(c[3:] for c in lp.CROWDED if c[:3] == (rows, size, dtype))
+    x = lp.crowded(rows, size, dtype)
+    columns = turns * threads * lp.UNIT[dtype]
+    for row in x[:2]:
+        scarce, n, elsewhere, nothing = lp.candidates(row[:columns], 20, dtype, turns, threads)
+        assert scarce and nothing > 0 and (elsewhere > lp.CANDIDATES if threads > 64 else n > lp.CANDIDATES)
+    # the last two: as much as there is room for, but for one and with one more
+    got = [lp.candidates(row[:columns], 20, dtype, turns, threads) for row in x[2:]]
+    assert all(g[0] for g in got) and [g[1] + g[3] for g in got] == [lp.CANDIDATES, lp.CANDIDATES + 1]
