@@ -429,10 +429,23 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_rows(LogpArgs a) {
   [[maybe_unused]] __shared__ uint64_t lists[kLogpThreads / 64][kRowCandidates];
   const uint64_t at = workgroup_of_grid() * (kLogpThreads / LANES) + threadIdx.x / LANES;
   if (LANES == 64 && at >= a.rows) return;
-  const uint32_t r = (uint32_t)(at < a.rows ? at : a.rows - 1), lane = threadIdx.x % LANES;
+  const uint32_t lane = threadIdx.x % LANES;
+  uint32_t r = (uint32_t)(at < a.rows ? at : a.rows - 1);
+  if constexpr (LANES == 64) r = __builtin_amdgcn_readfirstlane(r);
   const int64_t target = a.targets ? a.targets[r] : 0;
   const bool ignored = a.targets && target == a.ignore, column = a.logp && target >= 0 && target < (int64_t)a.size;
   const uint64_t row = a.x.at + r * a.x.ld;
+  // A row that counts for nothing is not read, where it has a wave to itself:
+  // 8192 x 2048 bfloat16 10.3 us where all rows count, 8.7 where half do, and
+  // 10.2 with the target looked at behind the loads.
+  if (LANES == 64 && ignored) {
+    if (lane == 0) store_nothing<ENTROPY>(a, r);
+    if (TOP && lane < a.top) {
+      a.top_logp[(uint64_t)r * a.top + lane] = kNone;
+      a.top_ids[(uint64_t)r * a.top + lane] = -1;
+    }
+    return;
+  }
   float given = 0.0f;
   if (column && !ignored && lane == 0) given = elem_float<DT>(load_elem<DT>(row + (uint64_t)target * kElem<DT>));
   u32x4 q[NV];
@@ -445,14 +458,6 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_rows(LogpArgs a) {
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) q[k] = logits_raw<DT, false>(row, lane + k * LANES, a.size);
-  }
-  if (LANES == 64 && ignored) {
-    if (lane == 0) store_nothing<ENTROPY>(a, r);
-    if (TOP && lane < a.top) {
-      a.top_logp[(uint64_t)r * a.top + lane] = kNone;
-      a.top_ids[(uint64_t)r * a.top + lane] = -1;
-    }
-    return;
   }
   float m = kNone;
   if constexpr (SCATTERED) {
@@ -620,6 +625,9 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_join(LogpArgs a) {
 // not fill: 7544 x 11328 bfloat16 68 us (63), 8192 x 8449 binary32 97 (91).
 // Bound by memory: 8192 x 8449 binary32 with entropies 92.8 us, 554 MB at 6.0
 // TB/s; 4096 x 50304 bfloat16 133 us, 824 MB at 6.2.
+// Rows that count for nothing are read too: with their targets looked at first,
+// by lanes or as scalars, a wave lives longer than its bytes are worth, 4096 x
+// 50304 131 us and 152 where all rows count, 128 and 120 where half do.
 template <int DT, bool ENTROPY, bool STREAMED>
 __global__ __launch_bounds__(kLogpThreads) void k_logp_grad(LogpArgs a, Split split) {
   constexpr uint32_t kU = kUnit<DT>;

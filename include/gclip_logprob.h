@@ -25,10 +25,12 @@
  *     and so is the gradient.
  *     A row with a NaN or +infinity has NaN for its s, logp, entropy and
  *     gradient; its top counts a NaN above everything.
- *   - A row whose target is `ignore` counts for nothing: it is not read, its
+ *   - A row whose target is `ignore` counts for nothing, whatever it holds: its
  *     logp, entropy and gradient are 0 (its stats too), its top has columns -1
- *     with log probabilities of -infinity.  Any other target that is no
- *     column gives NaN for logp, and a gradient of NaN.
+ *     with log probabilities of -infinity.  The forward call does not read such
+ *     rows of more than 1024 logits; shorter ones, and all of them in the
+ *     backward call, are read to no effect.  Any other target that is no column
+ *     gives NaN for logp, and a gradient of NaN.
  *   - Sums are binary32, of at most 32 terms in a lane and then of those,
  *     relative to the largest logit so far; a row's results are taken from
  *     them in binary64 and rounded once, those of rows of up to 2048 logits in

@@ -41,3 +41,33 @@ def test_crowded_rows(rows, size, dtype):
             lu.within(lu.values(r.top_logp[:few]), tops, tol[:, None] + 2 * lu.U * np.abs(tops), f"top {top}")
         assert np.array_equal(r.top_ids[:few].cpu().numpy(), ids[:, :top]), top
         assert bits(r.top_ids) == bits(r.top_ids[row]) and bits(r.top_logp) == bits(r.top_logp[row])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows,size", [(6, 1), (7, 40), (9, 300), (600, 382), (8200, 100), (8200, 600), (40, 1000),
+                                       (8200, 1025), (9, 2048), (600, 3000), (1600, 2500), (6, 70000), (300, 20000)])
+def test_rows_that_count_for_nothing_may_hold_anything(rows, size, dtype):
+    """NaNs and infinities of ignored rows, in the logits and in what the
+    backward pass is given of them, have no effect."""
+    import torch
+    g, rng = G(), np.random.default_rng([rows, size])
+    x = lu.matrix(rng.standard_normal((rows, size)), dtype)
+    t = torch.from_numpy(rng.integers(0, size, rows)).cuda()
+    none = torch.arange(rows, device="cuda") % 3 == 1
+    t[none] = -100
+    dl, dh = (torch.from_numpy(rng.standard_normal(rows)).float().cuda() for _ in range(2))
+    spoilt = x.clone()
+    spoilt[none] = float("nan")
+    spoilt[none.nonzero()[0]] = float("inf")
+    for top in (min(5, size), 0):
+        clean = g.token_log_probs_forward(x, t, entropy=True, top=top)
+        r = g.token_log_probs_forward(spoilt, t, entropy=True, top=top)
+        assert bits(r.logp, r.entropy, r.stats) == bits(clean.logp, clean.entropy, clean.stats)
+        assert not r.logp[none].any() and not r.entropy[none].any() and not r.stats[none].any()
+        if top:
+            assert (r.top_ids[none] == -1).all() and torch.isneginf(r.top_logp[none]).all()
+    bad = lambda v: torch.where(none.reshape(-1, *[1] * (v.dim() - 1)), float("nan"), v)  # noqa: E731
+    for de in (None, dh):
+        want = g.token_log_probs_backward(dl, de, x, t, clean.stats, clean.entropy)
+        d = g.token_log_probs_backward(bad(dl), None if de is None else bad(de), spoilt, t, bad(clean.stats), bad(clean.entropy))
+        assert bits(d) == bits(want) and not d[none].any()
