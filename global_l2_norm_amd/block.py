@@ -134,7 +134,8 @@ class Packed8:
             held = _empty(*lead, ld, dtype=_E4M3, device=x.device)
         scales = _empty(*lead, 1 if mode else (size + 127) // GCLIP_SCALE_BLOCK, dtype=_F32, device=x.device)
         self.held, self.size, self.scales = held, size, scales
-        self.fields = held.data_ptr(), ld, scales.data_ptr(), mode, 0
+        # a row of one block has one scale either way, which is a block's to a reader
+        self.fields = held.data_ptr(), ld, scales.data_ptr(), mode if size > GCLIP_SCALE_BLOCK else GCLIP_SCALES_BLOCK, 0
         return self
 
     @property
@@ -200,6 +201,15 @@ def _packed(p, x, name):
     fields = p.fields
     if p.held.data_ptr() != fields[0] or p.scales.data_ptr() != fields[2]:
         raise ValueError(f"{name} has another storage than when it was made")
+    return fields
+
+
+def _blocks(p, x, name):
+    """The same with a scale for each block, as the activation's gradient takes
+    them."""
+    fields = _packed(p, x, name)
+    if fields[3] != GCLIP_SCALES_BLOCK:
+        raise ValueError(f"{name} must have a scale for each {GCLIP_SCALE_BLOCK} columns (\"block\"), not one a row")
     return fields
 
 
@@ -290,8 +300,10 @@ def _forward(x, residual, weight, eps, mask, h, y, packed, keep, stats):
     if packed is not None:
         if y is not None:
             raise ValueError("out is for a y that is not packed")
-        y = Packed8._new(x, size, _mode(packed))
-        y8 = y.fields
+        mode = _mode(packed)
+        y = Packed8._new(x, size, mode)
+        # the scale of a row comes with its sum, and rounds otherwise than a block's
+        y8 = y.fields if size > GCLIP_SCALE_BLOCK else (*y.fields[:3], mode, 0)
     elif y is None:
         y = _empty_like(x, memory_format=_contiguous)
         yp, ldy = y.data_ptr(), size
@@ -475,9 +487,9 @@ def _activation_backward(dy, gate, up, kind, recompute, y, dgate, dup):
     gp = up_at = ldg = ldu = 0
     g8 = u8 = _NONE8
     if eight:
-        g8 = _packed(gate, dy, "gate")
+        g8 = _blocks(gate, dy, "gate")
         if up is not None:
-            u8 = _packed(up, dy, "up")
+            u8 = _blocks(up, dy, "up")
     else:
         ldg = _like(gate, dy, "gate")
         gp = gate.data_ptr()
