@@ -172,7 +172,9 @@ if torch is not None:
 
 def token_log_probs(logits, targets, *, entropy=False, top=0, ignore_index=-100):
     """A ``TokenLogProbs`` whose logp and entropy have gradients; the others
-    have none."""
+    have none.  Without targets there are none: ``token_log_probs_forward``."""
+    if targets is None:
+        raise TypeError("token_log_probs needs targets; token_log_probs_forward does without")
     targets = targets.contiguous()
     if not _tracked(logits):
         return token_log_probs_forward(logits, targets, entropy=entropy, top=top, ignore_index=ignore_index)

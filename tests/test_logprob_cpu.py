@@ -36,3 +36,13 @@ def test_crowded_rows_pass_the_room_from_other_waves(rows, size, dtype):
     # the last two: as much as there is room for, but for one and with one more
     got = [lp.candidates(row[:columns], 20, dtype, turns, threads) for row in x[2:]]
     assert all(g[0] for g in got) and [g[1] + g[3] for g in got] == [lp.CANDIDATES, lp.CANDIDATES + 1]
+
+
+def test_no_targets_are_refused_by_name():
+    import torch
+
+    import global_l2_norm_amd as G
+    x = torch.ones(4, 16)
+    for arg in (x, x.clone().requires_grad_()):
+        with pytest.raises(TypeError, match="needs targets"):
+            G.token_log_probs(arg, None, entropy=True)
