@@ -147,7 +147,7 @@ def _backward(dlogp, dentropy, logits, targets, stats, entropy, ignore, out):
 if torch is not None:
     from torch.autograd.function import once_differentiable
 
-    from .layers import _tracked
+    from .layers import _tracked, _without_tangent
 
     class _TokenLogProbs(torch.autograd.Function):
         @staticmethod
@@ -164,6 +164,7 @@ if torch is not None:
         def backward(ctx, dlogp, dentropy, *_):
             if dlogp is None and dentropy is None:
                 return (None,) * 5
+            _without_tangent(dlogp, dentropy)
             logits, targets, stats, entropy = ctx.saved_tensors
             dlogp = torch.zeros_like(stats[..., 0]) if dlogp is None else dlogp.contiguous()
             dentropy = dentropy.contiguous() if dentropy is not None else None

@@ -71,3 +71,18 @@ def test_rows_that_count_for_nothing_may_hold_anything(rows, size, dtype):
         want = g.token_log_probs_backward(dl, de, x, t, clean.stats, clean.entropy)
         d = g.token_log_probs_backward(bad(dl), None if de is None else bad(de), spoilt, t, bad(clean.stats), bad(clean.entropy))
         assert bits(d) == bits(want) and not d[none].any()
+
+
+def test_forward_over_reverse_is_refused():
+    import torch
+    import torch.autograd.forward_ad as forward_ad
+    g = G()
+    x = torch.randn(3, 50, device="cuda").requires_grad_()
+    t, one = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.ones(3, device="cuda")
+    r = g.token_log_probs(x, t, entropy=True)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(one, one)
+        for out in (r.logp, r.entropy):
+            with pytest.raises(NotImplementedError):
+                torch.autograd.grad(out, x, dual, retain_graph=True)
+        assert torch.autograd.grad(r.logp, x, one)[0].shape == x.shape

@@ -46,3 +46,23 @@ def test_no_targets_are_refused_by_name():
     for arg in (x, x.clone().requires_grad_()):
         with pytest.raises(TypeError, match="needs targets"):
             G.token_log_probs(arg, None, entropy=True)
+
+
+def test_tangents_of_the_results_gradients_are_refused():
+    """As the other operators do: without a check the logits' gradient would
+    come back without a tangent, as if it were constant."""
+    import types
+
+    import torch
+    import torch.autograd.forward_ad as forward_ad
+
+    from global_l2_norm_amd import logprob
+    x, one, stats = torch.ones(4, 16), torch.ones(4), torch.ones(4, 2)
+    ctx = types.SimpleNamespace(saved_tensors=(x, torch.zeros(4, dtype=torch.int64), stats, one), ignore=-100)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(one, one)
+        for grads in ((dual, None), (None, dual), (one, dual), (dual, one)):
+            with pytest.raises(NotImplementedError):
+                logprob._TokenLogProbs.backward(ctx, *grads, None, None, None)
+        with pytest.raises(ValueError, match="device"):  # no tangent: only that no GPU sees it
+            logprob._TokenLogProbs.backward(ctx, one, one, None, None, None)
