@@ -120,7 +120,8 @@ def _ld(t, name):
         return shape[-1]
     lead = [(n, s) for n, s in zip(shape[:-1], stride[:-1]) if n != 1]
     if (shape[-1] != 1 and stride[-1] != 1) or any(a[1] != b[0] * b[1] for a, b in zip(lead, lead[1:])):
-        raise ValueError(f"{name}: the last dimension must be adjacent in memory and the others at one distance")
+        raise ValueError(f"{name}: the last dimension must be adjacent in memory and the others at one distance; "
+                         f"a contiguous() copy is")
     return lead[-1][1] if lead else shape[-1]
 
 

@@ -66,3 +66,15 @@ def test_tangents_of_the_results_gradients_are_refused():
                 logprob._TokenLogProbs.backward(ctx, *grads, None, None, None)
         with pytest.raises(ValueError, match="device"):  # no tangent: only that no GPU sees it
             logprob._TokenLogProbs.backward(ctx, one, one, None, None, None)
+
+
+def test_rows_at_two_distances_are_refused_with_what_to_do():
+    """Logits shifted by one position, of more than one sequence."""
+    import torch
+
+    from global_l2_norm_amd import layers
+    logits = torch.ones(2, 5, 7)
+    with pytest.raises(ValueError, match=r"logits: .* a contiguous\(\) copy is"):
+        layers._ld(logits[:, :-1], "logits")
+    assert layers._ld(logits[:, :-1].contiguous(), "logits") == 7
+    assert layers._ld(logits[:1, :-1], "logits") == 7
