@@ -24,3 +24,24 @@ def test_one_scale_of_a_longer_row_is_refused_by_name():
     with pytest.raises(ValueError, match="gate must have a scale for each 128 columns"):
         block._blocks(block.Packed8._new(x, 129, _lib.GCLIP_SCALES_ROW), x, "gate")
     block._blocks(block.Packed8._new(x, 129, _lib.GCLIP_SCALES_BLOCK), x, "gate")
+
+
+def test_the_activations_polynomial_is_as_good_as_its_comment_says():
+    """P(t) / (e^(z^2) erfc(z) / (2 t)) with t = 1 / (1 + 0.3 z), for the
+    coefficients as the source has them, rounded to binary32."""
+    import os
+    import re
+
+    import numpy as np
+    from scipy.special import erfcx
+
+    import global_l2_norm_amd as G
+    with open(os.path.join(os.path.dirname(G.__file__), "csrc", "gclip_activation.hpp"), encoding="utf-8") as f:
+        part = re.search(r"KIND == GCLIP_ACT_GELU\) \{(.*?)h = e \* t \* h;", f.read(), re.S)[1]
+    said = float(re.search(r"for z up to 10, (\S+) off", part)[1])
+    c = [float(np.float32(v)) for v in re.findall(r"(?:float h = |, t, )(-?[0-9.]+)f", part)]
+    assert len(c) == 9
+    z = np.linspace(0.0, 10.0, 200001)
+    t = 1.0 / (1.0 + 0.3 * z)
+    off = np.abs(np.polyval(c, t) * 2.0 * t / erfcx(z) - 1.0).max()
+    assert said / 2 < off <= said <= 2.0 ** -24
