@@ -137,7 +137,8 @@ __global__ __launch_bounds__(kLongThreads) void k_rms_long(RmsFwdArgs a, DropArg
 // registers and more.  The first leaves a row's mean; the second takes strips
 // of columns down many rows, whose sums stay in registers, and reads the
 // matrices again, mostly from the cache before memory.  Workgroups of the
-// second: kLongStrips, two for each compute unit.  1000 x 40000 residual
+// second: kLongStrips in a 16-bit format, two for each compute unit, and twice
+// as many in binary32, whose strips are half as wide.  1000 x 40000 residual
 // gradients in bfloat16 41.9 and 48.4 us, and 4.8 for the join: 400 MB at 4.2
 // TB/s, of which 320 would do.
 constexpr uint32_t kLongStrips = 512;
@@ -450,7 +451,8 @@ hipError_t backward(const RmsBwdArgs& a, bool residual, const DropArgs* drop, hi
 
 // Rows in registers: a part for each workgroup.  Shorter rows: as many as
 // leave each lane four rows.  Longer ones: as many as make kLongStrips
-// workgroups of strips of 512 columns, and leave each wave two rows.
+// workgroups of strips of 512 columns, those of a 16-bit format, and leave each
+// wave two rows: the workspace serves any format.
 uint32_t rms_parts(int64_t rows, int64_t size) {
   if (rows == 0) return 0;
   const uint32_t n = (uint32_t)rows, c = (uint32_t)size;

@@ -33,8 +33,10 @@
  * Conventions: those of gclip_layer.h (matrices, in place, overlaps, arithmetic
  * in binary32 with one rounding to the storage format, bit-identical results
  * from run to run, capture, rows of 0).  Besides:
- *   - rows of 8 to 16384 columns have binary32 sums, taken again of the row
- *     scaled by 2^-96 where they overflow; others binary64 sums.
+ *   - The squares of a row of 8 to 16384 columns are summed in binary32, and
+ *     again of the row scaled by 2^-96 where that overflows; those of others in
+ *     binary64.  The gradients' sums are binary32, but for a row's of more than
+ *     16384 columns: binary64, of binary32 sums of eight.
  *   - What an 8-bit matrix is given for is computed from the stored 8-bit
  *     values: the norm's gradient takes n = (value * scale) * rstd with the
  *     rstd of the forward pass.
