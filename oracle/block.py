@@ -4,6 +4,8 @@ import math
 
 import numpy as np
 
+from .pieces import by_rows, in_pieces, joined
+
 BLOCK = 128
 LEAST_SCALE = 2.0 ** -112
 
@@ -27,11 +29,13 @@ def e4m3_table():
 E4M3 = e4m3_table()
 
 
+@by_rows(0)
 def e4m3_half_step(v):
     """Half of the distance of the values around v."""
     a = np.maximum(np.abs(v), 2.0 ** -6)
-    with np.errstate(divide="ignore", invalid="ignore"):
-        return np.where(np.isfinite(a), 2.0 ** (np.floor(np.log2(np.where(np.isfinite(a), a, 1.0))) - 4), 0.0)
+    finite = np.isfinite(a)
+    # a = f 2^e with f in [1/2, 1)
+    return np.where(finite, np.ldexp(1.0, np.frexp(np.where(finite, a, 1.0))[1] - 5), 0.0)
 
 
 def round_e4m3(v):
@@ -46,6 +50,7 @@ def groups(v, mode):
     return [slice(0, size)] if mode == "row" else [slice(c, min(c + BLOCK, size)) for c in range(0, size, BLOCK)]
 
 
+@by_rows(0)
 def scales(v, mode):
     out = []
     for g in groups(v, mode):
@@ -60,6 +65,7 @@ def spread(s, size, mode):
 
 
 # ---------------------------------------------------------------- RMS norm
+@by_rows(0)
 def rms(x, eps):
     """rstd"""
     return 1.0 / np.sqrt((x.astype(np.float64) ** 2).sum(1) / x.shape[1] + eps)
@@ -67,9 +73,12 @@ def rms(x, eps):
 
 def rms_gradient(dy, x, rstd, weight):
     """(dx, dweight)"""
-    n = x * rstd[:, None]
-    g = dy * weight
-    return rstd[:, None] * (g - n * ((g * n).sum(1, keepdims=True) / x.shape[1])), (dy * n).sum(0)
+    def piece(i, j):
+        n = x[i:j] * rstd[i:j, None]
+        g = dy[i:j] * weight
+        return rstd[i:j, None] * (g - n * ((g * n).sum(1, keepdims=True) / x.shape[1])), (dy[i:j] * n).sum(0)[None]
+    dx, dw = joined(in_pieces(piece, *x.shape))
+    return dx, dw.sum(0)
 
 
 # ---------------------------------------------------------------- the activation
@@ -83,6 +92,7 @@ def _logistic(x):
     return expit(x)
 
 
+@by_rows(1)
 def act(kind, x):
     """(act(x), its derivative)"""
     if kind == "relu":
@@ -100,6 +110,7 @@ def act(kind, x):
 
 
 # ---------------------------------------------------------------- log probabilities
+@by_rows(0)
 def log_probs(x):
     """(m, s, log p, p, entropy); rows of nothing but -infinity: m, s and log p
     of -infinity, and an entropy of 0."""
@@ -115,14 +126,21 @@ def log_probs(x):
     return m, s, z, p, h
 
 
+@by_rows(0)
 def top(x, k):
     """Columns of the k largest, NaNs above everything, of equal ones the
     lowest first."""
-    order = np.where(np.isnan(x), np.inf, x)
-    rank = np.lexsort((np.broadcast_to(np.arange(x.shape[1]), x.shape), -order, ~np.isnan(x)), axis=1)
-    return rank[:, :k]
+    out = np.empty((len(x), k), dtype=np.int64)
+    for row, r in zip(x, out):
+        # numpy's order has NaNs behind everything: the k-th from there
+        least = np.partition(row, len(row) - k)[len(row) - k] if k else np.nan
+        columns = np.flatnonzero(np.isnan(row) if np.isnan(least) else np.isnan(row) | (row >= least))
+        v = row[columns]
+        r[:] = columns[np.lexsort((columns, -np.where(np.isnan(v), np.inf, v), ~np.isnan(v)))[:k]]
+    return out
 
 
+@by_rows(0, 1, 2, 3, 4, 5, 6)
 def log_probs_gradient(x, target, dlogp, dentropy, m, s, entropy, ignore=-100):
     """dlogits from the given m, s and entropy."""
     x = x.astype(np.float64)

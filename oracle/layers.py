@@ -2,6 +2,8 @@
 definitions: numpy arrays [rows, size] in, binary64 out."""
 import numpy as np
 
+from .pieces import by_rows, in_pieces, joined
+
 LOW = np.uint64(0xFFFFFFFF)
 
 
@@ -31,16 +33,20 @@ def dropout_scale(p):
 def kept(rows, size, p, seed, step=0, site=0):
     """Truth values [rows, size]."""
     groups = -(-size // 8)
-    r, g = np.meshgrid(np.arange(rows), np.arange(groups), indexing="ij")
-    w = philox_words([g, r, np.full_like(g, site), np.full_like(g, step % (1 << 32))],
-                     [seed & 0xFFFFFFFF, seed >> 32])
-    u = np.empty((rows, groups, 8), dtype=np.uint32)
-    for i in range(4):
-        u[:, :, 2 * i] = w[i] & 0xFFFF
-        u[:, :, 2 * i + 1] = w[i] >> 16
-    return u.reshape(rows, groups * 8)[:, :size] >= dropout_threshold(p)
+
+    def piece(first, last):
+        r, g = np.meshgrid(np.arange(first, last), np.arange(groups), indexing="ij")
+        w = philox_words([g, r, np.full_like(g, site), np.full_like(g, step % (1 << 32))],
+                         [seed & 0xFFFFFFFF, seed >> 32])
+        u = np.empty((last - first, groups, 8), dtype=np.uint32)
+        for i in range(4):
+            u[:, :, 2 * i] = w[i] & 0xFFFF
+            u[:, :, 2 * i + 1] = w[i] >> 16
+        return u.reshape(last - first, groups * 8)[:, :size] >= dropout_threshold(p)
+    return joined(in_pieces(piece, rows, size))
 
 
+@by_rows(0)
 def statistics(x, eps):
     x = x.astype(np.float64)
     mean = x.sum(1) / x.shape[1]
@@ -56,8 +62,12 @@ def norm(x, weight, bias, eps):
 
 def norm_gradient(dy, x, mean, rstd, weight):
     """(dx, dweight, dbias)"""
-    n = (x - mean[:, None]) * rstd[:, None]
-    g = dy * weight
     size = x.shape[1]
-    dx = rstd[:, None] * (g - g.sum(1, keepdims=True) / size - n * ((g * n).sum(1, keepdims=True) / size))
-    return dx, (dy * n).sum(0), dy.sum(0)
+
+    def piece(i, j):
+        n = (x[i:j] - mean[i:j, None]) * rstd[i:j, None]
+        g = dy[i:j] * weight
+        dx = rstd[i:j, None] * (g - g.sum(1, keepdims=True) / size - n * ((g * n).sum(1, keepdims=True) / size))
+        return dx, (dy[i:j] * n).sum(0)[None], dy[i:j].sum(0)[None]
+    dx, dw, db = joined(in_pieces(piece, *x.shape))
+    return dx, dw.sum(0), db.sum(0)

@@ -25,6 +25,7 @@ F32, F16, BF16 = "f32", "f16", "bf16"
 DTYPES = (F32, F16, BF16)
 _CODE = {F32: 0, F16: 1, BF16: 2}
 _NP = {F32: np.float32, F16: np.uint16, BF16: np.uint16}
+APART = 1 << 22  # elements from which scale_ and accumulate_ are worth threads
 
 class Oracle:
     """Handle on one build of the C oracle (the default build, or another
@@ -342,8 +343,21 @@ def decide(norm, nonfinite, max_norm, avg_factor=1.0, error_if_nonfinite=False):
     return default().decide(norm, nonfinite, max_norm, avg_factor, error_if_nonfinite)
 
 
+def _in_runs(f, *lists):
+    """f of lists of the same shapes.  It works element by element: long lists
+    go as runs of consecutive elements (shards), a host thread each."""
+    total = sum(a.size for a in lists[0])
+    if total < APART or any(not a.flags.c_contiguous for arrays in lists for a in arrays):
+        return f(*lists)
+    from concurrent.futures import ThreadPoolExecutor
+    threads = min(8, os.cpu_count() or 1)
+    runs = [shards([a.reshape(-1) for a in arrays], threads) for arrays in lists]
+    with ThreadPoolExecutor(threads) as pool:
+        list(pool.map(f, *runs))
+
+
 def scale_(arrays, dtype, s):
-    return default().scale_(arrays, dtype, s)
+    _in_runs(lambda run: default().scale_(run, dtype, s), arrays)
 
 
 def clip_(arrays, dtype, max_norm, avg_factor=1.0, error_if_nonfinite=False):
@@ -355,7 +369,9 @@ def adamw(p, grad, m, v, dtype, s, lr, beta1, beta2, eps, weight_decay, step):
 
 
 def accumulate_(acc, contrib, dtype):
-    return default().accumulate_(acc, contrib, dtype)
+    if [a.shape for a in acc] != [g.shape for g in contrib]:
+        return default().accumulate_(acc, contrib, dtype)  # which refuses them
+    _in_runs(lambda run, more: default().accumulate_(run, more, dtype), acc, contrib)
 
 
 def accumulate_clip_(acc, contrib, dtype, max_norm, avg_factor=1.0, error_if_nonfinite=False):
