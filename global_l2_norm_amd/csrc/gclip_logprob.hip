@@ -28,8 +28,10 @@ struct Softmax {
   float m, s, t;
 };
 __device__ __forceinline__ float reference(float m) { return fmaxf(m, kLowest); }
-// The difference of two references; finite, so that nothing times it is nothing.
-__device__ __forceinline__ float drop_to(float from, float to) { return fmaxf(reference(from) - reference(to), -1e30f); }
+// The difference of two references; finite, and so times any sum of 2^31
+// exponentials, so that nothing times either is nothing.
+constexpr float kFar = -1e28f;
+__device__ __forceinline__ float drop_to(float from, float to) { return fmaxf(reference(from) - reference(to), kFar); }
 
 template <bool ENTROPY>
 __device__ __forceinline__ void rebase(Softmax& z, float m) {
@@ -51,7 +53,7 @@ __device__ __forceinline__ void take(Softmax& z, const float (&v)[N]) {
   for (int j = 0; j < N; ++j) {
     const float d = v[j] - r, e = __builtin_amdgcn_exp2f(d * kLog2e);
     s += e;
-    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, -1e30f), t);
+    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, kFar), t);
   }
   z.s += s;
   if (ENTROPY) z.t += t;
@@ -477,7 +479,7 @@ __global__ __launch_bounds__(kLogpThreads) void k_logp_rows(LogpArgs a) {
   for (uint32_t j = 0; j < NV * kU; ++j) {
     const float d = v[j] - ref, e = __builtin_amdgcn_exp2f(d * kLog2e);
     s += e;
-    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, -1e30f), t);
+    if (ENTROPY) t = __builtin_fmaf(e, fmaxf(d, kFar), t);
   }
   s = lanes_sum<LANES>(s);
   if (ENTROPY) t = lanes_sum<LANES>(t);

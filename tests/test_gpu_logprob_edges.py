@@ -86,3 +86,24 @@ def test_forward_over_reverse_is_refused():
             with pytest.raises(NotImplementedError):
                 torch.autograd.grad(out, x, dual, retain_graph=True)
         assert torch.autograd.grad(r.logp, x, one)[0].shape == x.shape
+
+
+def test_the_largest_rows_of_equal_logits_far_below_another():
+    """Rows of the largest extent, one workgroup each: a wave's sum of equal
+    logits, half a billion of them, is dropped where another wave has a far
+    larger one.  All rows are the same memory."""
+    import torch
+    rows, size = 257, 0x7ffffff0
+    assert lp.cut(rows, size, "bf16")[::2] == (1, 256)
+    x = torch.full((1, size), -2e30, dtype=torch.bfloat16, device="cuda")
+    x[0, -1] = 0.0
+    t = torch.full((rows,), size - 1, device="cuda")
+    r = G().token_log_probs_forward(x.expand(rows, size), t, entropy=True)
+    for got in (r.logp, r.entropy, r.stats):
+        assert not got.any(), got.flatten()[:4]
+    x[0, -1] = -2e30
+    r = G().token_log_probs_forward(x.expand(rows, size), t, entropy=True)
+    # a lane adds 2^31 / 256 ones, 32 at a time
+    want, tol = np.log(size), (size // (256 * 32) + 100) * lu.U
+    for got in (-lu.values(r.logp), lu.values(r.entropy), lu.values(r.stats[:, 1])):
+        assert np.abs(got - want).max() <= tol
