@@ -637,7 +637,12 @@ def residual_rms_norm(x, residual, weight=None, eps=1e-6, mask=None, *, checkpoi
 
 def activation(gate, up=None, kind="silu", *, checkpoint=False):
     """act(gate) * up, or act(gate) without up.  With ``checkpoint`` the
-    backward pass keeps gate and up in 8 bits alone, and starts from that."""
+    backward pass keeps gate and up in 8 bits alone, and starts from that.
+
+    The gradients of gate and up are two tensors.  Where both are halves of one
+    product's output, torch then puts them together, which takes longer than
+    the kernels; a backward pass of one's own writes both halves at once
+    (``activation_backward``'s out_gate and out_up)."""
     if not _tracked(gate, up):
         return activation_forward(gate, up, kind)[0]
     return _Activation.apply(gate, up, kind, checkpoint)

@@ -239,7 +239,8 @@ __device__ __forceinline__ void logits_settled(u32x4 q, uint32_t u, uint32_t siz
 // Long rows of 16-bit logits are bound by the exponentials: 4096 x 50304 with
 // entropies 69.6 us, 412 MB at 5.9 TB/s with the vector units full; 8192 x 8449
 // in binary32 by memory, 49.4 us, 277 MB at 5.6 TB/s.  Few rows by latency: 8 x
-// 131072 in segments 8.0 us with 20 alternatives and 5.8 for the join.
+// 131072 in segments 8.0 us with 20 alternatives and 5.8 for the join; their
+// lanes have one unit each and read kChunk, 7 MB of the 2 that it takes.
 template <int DT, int THREADS, bool ENTROPY, bool TOP, bool STREAMED>
 __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
   constexpr uint32_t kU = kUnit<DT>;
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(THREADS) void k_logp(LogpArgs a) {
 // that reach the k-th largest of the lanes' largest, found and ordered within
 // the wave; rows with NaNs or infinities, and those whose candidates do not
 // fit, are searched k times.  Bound by the vector units: 59629 x 382 in
-// bfloat16 14.4 us, 45 MB; 28860 x 186 with 20 alternatives 23.8 us, which
+// bfloat16 14.4 us, 45 MB; 28860 x 186 with 20 alternatives 23.5 us, which
 // were 137 by k_logp's way.
 constexpr uint32_t kRowCandidates = 128;
 __device__ __forceinline__ void wave_sync() {
